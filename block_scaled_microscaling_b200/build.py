@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libmxq.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
          "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-         "-cudart", "static", "-I", os.path.join(ROOT, "include")]
+         "-cudart", "static", "--threads", "0", "-I", os.path.join(ROOT, "include")]
 
 
 def sources():
@@ -32,7 +32,7 @@ def _stale():
         return True
     t = os.path.getmtime(LIB)
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        [os.path.join(ROOT, "include", "mxq.h")]
+        glob.glob(os.path.join(ROOT, "include", "*.h"))
     return any(os.path.getmtime(d) > t for d in deps)
 
 

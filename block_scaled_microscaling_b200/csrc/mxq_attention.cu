@@ -1,0 +1,703 @@
+// mxq_attention.cu -- attention over the paged MXFP4 key/value cache (sm_100a).
+//
+// For the queries of one sequence that share a key/value head (rows = query x head of the group),
+//   s[j, r] = scale * log2(e) * sum_d K[j, d] Q[r, d],   o[r, d] = sum_j 2^(s[j, r] - m_r) V[j, d] / sum_j 2^(s[j, r] - m_r)
+// over the keys j that row r sees. 17 bytes hold 32 cached values, so at the copy bandwidth 12 values arrive per
+// picosecond and the SMs have about three lane instructions for each: what bounds the kernel is turning codes into
+// operands. Hence:
+// - codes go from global memory to registers in the layout of mma.sync's fragments, without shared memory or
+//   shuffles. The summed index may be permuted freely, so the lane that holds key g's part of an operand owns a
+//   contiguous quarter of the key (16 bytes of codes and one scale at head_dim 128), and four lanes share it; for
+//   V, whose operand pairs two keys, a lane takes the same 8 bytes of four neighbouring keys and interleaves the
+//   nibbles of two keys with shifts and masks before the conversion.
+// - cvt.rn.f16x2.e2m1x2 converts two codes; one f16x2 product applies the block scale. Both products run in f16
+//   with fp32 sums (m16n8k16): keys (then head dimensions) fill the instruction's 16 rows and the queries its 8
+//   columns, so one query of up to 8 heads per key head (a decoding step) wastes nothing.
+// - f16 holds a code times 2^x exactly for -23 <= x <= 13, so block scales are taken relative to a reference per
+//   warp (K and V each), 2^6 below the largest block when it was set and raised by a vote when a block exceeds 2^13
+//   of it; codes of blocks more than 2^29 below the largest seen lose bits. Rows of Q are divided by a power of
+//   two for the same reason. Scores return to their true size in fp32.
+// - the running maximum m_r is raised only when a score exceeds it by 2^8 (one vote per 16 keys); the weights
+//   then are at most 2^8 and round to f16 (relative error 2^-12; below 2^-14 absolute, 2^-25).
+// Each warp takes every fourth group of 16 keys (a group lies within a page; page numbers are fetched 32 groups
+// at a time), with the next group's loads in flight; the four warps' results are joined through shared memory, and
+// a long sequence is split over several CTAs whose partial sums a second kernel joins in order.
+#include <atomic>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "mxq_device.cuh"
+#include "mxq_internal.h"
+
+namespace mxq {
+namespace {
+
+constexpr int kAtWarps = 4, kAtThreads = 32 * kAtWarps;
+constexpr int kAtMinGroups = 8;    // groups of 16 keys that a split has at least
+constexpr int kAtMaxSplits = 256;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct AtArgs {
+    KvCache c;
+    const __nv_bfloat16* q;
+    long long q_rows, q_row_stride, q_head_stride;
+    const int* starts;
+    const int* lens;
+    const int* table;
+    long long table_stride;
+    long long max_keys;
+    int batch, heads, group, max_q, window, splits, row_tiles;
+    float scale;   // already times log2(e)
+    __nv_bfloat16* out;
+    float* lse;
+    float* part;   // [(sequence, key head, row tile)][split][rows][D] sums, then their [..][rows][2] maximum and total
+    long long part_ml;  // offset of the latter
+};
+
+// what a CTA (and the joining kernel) works out about its sequence and rows
+struct Span {
+    int q0, n, nq;   // first row of q, queries of the sequence, of which computed
+    int len;         // keys
+};
+__device__ __forceinline__ Span span_of(const AtArgs& p, int b) {
+    Span s;
+    if (p.starts) {
+        const int rows = (int)p.q_rows;
+        s.q0 = min(max(__ldg(p.starts + b), 0), rows);
+        s.n = min(max(__ldg(p.starts + b + 1), s.q0), rows) - s.q0;
+    } else {
+        s.q0 = b * p.max_q;
+        s.n = p.max_q;
+    }
+    s.nq = min(s.n, p.max_q);
+    s.len = (int)min((long long)max(__ldg(p.lens + b), 0), p.max_keys);
+    return s;
+}
+// groups of 16 keys that the queries i0 .. i1 see together, and groups per split
+struct Groups {
+    int lo, hi, per;
+};
+__device__ __forceinline__ Groups groups_of(const AtArgs& p, const Span& s, int i0, int i1) {
+    const int hi = min(s.len, max(s.len - s.n + i1 + 1, 0));
+    const int lo = p.window > 0 ? min(max(s.len - s.n + i0 - p.window + 1, 0), hi) : 0;
+    Groups g;
+    g.lo = lo >> 4;
+    g.hi = (hi + 15) >> 4;
+    const int n = g.hi - g.lo;
+    g.per = max((n + p.splits - 1) / p.splits, kAtMinGroups);
+    return g;
+}
+
+__device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+// the four bytes of x, each two E2M1 codes, as f16 pairs (low nibble in the low half)
+__device__ __forceinline__ void e2m1_to_h2(uint32_t x, uint32_t* r) {
+    asm("{ .reg .b8 c0, c1, c2, c3;\n mov.b32 {c0, c1, c2, c3}, %4;\n"
+        "cvt.rn.f16x2.e2m1x2 %0, c0;\n cvt.rn.f16x2.e2m1x2 %1, c1;\n"
+        "cvt.rn.f16x2.e2m1x2 %2, c2;\n cvt.rn.f16x2.e2m1x2 %3, c3; }"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(x));
+}
+// 2^(byte - ref) as fp32 (0 far below 1; the conversion to f16 rounds small ones)
+__device__ __forceinline__ float rel_scale(int byte, int ref) { return __uint_as_float((uint32_t)max(byte - ref + 127, 0) << 23); }
+// 2^e for any integer e (clamped to the fp32 range, subnormals flushed)
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)min(max(e + 127, 0), 255) << 23); }
+
+// one group's bytes, in the lane's share
+template <int D> struct Loads {
+    uint32_t k[2][D / 32];  // keys 4 (g / 2) + g % 2 and + 2: codes of dimensions t D/4 ..
+    uint32_t v[4][D / 64];  // keys 4 t + i: codes of dimensions g D/8 ..
+    uint32_t ks[2];         // their scale bytes
+    uint32_t vs[4];
+};
+
+template <int D> __device__ __forceinline__ void fetch(const KvCache& c, int head, int page, int off, int g, int t, Loads<D>& L) {
+    if (page < 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) L.k[i][j] = 0;
+            L.ks[i] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) L.v[i][j] = 0;
+            L.vs[i] = 0;
+        }
+        return;
+    }
+    const long long row = ((long long)page * c.heads + head) * c.page + off;
+    const int ka = 4 * (g >> 1) + (g & 1);
+    const uint8_t* pk = reinterpret_cast<const uint8_t*>(c.kc) + (row + ka) * (D / 2) + t * (D / 8);
+    const uint8_t* pv = reinterpret_cast<const uint8_t*>(c.vc) + (row + 4 * t) * (D / 2) + g * (D / 16);
+    const uint8_t* sk = c.ks + (row + ka) * (D / 32) + (D == 128 ? t : t >> 1);
+    const uint8_t* sv = c.vs + (row + 4 * t) * (D / 32);
+    if constexpr (D == 128) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(pk + i * D));
+            L.k[i][0] = x.x;
+            L.k[i][1] = x.y;
+            L.k[i][2] = x.z;
+            L.k[i][3] = x.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(pv + i * (D / 2)));
+            L.v[i][0] = x.x;
+            L.v[i][1] = x.y;
+        }
+        const uint4 s = __ldg(reinterpret_cast<const uint4*>(sv));
+        const uint32_t w[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) L.vs[i] = (w[i] >> (8 * (g >> 1))) & 0xFFu;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(pk + i * D));
+            L.k[i][0] = x.x;
+            L.k[i][1] = x.y;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) L.v[i][0] = __ldg(reinterpret_cast<const uint32_t*>(pv + i * (D / 2)));
+        const uint2 s = __ldg(reinterpret_cast<const uint2*>(sv));
+        const uint32_t w[2] = {s.x, s.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) L.vs[i] = (w[i >> 1] >> (16 * (i & 1) + 8 * (g >> 2))) & 0xFFu;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) L.ks[i] = __ldg(sk + i * (D / 16));
+}
+
+// float offset of dimension d of row r in a warp's result: rows D + 4 floats apart, so that the lanes' 16-byte
+// writes (dimensions g D/8 .., rows 2t, 2t + 1) meet in a bank at most in pairs
+template <int D> __device__ __forceinline__ int res_off(int r, int d) { return r * (D + 4) + d; }
+
+// NQ: groups of eight rows that a warp handles together (their Q operands in shared memory when NQ is 4)
+template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ? 2 : 3) k_kv_attention(const AtArgs p) {
+    constexpr int ROWS = 8 * NQ, STEPS = D / 16, TILES = D / 16;
+    constexpr bool QS = NQ == 4;
+    extern __shared__ __align__(16) float dsm[];
+    __shared__ float sm_m[kAtWarps][ROWS], sm_l[kAtWarps][ROWS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    pdl_wait_then_release();
+    int id = blockIdx.x;
+    const int sp = id % p.splits;
+    id /= p.splits;
+    const int tile_id = id;
+    const int rt = id % p.row_tiles;
+    id /= p.row_tiles;
+    const int head = id % p.c.heads, b = id / p.c.heads;
+
+    const Span s = span_of(p, b);
+    const int rows = s.nq * p.group, r0 = rt * ROWS;
+    if (r0 >= rows) return;
+    const int i0 = r0 / p.group, i1 = (min(r0 + ROWS, rows) - 1) / p.group;
+    const Groups gr = groups_of(p, s, i0, i1);
+    const int first = gr.lo + sp * gr.per, last = min(first + gr.per, gr.hi);
+    const bool alone = gr.hi - gr.lo <= gr.per;  // one split holds all keys: it writes the output itself
+    if (first >= last && sp > 0) return;
+
+    // ---- the rows' queries: lane (g, t) holds row g of each eight, dimensions t D/4 .., divided by 2^e ----
+    uint32_t qf[QS ? 1 : NQ][STEPS][2];
+    uint2* const qsm = reinterpret_cast<uint2*>(dsm);
+    float mul[NQ][2];  // per column of the score tiles (rows 2t, 2t + 1): scale * log2(e) * 2^e
+    int pos[NQ][2];    // last key that the row sees (-1: no row)
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        const int r = r0 + 8 * n + g;
+        uint32_t w[D / 8];
+        if (r < rows) {
+            const int i = r / p.group, h = head * p.group + (r - i * p.group);
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + (s.q0 + i) * p.q_row_stride + h * p.q_head_stride + t * (D / 4));
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                const uint4 x = __ldg(src + j);
+                w[4 * j] = x.x;
+                w[4 * j + 1] = x.y;
+                w[4 * j + 2] = x.z;
+                w[4 * j + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) w[j] = 0;
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) top = max(top, max((w[j] & 0x7FFFu) << 16, w[j] & 0x7FFF0000u));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        const int e = min(max((int)(top >> 23), 1), 253) - 127;
+        const float down = pow2i(-e);
+#pragma unroll
+        for (int st = 0; st < STEPS; ++st) {
+            uint32_t f[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t x = w[2 * st + k];
+                f[k] = pack_h2(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xFFFF0000u) * down);
+            }
+            if constexpr (QS) {
+                if (warp == n) qsm[(n * STEPS + st) * 32 + lane] = make_uint2(f[0], f[1]);
+            } else {
+                qf[n][st][0] = f[0];
+                qf[n][st][1] = f[1];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int col = 2 * t + k, rr = r0 + 8 * n + col;
+            mul[n][k] = p.scale * pow2i(__shfl_sync(0xFFFFFFFFu, e, 4 * col));
+            pos[n][k] = rr < rows ? s.len - s.n + rr / p.group : -1;
+        }
+    }
+    if constexpr (QS) __syncthreads();
+
+    float o[NQ][TILES][4], m[NQ][2], l[NQ][2];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+        for (int u = 0; u < TILES; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[n][u][k] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            m[n][k] = -INFINITY;
+            l[n][k] = 0.f;
+        }
+    }
+    int kref = -1000, vref = -1000;  // block scales are taken relative to these bytes
+    float kmul = 1.f;                // 2^(kref - 127)
+    uint32_t vnan = 0;               // bit 2n + k: a value block that row sees is NaN
+
+    const int pos_lo = s.len - s.n + i0, pos_hi = s.len - s.n + i1;
+    int pages = -1, offs = 0;  // lane j: page and first row of the warp's group number base + j
+    auto page_of = [&](int grp) {
+        pages = -1;
+        offs = 0;
+        if (grp < last) {
+            const uint32_t key = 16u * (uint32_t)grp, at = key / (uint32_t)p.c.page;
+            offs = (int)(key - at * (uint32_t)p.c.page);
+            const int pg = __ldg(p.table + b * p.table_stride + at);
+            pages = pg >= 0 && pg < p.c.pages ? pg : -1;
+        }
+    };
+    Loads<D> next;
+    int grp = first + warp, it = 0;
+    page_of(grp + lane * kAtWarps);
+    int page = __shfl_sync(0xFFFFFFFFu, pages, 0);
+    if (grp < last) fetch<D>(p.c, head, page, __shfl_sync(0xFFFFFFFFu, offs, 0), g, t, next);
+    for (; grp < last; grp += kAtWarps) {
+        Loads<D> cur = next;
+        const bool in_page = page >= 0;
+        ++it;
+        if ((it & 31) == 0) page_of(grp + (1 + lane) * kAtWarps);
+        if (grp + kAtWarps < last) {
+            page = __shfl_sync(0xFFFFFFFFu, pages, it & 31);
+            fetch<D>(p.c, head, page, __shfl_sync(0xFFFFFFFFu, offs, it & 31), g, t, next);
+        }
+        const int key0 = 16 * grp;
+        const int ka = key0 + 4 * (g >> 1) + (g & 1);  // the lane's keys of the score tiles: ka, ka + 2
+        // every row sees every key of the group?
+        const bool whole = in_page && key0 + 15 < s.len && key0 + 15 <= pos_lo && (p.window <= 0 || key0 > pos_hi - p.window);
+        if (!whole) {  // bytes of keys that nobody sees count as zeros
+            const int end = in_page ? s.len : 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (ka + 2 * i >= end) cur.ks[i] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (key0 + 4 * t + i >= end) cur.vs[i] = 0;
+        }
+        // raise the references where a block (NaN blocks aside) exceeds 2^13 of them
+        {
+            int kt = -1, vt = -1;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) kt = max(kt, cur.ks[i] == 0xFFu ? -1 : (int)cur.ks[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vt = max(vt, cur.vs[i] == 0xFFu ? -1 : (int)cur.vs[i]);
+            const bool vbad = (cur.vs[0] == 0xFFu) | (cur.vs[1] == 0xFFu) | (cur.vs[2] == 0xFFu) | (cur.vs[3] == 0xFFu);
+            if (__any_sync(0xFFFFFFFFu, kt > kref + 13 || vt > vref + 13 || vbad)) {
+                kt = __reduce_max_sync(0xFFFFFFFFu, kt);
+                if (kt > kref + 13) {
+                    kref = kt - 6;
+                    kmul = pow2i(kref - 127);
+                }
+                vt = __reduce_max_sync(0xFFFFFFFFu, vt);
+                if (vt > vref + 13) {
+                    const float f = pow2i(vref - (vt - 6));  // 0 the first time: the sums are 0
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int u = 0; u < TILES; ++u)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) o[n][u][k] *= f;
+                    vref = vt - 6;
+                }
+                // a NaN block of V makes its 32 dimensions NaN for the rows that see its key, and for no others
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int tt = 0; tt < 4; ++tt) {
+                        const bool bad = __shfl_sync(0xFFFFFFFFu, cur.vs[i], (lane & ~3) | tt) == 0xFFu;
+                        const int key = key0 + 4 * tt + i;
+                        if (bad)
+#pragma unroll
+                            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k)
+                                    if (key <= pos[n][k] && (p.window <= 0 || key > pos[n][k] - p.window)) vnan |= 1u << (2 * n + k);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (cur.vs[i] == 0xFFu) cur.vs[i] = 0;
+            }
+        }
+        // ---- scores: keys x rows ----
+        float sc[NQ][4];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc[n][k] = 0.f;
+        {
+            uint32_t f[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float x = cur.ks[i] == 0xFFu ? __uint_as_float(0x7FC00000u) : rel_scale((int)cur.ks[i], kref);
+                f[i] = pack_h2(x, x);
+            }
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                uint32_t a[4], c[4];
+                e2m1_to_h2(cur.k[0][j], a);
+                e2m1_to_h2(cur.k[1][j], c);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    a[k] = mul_h2(a[k], f[0]);
+                    c[k] = mul_h2(c[k], f[1]);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        uint32_t b0, b1;
+                        if constexpr (QS) {
+                            const uint2 x = qsm[(n * STEPS + 2 * j + h) * 32 + lane];
+                            b0 = x.x;
+                            b1 = x.y;
+                        } else {
+                            b0 = qf[n][2 * j + h][0];
+                            b1 = qf[n][2 * j + h][1];
+                        }
+                        mma16816(sc[n], a[2 * h], c[2 * h], a[2 * h + 1], c[2 * h + 1], b0, b1);
+                    }
+            }
+        }
+        // ---- weights ----
+        bool up = false;
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                sc[n][k] *= mul[n][k & 1] * kmul;
+                if (!whole) {
+                    const int key = ka + (k & 2);
+                    const bool seen = in_page && key < s.len && key <= pos[n][k & 1] && (p.window <= 0 || key > pos[n][k & 1] - p.window);
+                    if (!seen) sc[n][k] = -INFINITY;
+                }
+            }
+            up |= fmaxf(sc[n][0], sc[n][2]) > m[n][0] + 8.f || fmaxf(sc[n][1], sc[n][3]) > m[n][1] + 8.f;
+        }
+        if (__any_sync(0xFFFFFFFFu, up)) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float x = fmaxf(sc[n][k], sc[n][k + 2]);
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
+                    x = fmaxf(m[n][k], x);
+                    const float f = m[n][k] == -INFINITY ? 0.f : ex2(m[n][k] - x);
+                    m[n][k] = x;
+                    l[n][k] *= f;
+#pragma unroll
+                    for (int u = 0; u < TILES; ++u) {
+                        o[n][u][k] *= f;
+                        o[n][u][k + 2] *= f;
+                    }
+                }
+            }
+        }
+        uint32_t pb[NQ][2];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            float w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                // a row without a key so far: every score is -inf (or NaN, which stays)
+                const float base = m[n][k & 1] == -INFINITY ? 0.f : m[n][k & 1];
+                w[k] = ex2(sc[n][k] - base);
+            }
+            l[n][0] += w[0] + w[2];
+            l[n][1] += w[1] + w[3];
+            pb[n][0] = transpose8x8(pack_h2(w[0], w[1]));
+            pb[n][1] = transpose8x8(pack_h2(w[2], w[3]));
+        }
+        // ---- sums: dimensions x rows ----
+        {
+            const uint32_t f0 = pack_h2(rel_scale((int)cur.vs[0], vref), rel_scale((int)cur.vs[1], vref));
+            const uint32_t f1 = pack_h2(rel_scale((int)cur.vs[2], vref), rel_scale((int)cur.vs[3], vref));
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                uint32_t e0[4], e1[4], d0[4], d1[4];  // even, odd dimensions of keys 4t, 4t + 1 and 4t + 2, 4t + 3
+                e2m1_to_h2((cur.v[0][j] & 0x0F0F0F0Fu) | ((cur.v[1][j] << 4) & 0xF0F0F0F0u), e0);
+                e2m1_to_h2((cur.v[2][j] & 0x0F0F0F0Fu) | ((cur.v[3][j] << 4) & 0xF0F0F0F0u), e1);
+                e2m1_to_h2(((cur.v[0][j] >> 4) & 0x0F0F0F0Fu) | (cur.v[1][j] & 0xF0F0F0F0u), d0);
+                e2m1_to_h2(((cur.v[2][j] >> 4) & 0x0F0F0F0Fu) | (cur.v[3][j] & 0xF0F0F0F0u), d1);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t a0 = mul_h2(e0[k], f0), a1 = mul_h2(d0[k], f0), a2 = mul_h2(e1[k], f1), a3 = mul_h2(d1[k], f1);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) mma16816(o[n][4 * j + k], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                }
+            }
+        }
+    }
+
+    // ---- join the warps ----
+    const float vtrue = vref > -1000 ? pow2i(vref - 127) : 0.f;
+    if constexpr (QS) __syncthreads();  // every warp is done with the queries: their memory takes the results
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) l[n][k] += __shfl_xor_sync(0xFFFFFFFFu, l[n][k], d);
+            if (g == 0) {
+                sm_m[warp][8 * n + 2 * t + k] = m[n][k];
+                sm_l[warp][8 * n + 2 * t + k] = l[n][k];
+            }
+        }
+    __syncthreads();
+    float* const mine = dsm + warp * ROWS * (D + 4);
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = 8 * n + 2 * t + k;
+            float top = sm_m[0][r];
+#pragma unroll
+            for (int w = 1; w < kAtWarps; ++w) top = fmaxf(top, sm_m[w][r]);
+            // a warp without a visible key has sums of 0 (or NaN, which stays)
+            float f = (m[n][k] == -INFINITY ? 1.f : ex2(m[n][k] - top)) * vtrue;
+            if (vnan & (1u << (2 * n + k))) f = __uint_as_float(0x7FC00000u);
+            // the lane's dimensions g D/8 ..: tile 4j + q holds 8j + 2q (first eight rows of the tile) and the next
+#pragma unroll
+            for (int j = 0; j < TILES; j += 2)
+                *reinterpret_cast<float4*>(mine + res_off<D>(r, g * (D / 8) + 2 * j)) =
+                    make_float4(o[n][j][k] * f, o[n][j][k + 2] * f, o[n][j + 1][k] * f, o[n][j + 1][k + 2] * f);
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < ROWS * (D / 4); i += kAtThreads) {
+        const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+        if (r0 + r >= rows) break;
+        float top = sm_m[0][r];
+#pragma unroll
+        for (int w = 1; w < kAtWarps; ++w) top = fmaxf(top, sm_m[w][r]);
+        float total = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kAtWarps; ++w) {
+            total += sm_l[w][r] * (sm_m[w][r] == -INFINITY ? 1.f : ex2(sm_m[w][r] - top));
+            const float4 x = *reinterpret_cast<const float4*>(dsm + w * ROWS * (D + 4) + res_off<D>(r, d));
+            a.x += x.x;
+            a.y += x.y;
+            a.z += x.z;
+            a.w += x.w;
+        }
+        if (alone) {
+            const float inv = total == 0.f ? 0.f : 1.f / total;
+            const int tok = (r0 + r) / p.group, h = head * p.group + (r0 + r - tok * p.group);
+            const long long at = (long long)(s.q0 + tok) * p.heads + h;
+            *reinterpret_cast<uint2*>(p.out + at * D + d) = make_uint2(bf16x2(a.x * inv, a.y * inv), bf16x2(a.z * inv, a.w * inv));
+            if (p.lse && d == 0) p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+        } else {
+            const long long at = ((long long)tile_id * p.splits + sp) * ROWS + r;
+            *reinterpret_cast<float4*>(p.part + at * D + d) = a;
+            if (d == 0) *reinterpret_cast<float2*>(p.part + p.part_ml + at * 2) = make_float2(top, total);
+        }
+    }
+}
+
+// join the splits of one row: CTA (sequence, query, head), one thread per dimension
+template <int D, int NQ> __global__ void __launch_bounds__(D) k_kv_attention_join(const AtArgs p) {
+    constexpr int ROWS = 8 * NQ;
+    const int d = threadIdx.x;
+    pdl_wait_then_release();
+    int id = blockIdx.x;
+    const int h = id % p.heads;
+    id /= p.heads;
+    const int i = id % p.max_q, b = id / p.max_q;
+    const Span s = span_of(p, b);
+    if (i >= s.nq) return;
+    const int head = h / p.group, row = i * p.group + h - head * p.group, rt = row / ROWS, r0 = rt * ROWS;
+    const Groups gr = groups_of(p, s, r0 / p.group, (min(r0 + ROWS, s.nq * p.group) - 1) / p.group);
+    const int n = (gr.hi - gr.lo + gr.per - 1) / gr.per;
+    if (n <= 1) return;  // written by its split
+    const long long first = (((long long)b * p.c.heads + head) * p.row_tiles + rt) * p.splits * ROWS + (row - r0);
+    const float* ml = p.part + p.part_ml + first * 2;
+    float top = -INFINITY;
+    for (int q = 0; q < n; ++q) top = fmaxf(top, __ldcg(ml + (long long)q * ROWS * 2));
+    float total = 0.f, sum = 0.f;
+    const float* part = p.part + first * D + d;
+#pragma unroll 8
+    for (int q = 0; q < n; ++q) {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(ml + (long long)q * ROWS * 2));
+        const float f = x.x == -INFINITY ? 1.f : ex2(x.x - top);
+        total += x.y * f;
+        sum += __ldcg(part + (long long)q * ROWS * D) * f;
+    }
+    const long long at = (long long)(s.q0 + i) * p.heads + h;
+    p.out[at * D + d] = __float2bfloat16_rn(total == 0.f ? 0.f : sum / total);
+    if (p.lse && d == 0) p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+}
+
+int nq_of(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+struct Plan {
+    int nq, row_tiles, splits;
+    long long tiles;
+};
+// rows of a key head in eights, and the keys in as many splits as give each SM about four CTAs, none below
+// kAtMinGroups groups of 16 keys
+Plan plan_of(const KvCache& c, long long batch, int max_q, int heads, long long max_keys, int sms) {
+    Plan p;
+    const long long rows = (long long)max_q * (heads / c.heads);
+    p.nq = nq_of(rows);
+    p.row_tiles = (int)((rows + 8 * p.nq - 1) / (8 * p.nq));
+    p.tiles = batch * c.heads * p.row_tiles;
+    const long long groups = (max_keys + 15) / 16;
+    long long want = (long long)sms * (p.nq == 4 ? 2 : 4) / (p.tiles > 0 ? p.tiles : 1);
+    if (want > groups / kAtMinGroups) want = groups / kAtMinGroups;
+    if (want > kAtMaxSplits) want = kAtMaxSplits;
+    p.splits = want < 1 ? 1 : (int)want;
+    return p;
+}
+
+template <int D, int NQ> cudaError_t go(const AtArgs& a, long long tiles, int dev, cudaStream_t st) {
+    constexpr int RES = kAtWarps * 8 * NQ * (D + 4) * 4, QB = NQ == 4 ? NQ * (D / 16) * 32 * 8 : 0;
+    constexpr int SMEM = RES > QB ? RES : QB;
+    auto* kern = k_kv_attention<D, NQ>;
+    if (SMEM > 47 * 1024) {
+        static std::atomic<unsigned long long> ready{0};
+        const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+        if (!(ready.load(std::memory_order_acquire) & bit)) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+            if (e != cudaSuccess) return e;
+            ready.fetch_or(bit, std::memory_order_release);
+        }
+    }
+    if (tiles * a.splits > 0x7FFFFFFFLL || (long long)a.batch * a.max_q * a.heads > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * a.splits));
+    cfg.blockDim = dim3(kAtThreads);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+    if (e != cudaSuccess || a.splits == 1) return e;
+    cfg.gridDim = dim3((unsigned)((long long)a.batch * a.max_q * a.heads));
+    cfg.blockDim = dim3(D);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, k_kv_attention_join<D, NQ>, a);
+}
+
+int sm_count(int dev) {
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        sms = 148;
+    }
+    return sms;
+}
+
+}  // namespace
+
+long long kv_attention_workspace(const KvCache& c, long long batch, int max_q, int heads, long long max_keys) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
+    const Plan p = plan_of(c, batch, max_q, heads, max_keys, sm_count(dev));
+    if (p.splits == 1) return 0;
+    return p.tiles * p.splits * 8 * p.nq * (c.db * 32 + 2) * 4;
+}
+
+cudaError_t launch_kv_attention(const KvAttention& x, cudaStream_t st) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const Plan pl = plan_of(x.c, x.batch, x.max_q, x.heads, x.max_keys, sm_count(dev));
+    AtArgs a{};
+    a.c = x.c;
+    a.q = static_cast<const __nv_bfloat16*>(x.q);
+    a.q_rows = x.q_rows;
+    a.q_row_stride = x.q_row_stride;
+    a.q_head_stride = x.q_head_stride;
+    a.starts = x.starts;
+    a.lens = x.lens;
+    a.table = x.table;
+    a.table_stride = x.table_stride;
+    a.max_keys = x.max_keys;
+    a.batch = (int)x.batch;
+    a.heads = x.heads;
+    a.group = x.heads / x.c.heads;
+    a.max_q = x.max_q;
+    a.window = x.window;
+    a.splits = pl.splits;
+    a.row_tiles = pl.row_tiles;
+    a.scale = x.scale * kLog2e;
+    a.out = static_cast<__nv_bfloat16*>(x.out);
+    a.lse = x.lse;
+    a.part = static_cast<float*>(x.workspace);
+    a.part_ml = pl.tiles * pl.splits * 8 * pl.nq * (x.c.db * 32);
+    if (x.c.db == 4) {
+        if (pl.nq == 1) return go<128, 1>(a, pl.tiles, dev, st);
+        if (pl.nq == 2) return go<128, 2>(a, pl.tiles, dev, st);
+        return go<128, 4>(a, pl.tiles, dev, st);
+    }
+    if (pl.nq == 1) return go<64, 1>(a, pl.tiles, dev, st);
+    if (pl.nq == 2) return go<64, 2>(a, pl.tiles, dev, st);
+    return go<64, 4>(a, pl.tiles, dev, st);
+}
+
+}  // namespace mxq

@@ -1,0 +1,247 @@
+"""include/mxq_ops.h: exported symbols, a C99 caller, statuses before any CUDA call, and the refusals of the
+torch helpers, all on the CPU (no kernel runs)."""
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+from block_scaled_microscaling_b200 import build as mxq_build
+from block_scaled_microscaling_b200 import mxq, ops
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "mxq_ops.h")
+FP4, FP8 = mxq.FORMATS["mxfp4"], mxq.FORMATS["mxfp8"]
+F32, BF16 = 0, 1
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    mxq_build.build()
+    return ops.lib()
+
+
+class FakeCuda:
+    """A host tensor that reports is_cuda = True; everything else is the tensor's own."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def fake(*shape, dtype=torch.bfloat16):
+    return FakeCuda(torch.zeros(shape, dtype=dtype))
+
+
+def u8(*shape):
+    return fake(*shape, dtype=torch.uint8)
+
+
+def test_exports_every_declared_symbol(library):
+    syms = re.findall(r"MXQ_API\s+[\w\s\*]+?\b(mxq_\w+)\s*\(", open(HEADER).read())
+    assert sorted(syms) == sorted(ops.OPS_EXPORTS)
+    out = subprocess.run(["nm", "-D", "--defined-only", mxq.LIB_PATH], capture_output=True, text=True).stdout
+    exported = set(re.findall(r"\bT\s+(mxq_\w+)", out))
+    assert set(syms) <= exported
+
+
+def test_c99_caller(tmp_path):
+    src = tmp_path / "c.c"
+    src.write_text('#include <stdio.h>\n#include "mxq_ops.h"\n'
+                   "int main(void) { mxq_kv_cache c = {0, 0, 0, 0, 100, 8, 64, 128};\n"
+                   "  if (mxq_kv_attention_workspace_bytes(&c, 0, 1, 1, 32, 100) != 0) return 1;\n"
+                   "  return mxq_matmul(MXQ_MXFP4_E2M1, 0, 0, 0, 0, 1, 1, 33, 0, MXQ_BF16, 0) == MXQ_ERR_SHAPE ? 0 : 2; }\n")
+    exe = tmp_path / "c"
+    lib_dir = os.path.dirname(mxq.LIB_PATH)
+    subprocess.run(["gcc", "-std=c99", "-pedantic", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"), str(src),
+                    "-o", str(exe), "-L", lib_dir, "-lmxq", f"-Wl,-rpath,{lib_dir}"], check=True)
+    assert subprocess.run([str(exe)]).returncode == 0
+
+
+def test_product_statuses_before_any_cuda_call():
+    mm = ops.mxq_matmul
+    assert mm(9, None, None, None, None, 1, 1, 32, None, BF16, None) == 1       # format
+    assert mm(FP4, None, None, None, None, 1, 1, 32, None, 5, None) == 1        # dtype
+    assert mm(1, None, None, None, None, 1, 1, 32, None, BF16, None) == 4       # MXFP6: not a product format
+    assert mm(0, None, None, None, None, 1, 1, 32, None, BF16, None) == 4       # AXS-6
+    assert mm(FP4, None, None, None, None, 1, 1, 33, None, BF16, None) == 2     # k % 32
+    assert mm(FP4, None, None, None, None, 1, 1, 0, None, BF16, None) == 2
+    assert mm(FP4, None, None, None, None, -1, 1, 32, None, BF16, None) == 2
+    assert mm(FP8, None, None, None, None, 1, -1, 32, None, BF16, None) == 2
+    assert mm(FP8, None, None, None, None, 1 << 31, 1, 32, None, BF16, None) == 2
+    assert mm(FP8, None, None, None, None, 1, 1, 1 << 32, None, BF16, None) == 2
+    assert mm(FP8, None, None, None, None, (1 << 31) - 400, (1 << 31) - 400, 32, None, BF16, None) == 2  # out too large
+    assert mm(FP8, None, None, None, None, 0, 5, 32, None, BF16, None) == 0     # empty
+    assert mm(FP8, None, None, None, None, 5, 0, 32, None, BF16, None) == 0
+    assert mm(FP8, None, None, None, None, 5, 5, 32, None, BF16, None) == 1     # null
+    qb = ops.mxq_quantize_both
+    assert qb(FP4, FP8, None, BF16, 5, 48, None, None, None, None, None) == 2
+    assert qb(FP4, FP8, None, BF16, 5, 64, None, None, None, None, None) == 1   # neither direction
+    assert qb(1, FP8, None, BF16, 5, 64, 16, 16, None, None, None) == 4
+    assert qb(1, FP8, None, BF16, 0, 64, None, None, 16, 16, None) == 0         # the unused format does not count
+    assert qb(FP4, 2, None, BF16, 5, 64, None, None, 16, 16, None) == 4
+    assert qb(FP4, 17, None, BF16, 5, 64, None, None, 16, 16, None) == 1
+    assert qb(FP4, FP8, None, 3, 5, 64, 16, 16, 16, 16, None) == 1
+    assert qb(FP4, FP8, None, BF16, -1, 64, 16, 16, 16, 16, None) == 2
+    assert qb(FP4, FP8, None, BF16, 5, 64, 16, 16, 16, 16, None) == 1           # null source
+
+
+def test_swiglu_statuses_before_any_cuda_call():
+    f = lambda rows, cols, ld, dt=BF16: ops.mxq_swiglu_forward(None, None, dt, rows, cols, ld, None, None, None, None, None, None)  # noqa: E731
+    b = lambda rows, cols, ld, dt=BF16: ops.mxq_swiglu_backward(None, dt, None, None, None, None, rows, cols, None, None, ld, None)  # noqa: E731
+    for call in (f, b):
+        assert call(4, 48, 48) == 2
+        assert call(4, 64, 32) == 2            # ld < cols
+        assert call(-1, 64, 64) == 2
+        assert call(1 << 40, 64, 1 << 20) == 2  # size overflow
+        assert call(4, 64, 68) == 3            # row stride not 16-byte aligned
+        assert call(4, 64, 64, 7) == 1
+        assert call(0, 64, 64) == 0
+        assert call(4, 64, 64) == 1            # null
+
+
+def cache(pages=4, heads=2, page=16, dim=64):
+    return (None, None, None, None, pages, heads, page, dim)
+
+
+def test_cache_statuses_before_any_cuda_call():
+    ap = lambda c, tokens=1, ks=128, vs=128, dt=BF16: ops.mxq_kv_append(c, None, ks, None, vs, dt, tokens, None, None)  # noqa: E731
+    rd = lambda c, tokens=1, dt=BF16: ops.mxq_kv_read(c, None, tokens, None, None, dt, None)  # noqa: E731
+    for call in (ap, rd):
+        assert call(cache(dim=96)) == 4
+        assert call(cache(dim=0)) == 2
+        assert call(cache(page=24)) == 2
+        assert call(cache(page=0)) == 2
+        assert call(cache(pages=-1)) == 2
+        assert call(cache(pages=1 << 40)) == 2
+        assert call(cache(heads=0)) == 2
+        assert call(cache(), -1) == 2
+        assert call(cache(), dt=4) == 1
+        assert call(cache(), 0) == 0
+        assert call(cache()) == 1
+    assert ap(cache(), ks=120) == 2            # stride below a token
+    assert ap(cache(), vs=132) == 3            # misaligned stride
+    at = lambda c=cache(), rows=2, rs=512, hs=64, heads=4, batch=2, starts=None, mq=1, ts=4, win=0, keys=64: ops.mxq_kv_attention(  # noqa: E731
+        c, None, rows, rs, hs, heads, batch, starts, mq, None, keys, None, ts, 1.0, win, None, None, None, 0, None)
+    assert at(cache(dim=32)) == 4
+    assert at(heads=3) == 2
+    assert at(heads=0) == 2
+    assert at(batch=-1) == 2
+    assert at(mq=2) == 2                       # 2 rows are not 2 sequences of 2 queries
+    assert at(win=-1) == 2
+    assert at(keys=-1) == 2
+    assert at(rs=516) == 3
+    assert at(hs=68) == 3
+    assert at(rows=0, mq=0) == 0
+    assert at(rows=0, batch=0) == 0
+    assert at(starts=16, mq=0) == 0
+    assert at() == 1
+    ws = ops.mxq_kv_attention_workspace_bytes
+    assert ws(cache(dim=96), 1, 1, 1, 2, 64) == 0
+    assert ws(cache(), 1, 1, 1, 2, 64) == 0                       # few keys: one split
+    assert ws(cache(pages=4096), 1, 1, 1, 2, 65536) > 0           # many: partial sums
+    assert ws(cache(pages=4096), 1, 1, 128, 2, 65536) == ws(cache(pages=4096), 1, 1, 1, 2, 65536)  # one row is one query
+
+
+def test_helpers_refuse_host_tensors():
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    c, s = torch.zeros((4, 32), dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8)
+    w = torch.zeros((64, 64), dtype=torch.bfloat16)
+    for call in [lambda: ops.matmul(c, s, c, s, "mxfp4"), lambda: ops.quantize_both(x, "mxfp4"),
+                 lambda: ops.linear(x, c, s, "mxfp4"), lambda: ops.linear_ste(x, w), lambda: ops.swiglu(x),
+                 lambda: ops.KVCache(*(torch.zeros((1, 1, 16, n), dtype=torch.uint8) for n in (32, 2, 32, 2)))]:
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call()
+
+
+def test_matmul_helper_refusals():
+    s = u8(512)
+    for call in [lambda: ops.matmul(u8(4, 32), s, u8(4, 48), s, "mxfp4"),      # different k
+                 lambda: ops.matmul(u8(4, 40), s, u8(4, 40), s, "mxfp4"),      # not whole blocks
+                 lambda: ops.matmul(u8(128), s, u8(4, 32), s, "mxfp4"),
+                 lambda: ops.matmul(u8(4, 32), u8(511), u8(4, 32), s, "mxfp4"),
+                 lambda: ops.matmul(u8(200, 32), s, u8(4, 32), s, "mxfp4"),    # 200 rows take two tile rows
+                 lambda: ops.matmul(FakeCuda(torch.zeros((32, 4), dtype=torch.uint8).t()), s, u8(4, 32), s, "mxfp4"),
+                 lambda: ops.matmul(u8(4, 32), s, u8(4, 32), s, "mxfp4", out=fake(4, 3)),
+                 lambda: ops.matmul(u8(4, 32), s, u8(4, 32), s, "mxfp4", out=FakeCuda(torch.zeros((4, 8), dtype=torch.bfloat16)[:, ::2])),
+                 lambda: ops.matmul(u8(4, 32), s, u8(4, 32), s, "nvfp4")]:
+        with pytest.raises(ValueError):
+            call()
+    for call in [lambda: ops.matmul(u8(4, 32), s, u8(4, 32), s, "mxfp4", out=fake(4, 4), dtype=torch.float32),
+                 lambda: ops.matmul(fake(4, 32), s, u8(4, 32), s, "mxfp4")]:
+        with pytest.raises(TypeError):
+            call()
+    for fmt in ("axs6", "mxfp6_e2m3", "mxfp6_e3m2"):
+        with pytest.raises(mxq.MXQError) as e:
+            ops.matmul(u8(4, 32), s, u8(4, 32), s, fmt)
+        assert e.value.status == 4
+    with pytest.raises(mxq.MXQError) as e:
+        ops.matmul(u8(4, 0), s, u8(4, 0), s, "mxfp4")
+    assert e.value.status == 2
+
+
+def test_linear_helper_refusals():
+    for call in [lambda: ops.quantize_both(fake(4, 64)), lambda: ops.quantize_both(fake(2, 4, 64), "mxfp4"),
+                 lambda: ops.quantize_both(FakeCuda(torch.zeros((64, 32)).t()), "mxfp4"),
+                 lambda: ops.linear(fake(4, 64), u8(8, 16), u8(512), "mxfp4"),
+                 lambda: ops.linear(FakeCuda(torch.zeros((64, 4)).t()), u8(8, 32), u8(512), "mxfp4"),
+                 lambda: ops.linear_ste(fake(4, 64), fake(32, 32)), lambda: ops.linear_ste(fake(4, 64), fake(32)),
+                 lambda: ops.swiglu(fake(4, 64), fake(4, 32)),
+                 lambda: ops.swiglu(fake(4, 64), fake(4, 64, dtype=torch.float32))]:
+        with pytest.raises(ValueError):
+            call()
+    for call in [lambda: ops.linear_ste(fake(4, 64), fake(33, 64)), lambda: ops.linear_ste(fake(4, 48), fake(32, 48)),
+                 lambda: ops.quantize_both(fake(4, 48), "mxfp8"), lambda: ops.swiglu(fake(4, 96)),
+                 lambda: ops.swiglu(fake(4, 63)), lambda: ops.swiglu(fake(4, 0), fake(4, 0))]:
+        with pytest.raises(mxq.MXQError) as e:
+            call()
+        assert e.value.status == 2
+    with pytest.raises(mxq.MXQError) as e:
+        ops.linear_ste(fake(4, 64), fake(32, 64), "mxfp6_e2m3")
+    assert e.value.status == 4
+    for call in [lambda: ops.linear_ste(fake(4, 64, dtype=torch.float16), fake(32, 64)),
+                 lambda: ops.swiglu(fake(4, 64, dtype=torch.float16))]:
+        with pytest.raises(TypeError):
+            call()
+
+
+def fake_cache(pages=4, heads=2, page=16, dim=64):
+    return ops.KVCache(*(u8(pages, heads, page, n) for n in (dim // 2, dim // 32, dim // 2, dim // 32)))
+
+
+def test_cache_helper_refusals():
+    i64 = lambda n: fake(n, dtype=torch.int64)  # noqa: E731
+    i32 = lambda *n: fake(*n, dtype=torch.int32)  # noqa: E731
+    c = fake_cache()
+    for call in [lambda: ops.KVCache(u8(4, 16, 32), u8(4, 16, 2), u8(4, 16, 32), u8(4, 16, 2)),
+                 lambda: ops.KVCache(u8(4, 2, 16, 32), u8(4, 2, 16, 1), u8(4, 2, 16, 32), u8(4, 2, 16, 2)),
+                 lambda: ops.KVCache(u8(4, 2, 16, 32), u8(4, 2, 16, 2), u8(4, 2, 32, 32), u8(4, 2, 16, 2)),
+                 lambda: ops.kv_append(fake(3, 2, 32), fake(3, 2, 64), c, i64(3)),
+                 lambda: ops.kv_append(fake(3, 2, 64), fake(4, 2, 64), c, i64(3)),
+                 lambda: ops.kv_append(fake(3, 2, 64), fake(3, 2, 64, dtype=torch.float32), c, i64(3)),
+                 lambda: ops.kv_append(fake(3, 2, 64), fake(3, 2, 64), c, i64(2)),
+                 lambda: ops.kv_append(FakeCuda(torch.zeros((3, 64, 2)).mT), fake(3, 2, 64, dtype=torch.float32), c, i64(3)),
+                 lambda: ops.kv_read(c, torch.zeros(3, dtype=torch.int64)),
+                 lambda: ops.kv_attention(fake(2, 4, 32), c, i32(2, 4), i32(2)),
+                 lambda: ops.kv_attention(fake(2, 4, 64, dtype=torch.float32), c, i32(2, 4), i32(2)),
+                 lambda: ops.kv_attention(fake(2, 3, 64), c, i32(2, 4), i32(2)),
+                 lambda: ops.kv_attention(fake(2, 4, 64), c, i32(3, 4), i32(2)),
+                 lambda: ops.kv_attention(fake(3, 4, 64), c, i32(2, 4), i32(2)),
+                 lambda: ops.kv_attention(fake(4, 4, 64), c, i32(2, 4), i32(2), max_q=1),
+                 lambda: ops.kv_attention(fake(2, 4, 64), c, i32(2, 4), i32(2), q_starts=i32(2)),
+                 lambda: ops.kv_attention(fake(2, 4, 64), c, i32(2, 4), i32(2), window=-1),
+                 lambda: ops.kv_attention(fake(2, 4, 64), c, i32(2, 4), i32(2), max_keys=-1),
+                 lambda: ops.kv_attention(fake(2, 4, 64), c, i32(2, 4), torch.zeros(2, dtype=torch.int32)),
+                 lambda: ops.kv_attention(FakeCuda(torch.zeros((2, 4, 128), dtype=torch.bfloat16)[..., ::2]), c, i32(2, 4), i32(2))]:
+        with pytest.raises(ValueError):
+            call()
+    for call in [lambda: ops.kv_append(fake(3, 2, 64), fake(3, 2, 64), c, i32(3)),
+                 lambda: ops.kv_read(c, i32(3)),
+                 lambda: ops.kv_attention(fake(2, 4, 64), c, i64(8), i32(2)),
+                 lambda: ops.kv_attention(fake(2, 4, 64), c, i32(2, 4), i64(2))]:
+        with pytest.raises(TypeError):
+            call()

@@ -1,0 +1,231 @@
+"""linear_ste and swiglu on the GPU: outputs and gradients against 64-bit formulas on the rounded operands and
+against differences.
+
+Tolerances: products as in test_matmul_gpu.py. swiglu computes in fp32 with an exponential and a division of at most
+two units in the last place (2^-22 each); a dozen such steps stay below 2^-18 relative for bf16 and, the steps other
+than these rounding by 2^-24, below 2^-20 for fp32. The factor 1 + g (1 - s) is a sum of terms of up to 1 + |g|, so its error counts against
+that sum of magnitudes. Outputs then round by half a step of their type."""
+import pytest
+import torch
+
+from block_scaled_microscaling_b200 import mxq, ops
+
+from test_matmul_gpu import close, decoded, half_step, values
+
+pytestmark = pytest.mark.gpu
+
+
+def columns(x, fmt="mxfp8"):
+    """x rounded with blocks of 32 rows, in 64 bits."""
+    rows = x.shape[0]
+    xt = torch.nn.functional.pad(x, (0, 0, 0, -rows % 32)).T.contiguous()
+    return mxq.fake_quantize(xt, fmt).double().T[:rows]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("m,n,k", [(1, 32, 32), (31, 64, 96), (32, 160, 64), (77, 96, 544), (333, 1024, 288), (260, 32, 1024)])
+def test_linear_ste(m, n, k, fmt, dtype):
+    x, w, g = values(m, m, k, dtype), values(n, n, k, dtype), values(k, m, n, dtype)
+    x.requires_grad_(), w.requires_grad_()
+    y = ops.linear_ste(x, w, fmt)
+    dx, dw = torch.autograd.grad(y, (x, w), g)
+    mxq.check_device()
+    assert (y.dtype, dx.dtype, dw.dtype) == (dtype,) * 3
+    x, w = x.detach(), w.detach()
+    a, b = decoded(x, fmt), decoded(w, fmt)
+    close(y.detach(), a @ b.T, a.abs() @ b.abs().T, k)
+    a, b = decoded(g, "mxfp8"), columns(w)
+    close(dx, a @ b, a.abs() @ b.abs(), n)
+    a, b = columns(g), columns(x)
+    close(dw, a.T @ b, a.abs().T @ b.abs(), m)
+
+
+def test_linear_ste_against_differences():
+    """Operands on the formats' grid under every scale that can arise: the layer is then linear and differences of
+    sum(y * g) over steps that stay on the grid are its gradient exactly."""
+    rng = torch.Generator(device="cuda").manual_seed(0)
+    pick = lambda *s: (torch.randint(1, 4, s, generator=rng, device="cuda") * (2 * torch.randint(0, 2, s, generator=rng, device="cuda") - 1)).float()  # noqa: E731
+    x, w, g = pick(40, 64), pick(32, 64), pick(40, 32)
+    x.requires_grad_(), w.requires_grad_()
+    loss = lambda a, b: (ops.linear_ste(a, b, "mxfp8").double() * g).sum()  # noqa: E731
+    dx, dw = torch.autograd.grad((ops.linear_ste(x, w) * g).sum(), (x, w))
+    for t, d, f in ((x, dx, lambda a: loss(a, w)), (w, dw, lambda b: loss(x, b))):
+        for i, j in ((0, 0), (7, 33), (31, 63)):
+            up, down = t.detach().clone(), t.detach().clone()
+            up[i, j] += 0.5
+            down[i, j] -= 0.5
+            assert float(f(up) - f(down)) == float(d[i, j])
+
+
+def test_linear_ste_leading_dimensions_strides_and_partial_gradients():
+    x, w = values(1, 6 * 128, 64).view(6, 128, 64).transpose(0, 1), values(2, 32, 64)
+    x.requires_grad_()
+    y = ops.linear_ste(x, w)
+    assert y.shape == (128, 6, 32)
+    g = values(3, 1, 32).view(1, 1, 32).expand(128, 6, 32)  # a broadcast gradient
+    dx, = torch.autograd.grad(y, x, g)
+    assert dx.shape == x.shape
+    a, b = decoded(g.reshape(-1, 32), "mxfp8"), columns(w)
+    close(dx.reshape(-1, 64), a @ b, a.abs() @ b.abs(), 32)
+    x = x.detach()
+    w.requires_grad_()
+    dw, = torch.autograd.grad(ops.linear_ste(x, w), w, g)
+    a, b = columns(g.reshape(-1, 32)), columns(x.reshape(-1, 64))
+    close(dw, a.T @ b, a.abs().T @ b.abs(), 768)
+    with torch.no_grad():
+        assert not ops.linear_ste(x, w).requires_grad
+
+
+def test_linear_ste_without_tokens():
+    x = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    w = values(2, 32, 64).requires_grad_()
+    y = ops.linear_ste(x, w)
+    assert y.shape == (0, 32)
+    dx, dw = torch.autograd.grad(y, (x, w), torch.zeros_like(y))
+    assert dx.shape == (0, 64) and (dw == 0).all() and dw.shape == w.shape
+
+
+def test_linear_ste_keeps_33_64ths_of_the_input():
+    x, w = values(1, 4096, 2560).requires_grad_(), values(2, 32, 2560).requires_grad_()
+    kept = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: kept.append(t) or t, lambda t: t):
+        ops.linear_ste(x, w)
+    size = sum(t.numel() * t.element_size() for t in kept if t.data_ptr() != w.data_ptr())
+    assert size == x.numel() * 33 // 32
+
+
+def swiglu64(gate, up):
+    return gate / (1 + torch.exp(-gate)) * up
+
+
+def swiglu_grads64(gate, up, dy):
+    s = 1 / (1 + torch.exp(-gate))
+    return dy * up * s * (1 + gate * (1 - s)), dy * gate * s, (dy * up * s).abs() * (1 + gate.abs())
+
+
+def near(got, want, size):
+    rel = 2.0 ** -18 if got.dtype == torch.bfloat16 else 2.0 ** -20
+    err = (got.double() - want).abs()
+    tiny = torch.finfo(got.dtype).tiny  # results below the normal range may flush
+    bad = err > half_step(got.dtype) * want.abs() + rel * size + tiny
+    assert not bad.any(), (int(bad.sum()), float(err[bad].max()))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("packed", [True, False])
+@pytest.mark.parametrize("rows,cols", [(1, 32), (3, 64), (5, 2560), (129, 96), (1000, 9728)])
+def test_swiglu(rows, cols, packed, dtype):
+    both = values(rows, rows, 2 * cols, dtype)
+    dy = values(cols, rows, cols, dtype)
+    gate, up = both[:, :cols], both[:, cols:]
+    if packed:
+        both.requires_grad_()
+        y = ops.swiglu(both)
+        d, = torch.autograd.grad(y, both, dy)
+        assert d.shape == both.shape
+        dgate, dup = d[:, :cols], d[:, cols:]
+    else:
+        a, b = gate.clone().requires_grad_(), up.clone().requires_grad_()
+        y = ops.swiglu(a, b)
+        dgate, dup = torch.autograd.grad(y, (a, b), dy)
+    assert y.shape == dy.shape and y.dtype == dtype
+    gate, up, dy = gate.detach(), up.detach(), dy.double()
+    want = swiglu64(gate.double(), up.double())
+    near(y.detach(), want, want.abs())
+    g8, u8 = decoded(gate, "mxfp8"), decoded(up, "mxfp8")
+    wg, wu, size = swiglu_grads64(g8, u8, dy)
+    near(dgate, wg, size)
+    near(dup, wu, wu.abs())
+
+
+def test_swiglu_gradients_against_differences():
+    """Central differences (step 2^-13) of the 64-bit function at the rounded point: error below step^2 times the
+    third derivative (under 1) times the other factors, plus the tolerance above."""
+    both = torch.randn((4, 64), generator=torch.Generator(device="cuda").manual_seed(0), device="cuda").requires_grad_()
+    dy = torch.randn((4, 32), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    d, = torch.autograd.grad(ops.swiglu(both), both, dy)
+    g, u = decoded(both.detach()[:, :32], "mxfp8"), decoded(both.detach()[:, 32:], "mxfp8")
+    h = 2.0 ** -13
+    dg = (swiglu64(g + h, u) - swiglu64(g - h, u)) / (2 * h) * dy
+    du = (swiglu64(g, u + h) - swiglu64(g, u - h)) / (2 * h) * dy
+    bound = lambda f: (h * h + 2.0 ** -20 * (1 + g.abs())) * (dy.abs() * f)  # noqa: E731
+    assert ((d[:, :32].double() - dg).abs() <= bound(u.abs())).all()
+    assert ((d[:, 32:].double() - du).abs() <= bound(g.abs())).all()
+
+
+def test_swiglu_strided_halves_extremes_and_no_grad():
+    both = values(1, 6 * 10, 128).view(6, 10, 128)
+    gate, up = both[..., :64], both[..., 64:]
+    want = ops.swiglu(gate.contiguous(), up.contiguous())
+    assert torch.equal(ops.swiglu(gate, up), want)            # one stride for both
+    assert torch.equal(ops.swiglu(gate, up.contiguous()), want)
+    assert torch.equal(ops.swiglu(both), want)
+    odd = torch.zeros((60, 65), dtype=torch.bfloat16, device="cuda")  # a stride that is not 16-byte aligned
+    odd[:, :64] = gate.reshape(60, 64)
+    assert torch.equal(ops.swiglu(odd[:, :64], up.reshape(60, 64)), want.view(60, 64))
+    x = torch.tensor([0.0, -0.0, 200.0, -200.0, 1e38, -1e38, 90.0, -90.0] * 8, device="cuda")[None]
+    y = ops.swiglu(x.clone().requires_grad_())
+    assert torch.isfinite(y[0, 2:4]).all() and (y[0, 3] == 0) and torch.isfinite(y[0, 5])
+    bad = values(2, 3, 128).requires_grad_()
+    with torch.no_grad():
+        bad[1, 5] = float("nan")       # gate's first block of row 1
+    d, = torch.autograd.grad(ops.swiglu(bad), bad, torch.ones((3, 64), dtype=bad.dtype, device="cuda"))
+    nan = torch.zeros_like(d, dtype=torch.bool)
+    nan[1, :32], nan[1, 64:96] = True, True
+    assert torch.equal(torch.isnan(d), nan)
+    assert ops.swiglu(torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda")).shape == (0, 32)
+
+
+def test_swiglu_entry_point_strides_and_overlaps():
+    buf = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    p, st = buf.data_ptr(), torch.cuda.current_stream().cuda_stream
+    f, b = ops.mxq_swiglu_forward, ops.mxq_swiglu_backward
+    ck = (p + 8192, p + 9216, p + 10240, p + 11264)
+    assert f(p, p + 64, 1, 4, 32, 64, p + 4096, *ck, st) == 0          # halves of one matrix
+    assert f(p, p + 64, 1, 4, 32, 64, p + 4096, None, None, None, None, st) == 0
+    assert f(p, p + 64, 1, 4, 32, 64, p + 4096, p + 8192, None, None, None, st) == 1
+    assert f(p, p + 64, 1, 4, 32, 64, p + 256, *ck, st) == 1           # out over gate
+    assert f(p, p + 64, 1, 4, 32, 64, p + 8192, *ck, st) == 1          # out over a checkpoint
+    assert f(p + 2, p + 64, 1, 4, 32, 64, p + 4096, *ck, st) == 3
+    assert b(p + 4096, 1, *ck, 4, 32, p, p + 64, 64, st) == 0          # interleaved halves
+    assert b(p + 4096, 1, *ck, 4, 32, p, p + 32, 64, st) == 1          # rows overlap
+    assert b(p + 4096, 1, *ck, 4, 32, p, p, 64, st) == 1
+    assert b(p + 4096, 1, *ck, 4, 32, p + 4096, p + 64, 64, st) == 1   # over grad
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_mlp_step_as_it_is_used(fmt):
+    """down(swiglu(up(x))) with its gradients, twice, and captured into a graph: the same bits every time."""
+    x, w1, w2 = values(1, 150, 256), values(2, 2 * 320, 256), values(3, 256, 320)
+    leaves = [t.requires_grad_() for t in (x, w1, w2)]
+    g = values(4, 150, 256)
+
+    def step():
+        y = ops.linear_ste(ops.swiglu(ops.linear_ste(x, w1, fmt)), w2, fmt)
+        return [y.detach(), *torch.autograd.grad(y, leaves, g)]
+
+    first, again = step(), step()
+    mxq.check_device()
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+    assert all(torch.isfinite(t).all() for t in first)
+    # forward against the definition
+    a, b = decoded(x.detach(), fmt), decoded(w1.detach(), fmt)
+    h = ops.linear_ste(x.detach(), w1.detach(), fmt)
+    close(h, a @ b.T, a.abs() @ b.abs().T, 256)
+    s = ops.swiglu(h)
+    a, b = decoded(s, fmt), decoded(w2.detach(), fmt)
+    close(first[0], a @ b.T, a.abs() @ b.abs().T, 320)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for t in out:
+        t.zero_()
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(first, out))
