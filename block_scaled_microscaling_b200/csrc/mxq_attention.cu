@@ -49,6 +49,7 @@ struct AtArgs {
     long long table_stride;
     long long max_keys;
     int batch, heads, group, max_q, window, splits, row_tiles;
+    bool fill;
     float scale;   // already times log2(e)
     __nv_bfloat16* out;
     float* lse;
@@ -88,6 +89,28 @@ __device__ __forceinline__ Groups groups_of(const AtArgs& p, const Span& s, int 
     const int n = g.hi - g.lo;
     g.per = max((n + p.splits - 1) / p.splits, kAtMinGroups);
     return g;
+}
+
+// zeros (and -inf) for the rows of this key head's queries that no CTA computes: before the first sequence, beyond
+// max_q in each, behind the last
+template <int D> __device__ void fill_rows(const AtArgs& p, const Span& s, int b, int head) {
+    for (int part = 0; part < 3; ++part) {
+        int lo = s.q0 + s.nq, hi = s.q0 + s.n;
+        if (part == 1) {
+            lo = 0;
+            hi = b == 0 ? s.q0 : 0;
+        } else if (part == 2) {
+            lo = s.q0 + s.n;
+            hi = b == p.batch - 1 ? (int)p.q_rows : lo;
+        }
+        for (int r = lo; r < hi; ++r) {
+            const long long at = (long long)r * p.heads + head * p.group;
+            for (int i = threadIdx.x; i < p.group * (D / 8); i += kAtThreads)
+                reinterpret_cast<uint4*>(p.out + at * D)[i] = make_uint4(0, 0, 0, 0);
+            if (p.lse)
+                for (int i = threadIdx.x; i < p.group; i += kAtThreads) p.lse[at + i] = -INFINITY;
+        }
+    }
 }
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -217,6 +240,7 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
 
     const Span s = span_of(p, b);
     const int rows = s.nq * p.group, r0 = rt * ROWS;
+    if (p.fill && rt == 0 && sp == 0) fill_rows<D>(p, s, b, head);
     if (r0 >= rows) return;
     const int i0 = r0 / p.group, i1 = (min(r0 + ROWS, rows) - 1) / p.group;
     const Groups gr = groups_of(p, s, i0, i1);
@@ -683,6 +707,7 @@ cudaError_t launch_kv_attention(const KvAttention& x, cudaStream_t st) {
     a.group = x.heads / x.c.heads;
     a.max_q = x.max_q;
     a.window = x.window;
+    a.fill = x.fill;
     a.splits = pl.splits;
     a.row_tiles = pl.row_tiles;
     a.scale = x.scale * kLog2e;

@@ -134,6 +134,7 @@ struct KvAttention {
     long long q_rows, q_row_stride, q_head_stride, batch, max_keys, table_stride;
     const int *starts, *lens, *table;
     int heads, max_q, window;
+    bool fill;  // rows that no query of a sequence computes get zeros
     float scale;
     void* out;
     float* lse;

@@ -14,6 +14,12 @@ constexpr int64_t kMaxInt = 0x7FFFFFFF;
 
 bool product_format(mxq_format f) { return f == MXQ_MXFP4_E2M1 || f == MXQ_MXFP8_E4M3; }
 
+bool product_shape_ok(int64_t m, int64_t n, int64_t k) {
+    if (m < 0 || n < 0 || m >= kMaxInt - 256 || n >= kMaxInt - 256 || k >= kMaxInt - 512) return false;
+    if (check_shape(m, k) != MXQ_OK || check_shape(n, k) != MXQ_OK) return false;
+    return n == 0 || m <= kMaxElems / n;
+}
+
 struct Range {
     const void* p;
     size_t n;
@@ -82,10 +88,7 @@ mxq_status mxq_matmul(mxq_format fmt, const void* a_codes, const void* a_scales,
                       int64_t m, int64_t n, int64_t k, void* out, mxq_dtype dtype, mxq_stream stream) {
     if (!fmt_ok(fmt) || !dtype_ok(dtype)) return MXQ_ERR_INVALID_ARG;
     if (!product_format(fmt)) return MXQ_ERR_UNSUPPORTED;
-    if (m < 0 || n < 0 || m >= kMaxInt - 256 || n >= kMaxInt - 256 || k >= kMaxInt - 512) return MXQ_ERR_SHAPE;
-    MXQ_TRY(check_shape(m, k));
-    MXQ_TRY(check_shape(n, k));
-    if (n > 0 && m > kMaxElems / n) return MXQ_ERR_SHAPE;
+    if (!product_shape_ok(m, n, k)) return MXQ_ERR_SHAPE;
     if (m == 0 || n == 0) return MXQ_OK;
     MXQ_TRY(check_ptr(a_codes, 16));
     MXQ_TRY(check_ptr(a_scales, 16));
@@ -130,6 +133,33 @@ mxq_status mxq_quantize_both(mxq_format row_fmt, mxq_format col_fmt, const void*
     if (!disjoint(in, res)) return MXQ_ERR_INVALID_ARG;
     return from_cuda(mxq::launch_quantize_both(r ? (int)row_fmt : -1, c ? (int)col_fmt : -1, src, (int)dtype, rows, cols,
                                                row_codes, row_scales, col_codes, col_scales, (cudaStream_t)stream));
+}
+
+size_t mxq_linear_workspace_bytes(mxq_format fmt, int64_t m, int64_t k) {
+    if (!fmt_ok(fmt) || !product_format(fmt) || check_shape(m, k) != MXQ_OK) return 0;
+    return codes_bytes(fmt, m, k) + mxq_mma_scales_bytes(m, k);  // codes: whole blocks, so the scales are 16-byte aligned
+}
+
+mxq_status mxq_linear(mxq_format fmt, const void* x, mxq_dtype dtype, int64_t m, int64_t k, const void* b_codes,
+                      const void* b_scales, int64_t n, void* out, void* workspace, size_t workspace_bytes,
+                      mxq_stream stream) {
+    if (!fmt_ok(fmt) || !dtype_ok(dtype)) return MXQ_ERR_INVALID_ARG;
+    if (!product_format(fmt)) return MXQ_ERR_UNSUPPORTED;
+    if (!product_shape_ok(m, n, k)) return MXQ_ERR_SHAPE;
+    if (m == 0 || n == 0) return MXQ_OK;
+    for (const void* p : {x, b_codes, b_scales, (const void*)out, (const void*)workspace}) MXQ_TRY(check_ptr(p, 16));
+    const size_t nc = codes_bytes(fmt, m, k), need = nc + mxq_mma_scales_bytes(m, k);
+    if (workspace_bytes < need) return MXQ_ERR_INVALID_ARG;
+    const Range in[] = {{x, (size_t)m * (size_t)k * dtype_bytes(dtype)},
+                        {b_codes, codes_bytes(fmt, n, k)},
+                        {b_scales, mxq_mma_scales_bytes(n, k)}};
+    const Range res[] = {{out, (size_t)m * (size_t)n * dtype_bytes(dtype)}, {workspace, need}};
+    if (!disjoint(in, res)) return MXQ_ERR_INVALID_ARG;
+    void* const scales = static_cast<char*>(workspace) + nc;
+    MXQ_TRY(from_cuda(mxq::launch_quantize_both((int)fmt, -1, x, (int)dtype, m, k, workspace, scales, nullptr, nullptr,
+                                                (cudaStream_t)stream)));
+    return from_cuda(mxq::launch_matmul((int)fmt, workspace, scales, b_codes, b_scales, m, n, k, out, (int)dtype,
+                                        (cudaStream_t)stream));
 }
 
 mxq_status mxq_swiglu_forward(const void* gate, const void* up, mxq_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
@@ -230,7 +260,7 @@ size_t mxq_kv_attention_workspace_bytes(const mxq_kv_cache* cache, int64_t batch
 mxq_status mxq_kv_attention(const mxq_kv_cache* cache, const void* q, int64_t q_rows, int64_t q_row_stride,
                             int64_t q_head_stride, int32_t q_heads, int64_t batch, const int32_t* q_starts, int32_t max_q,
                             const int32_t* seq_lens, int64_t max_keys, const int32_t* block_table, int64_t table_stride,
-                            float scale, int32_t window, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                            float scale, int32_t window, int32_t fill, void* out, float* lse, void* workspace, size_t workspace_bytes,
                             mxq_stream stream) {
     MXQ_TRY(check_cache(cache));
     if (q_heads < 1 || q_heads % cache->kv_heads != 0 || batch < 0 || batch > kMaxInt || q_rows < 0 || q_rows > kMaxInt - 1 ||
@@ -283,6 +313,7 @@ mxq_status mxq_kv_attention(const mxq_kv_cache* cache, const void* q, int64_t q_
     x.heads = q_heads;
     x.max_q = max_q;
     x.window = window;
+    x.fill = fill != 0;
     x.scale = scale;
     x.out = out;
     x.lse = lse;

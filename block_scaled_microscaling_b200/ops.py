@@ -19,9 +19,9 @@ import ctypes
 import math
 
 from . import mxq
-from .mxq import DTYPES, FORMATS, MXQError, _as2d, _check, _dt, _finish, _fits, _fmt, _on_gpu, _stream, _torch
+from .mxq import MXQError, _as2d, _check, _dt, _finish, _fits, _fmt, _on_gpu, _torch
 
-OPS_EXPORTS = ["mxq_matmul", "mxq_quantize_both", "mxq_swiglu_forward", "mxq_swiglu_backward", "mxq_kv_append",
+OPS_EXPORTS = ["mxq_matmul", "mxq_quantize_both", "mxq_linear_workspace_bytes", "mxq_linear", "mxq_swiglu_forward", "mxq_swiglu_backward", "mxq_kv_append",
                "mxq_kv_read", "mxq_kv_attention_workspace_bytes", "mxq_kv_attention"]
 PRODUCT_FORMATS = ("mxfp4", "mxfp8")
 
@@ -45,13 +45,15 @@ def lib():
         for name, args, res in [
             ("mxq_matmul", [i32, vp, vp, vp, vp, i64, i64, i64, vp, i32, vp], i32),
             ("mxq_quantize_both", [i32, i32, vp, i32, i64, i64, vp, vp, vp, vp, vp], i32),
+            ("mxq_linear_workspace_bytes", [i32, i64, i64], sz),
+            ("mxq_linear", [i32, vp, i32, i64, i64, vp, vp, i64, vp, vp, sz, vp], i32),
             ("mxq_swiglu_forward", [vp, vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp], i32),
             ("mxq_swiglu_backward", [vp, i32, vp, vp, vp, vp, i64, i64, vp, vp, i64, vp], i32),
             ("mxq_kv_append", [cache, vp, i64, vp, i64, i32, i64, vp, vp], i32),
             ("mxq_kv_read", [cache, vp, i64, vp, vp, i32, vp], i32),
             ("mxq_kv_attention_workspace_bytes", [cache, i64, i64, i32, i32, i64], sz),
-            ("mxq_kv_attention", [cache, vp, i64, i64, i64, i32, i64, vp, i32, vp, i64, vp, i64, f32, i32, vp, vp, vp, sz, vp],
-             i32),
+            ("mxq_kv_attention", [cache, vp, i64, i64, i64, i32, i64, vp, i32, vp, i64, vp, i64, f32, i32, i32, vp, vp, vp, sz,
+                                  vp], i32),
         ]:
             fn = getattr(L, name)
             fn.argtypes = args
@@ -69,6 +71,14 @@ def mxq_matmul(fmt, a_codes, a_scales, b_codes, b_scales, m, n, k, out, dtype, s
 def mxq_quantize_both(row_fmt, col_fmt, src, dtype, rows, cols, row_codes, row_scales, col_codes, col_scales, stream):
     return lib().mxq_quantize_both(row_fmt, col_fmt, src, dtype, rows, cols, row_codes, row_scales, col_codes, col_scales,
                                    stream)
+
+
+def mxq_linear_workspace_bytes(fmt, m, k):
+    return lib().mxq_linear_workspace_bytes(fmt, m, k)
+
+
+def mxq_linear(fmt, x, dtype, m, k, b_codes, b_scales, n, out, workspace, workspace_bytes, stream):
+    return lib().mxq_linear(fmt, x, dtype, m, k, b_codes, b_scales, n, out, workspace, workspace_bytes, stream)
 
 
 def mxq_swiglu_forward(gate, up, dtype, rows, cols, ld, out, gate_codes, gate_scales, up_codes, up_scales, stream):
@@ -95,9 +105,9 @@ def mxq_kv_attention_workspace_bytes(cache, batch, q_rows, max_q, q_heads, max_k
 
 
 def mxq_kv_attention(cache, q, q_rows, q_row_stride, q_head_stride, q_heads, batch, q_starts, max_q, seq_lens, max_keys,
-                     block_table, table_stride, scale, window, out, lse, workspace, workspace_bytes, stream):
+                     block_table, table_stride, scale, window, fill, out, lse, workspace, workspace_bytes, stream):
     return lib().mxq_kv_attention(ctypes.byref(_Cache(*cache)), q, q_rows, q_row_stride, q_head_stride, q_heads, batch,
-                                  q_starts, max_q, seq_lens, max_keys, block_table, table_stride, scale, window, out, lse,
+                                  q_starts, max_q, seq_lens, max_keys, block_table, table_stride, scale, window, fill, out, lse,
                                   workspace, workspace_bytes, stream)
 
 
@@ -121,6 +131,48 @@ def _on(stream, call):
         return call()
     with _torch().cuda.stream(stream):
         return call()
+
+
+def _raw_stream(t):
+    """Handle of the stream current on t's device (torch.cuda.current_stream() takes as long as a launch)."""
+    return _torch()._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _bytes(n, like):
+    torch = _torch()
+    return torch.empty(n, dtype=torch.uint8, device=like.device)
+
+
+class _Operand:
+    """Pointers of the codes and tile-layout scales of a [rows, cols] operand that lie one after the other from `at` on
+    (payloads are multiples of 16 bytes and scale tiles of 512, so all are aligned as the product wants them)."""
+    __slots__ = ("codes", "scales", "end")
+
+    def __init__(self, at, fmt, rows, cols):
+        self.codes = at
+        self.scales = at + rows * (cols // 32) * 4 * mxq.ELEM_BITS[fmt]
+        self.end = self.scales + _scale_bytes(rows, cols)
+
+
+def _scale_bytes(rows, cols):
+    return -(-rows // 128) * 128 * (-(-cols // 128) * 4)
+
+
+def _operand_bytes(fmt, rows, cols):
+    return rows * (cols // 32) * 4 * mxq.ELEM_BITS[fmt] + _scale_bytes(rows, cols)
+
+
+def _both(x, row, row_fmt, col, col_fmt):
+    """Quantize the contiguous 2-D x into the operands `row` and / or `col` (None: left out)."""
+    _check(mxq_quantize_both(mxq.FORMATS[row_fmt], mxq.FORMATS[col_fmt], x.data_ptr(), _dt(x), x.shape[0], x.shape[1],
+                             row and row.codes, row and row.scales, col and col.codes, col and col.scales, _raw_stream(x)),
+           "mxq_quantize_both")
+
+
+def _product(a, b, fmt, m, n, k, out):
+    _check(mxq_matmul(mxq.FORMATS[fmt], a.codes, a.scales, b.codes, b.scales, m, n, k, out.data_ptr(), _dt(out),
+                      _raw_stream(out)), "mxq_matmul")
+    return out
 
 
 def matmul(a_codes, a_scales, b_codes, b_scales, fmt, out=None, dtype=None, stream=None, check=False):
@@ -157,7 +209,7 @@ def matmul(a_codes, a_scales, b_codes, b_scales, fmt, out=None, dtype=None, stre
             raise ValueError(f"out must hold {m} x {n} values")
         _fits(o, 0, "out")
         _check(mxq_matmul(f, a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(), m, n, k,
-                          o.data_ptr(), _dt(o), _stream(None)), "mxq_matmul")
+                          o.data_ptr(), _dt(o), _raw_stream(o)), "mxq_matmul")
         return o
 
     o = _on(stream, call)
@@ -192,8 +244,8 @@ def quantize_both(x, row_fmt=None, col_fmt=None, stream=None):
         if col_fmt is not None:
             cc, cs = mxq.empty_codes(col_fmt, cols, rows32, x.device), e(mxq.mxq_mma_scales_bytes(cols, rows32) if rows else 0)
         p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        _check(mxq_quantize_both(fr, fc, x.data_ptr(), dt, rows, cols, p(rc), p(rs), p(cc), p(cs), _stream(None)),
-               "mxq_quantize_both")
+        _check(mxq_quantize_both(fr, fc, x.data_ptr(), dt, rows, cols, p(rc), p(rs), p(cc), p(cs),
+                                 _raw_stream(x)), "mxq_quantize_both")
         return rc, rs, cc, cs
 
     return _on(stream, call)
@@ -205,16 +257,29 @@ def linear(x, w_codes, w_scales, fmt, out=None, stream=None, check=False):
     if not x.is_contiguous() or x.dim() == 0:
         raise ValueError("x must be contiguous, of at least one dimension")
     _on_gpu(x, "x")
-    _product_fmt(fmt)
+    f = _product_fmt(fmt)
     rows, k = _as2d(x)
     if w_codes.dim() != 2 or w_codes.shape[1] * 32 != k * 4 * mxq.ELEM_BITS[fmt]:
         raise ValueError(f"w_codes {tuple(w_codes.shape)} do not belong to rows of {k} values in {fmt}")
     n = w_codes.shape[0]
+    for t, need, what in ((w_codes, 0, "w_codes"), (w_scales, mxq.mxq_mma_scales_bytes(n, k), "w_scales")):
+        _on_gpu(t, what)
+        _u8(t, what)
+        _fits(t, need, what)
 
     def call():
-        o = out if out is not None else _torch().empty((*x.shape[:-1], n), dtype=x.dtype, device=x.device)
-        codes, scales, _, _ = quantize_both(x.view(rows, k), fmt)
-        matmul(codes, scales, w_codes, w_scales, fmt, out=o, dtype=x.dtype)
+        o = out
+        if o is None:
+            o = _torch().empty((*x.shape[:-1], n), dtype=x.dtype, device=x.device)
+        else:
+            _on_gpu(o, "out")
+            if o.dtype != x.dtype or o.numel() != rows * n:
+                raise ValueError(f"out must hold {rows} x {n} values of {x.dtype}")
+            _fits(o, 0, "out")
+        need = mxq_linear_workspace_bytes(f, rows, k)
+        ws = _bytes(need, x)
+        _check(mxq_linear(f, x.data_ptr(), _dt(x), rows, k, w_codes.data_ptr(), w_scales.data_ptr(), n, o.data_ptr(),
+                          ws.data_ptr(), need, _raw_stream(x)), "mxq_linear")
         return o
 
     o = _on(stream, call)
@@ -225,7 +290,14 @@ def linear(x, w_codes, w_scales, fmt, out=None, stream=None, check=False):
 # ---- training: straight-through gradients from 8-bit checkpoints ----------------------
 
 def _flat(t):
-    return t.reshape(-1, t.shape[-1]).contiguous()
+    t = t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _checkpoint(buf, rows, cols):
+    """Pointers of gate's codes and scales and up's in one allocation of 66 bytes per block (codes first: aligned)."""
+    p, n = buf.data_ptr(), rows * cols
+    return p, p + 2 * n, p + n, p + 2 * n + n // 32
 
 
 def _functions():
@@ -236,36 +308,83 @@ def _functions():
     torch = _torch()
     from torch.autograd.function import once_differentiable
 
+    def first_order(backward, ctx, grad):
+        """The gradients are not differentiable: under create_graph a second derivative raises."""
+        if torch.is_grad_enabled():
+            return once_differentiable(backward)(ctx, grad)
+        return backward(ctx, grad)
+
+    def linear_backward(ctx, grad):
+        weight, kept = ctx.saved_tensors
+        (m, n, k), (xt, wt) = ctx.sizes, ctx.types
+        dx = dw = None
+        if m == 0:  # no tokens
+            dx = None if weight is None else torch.empty(ctx.shape, dtype=xt, device=grad.device)
+            dw = None if kept is None else torch.zeros((n, k), dtype=wt, device=grad.device)
+            return dx, dw, None
+        g, m32 = _flat(grad), -(-m // 32) * 32
+        need = 0 if weight is None else _operand_bytes("mxfp8", m, n) + _operand_bytes("mxfp8", k, n)
+        need += 0 if kept is None else _operand_bytes("mxfp8", n, m32)
+        scratch = _bytes(need, g)
+        at, row, col = scratch.data_ptr(), None, None
+        if weight is not None:
+            row = _Operand(at, "mxfp8", m, n)
+            w = _Operand(row.end, "mxfp8", k, n)
+            at = w.end
+        if kept is not None:
+            col = _Operand(at, "mxfp8", n, m32)
+        if row or col:
+            _both(g, row, "mxfp8", col, "mxfp8")
+        if row:
+            _both(weight if weight.is_contiguous() else weight.contiguous(), None, "mxfp8", w, "mxfp8")
+            dx = _product(row, w, "mxfp8", m, k, n, torch.empty(ctx.shape, dtype=xt, device=g.device))
+        if col:
+            x = _Operand(kept.data_ptr(), "mxfp8", k, m32)
+            dw = _product(col, x, "mxfp8", n, k, m32, torch.empty((n, k), dtype=wt, device=g.device))
+        return dx, dw, None
+
     class Linear(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, weight, fmt):
             x2 = _flat(x)
+            (m, k), n = x2.shape, weight.shape[0]
             need_dx, need_dw = ctx.needs_input_grad[:2]
-            codes, scales, ctx_codes, ctx_scales = quantize_both(x2, fmt, "mxfp8" if need_dw else None)
-            wc, ws, _, _ = quantize_both(weight.contiguous(), fmt)
-            y = matmul(codes, scales, wc, ws, fmt, dtype=x.dtype)
-            # the checkpoint is the operand of the weight's gradient: x rounded along the tokens
-            ctx.save_for_backward(weight if need_dx else None, ctx_codes, ctx_scales)
-            ctx.shape, ctx.types = x.shape, (x.dtype, weight.dtype)
-            return y.view(*x.shape[:-1], weight.shape[0])
+            y = torch.empty((*x.shape[:-1], n), dtype=x.dtype, device=x.device)
+            kept = None
+            if m:
+                m32 = -(-m // 32) * 32
+                scratch = _bytes(_operand_bytes(fmt, m, k) + _operand_bytes(fmt, n, k), x2)
+                a = _Operand(scratch.data_ptr(), fmt, m, k)
+                b, col = _Operand(a.end, fmt, n, k), None
+                if need_dw:  # the checkpoint is the operand of the weight's gradient: x rounded along the tokens
+                    kept = _bytes(_operand_bytes("mxfp8", k, m32), x2)
+                    col = _Operand(kept.data_ptr(), "mxfp8", k, m32)
+                _both(x2, a, fmt, col, "mxfp8")
+                _both(weight if weight.is_contiguous() else weight.contiguous(), b, fmt, None, "mxfp8")
+                _product(a, b, fmt, m, n, k, y)
+            elif need_dw:
+                kept = _bytes(0, x2)
+            ctx.save_for_backward(weight if need_dx else None, kept)
+            ctx.shape, ctx.sizes, ctx.types = x.shape, (m, n, k), (x.dtype, weight.dtype)
+            return y
 
         @staticmethod
-        @once_differentiable
         def backward(ctx, grad):
-            weight, xc, xs = ctx.saved_tensors
-            need_dx, need_dw = weight is not None, xc is not None
-            dx = dw = None
-            if not need_dx and not need_dw:
-                return None, None, None
-            rc, rs, cc, cs = quantize_both(_flat(grad), "mxfp8" if need_dx else None, "mxfp8" if need_dw else None)
-            if need_dx:
-                _, _, wc, ws = quantize_both(weight.contiguous(), None, "mxfp8")
-                dx = matmul(rc, rs, wc, ws, "mxfp8", dtype=ctx.types[0]).view(ctx.shape)
-            if need_dw and grad.numel() == 0:  # no tokens
-                dw = torch.zeros((grad.shape[-1], ctx.shape[-1]), dtype=ctx.types[1], device=grad.device)
-            elif need_dw:
-                dw = matmul(cc, cs, xc, xs, "mxfp8", dtype=ctx.types[1])
-            return dx, dw, None
+            return first_order(linear_backward, ctx, grad)
+
+    def swiglu_backward(ctx, grad):
+        kept, = ctx.saved_tensors
+        g, rows, cols, size = grad.contiguous(), ctx.rows, ctx.cols, grad.element_size()
+        if ctx.packed:
+            dgate, dup, ld = torch.empty((*g.shape[:-1], 2 * cols), dtype=g.dtype, device=g.device), None, 2 * cols
+            pg, pu = dgate.data_ptr(), dgate.data_ptr() + cols * size
+        else:
+            dgate, dup, ld = torch.empty_like(g), torch.empty_like(g), cols
+            pg, pu = dgate.data_ptr(), dup.data_ptr()
+        gc, gs, uc, us = _checkpoint(kept, rows, cols)
+        _check(mxq_swiglu_backward(g.data_ptr(), _dt(g), gc, gs, uc, us, rows, cols, pg, pu, ld, _raw_stream(g)),
+               "mxq_swiglu_backward")
+        return dgate, dup
 
     class Swiglu(torch.autograd.Function):
         @staticmethod
@@ -276,42 +395,28 @@ def _functions():
                 x, ld = gate.contiguous(), 2 * cols
                 pg, pu = x.data_ptr(), x.data_ptr() + cols * x.element_size()
                 rows = x.numel() // (2 * cols)
-                shape = (*gate.shape[:-1], cols)
+                out = torch.empty((*gate.shape[:-1], cols), dtype=gate.dtype, device=gate.device)
             else:
-                cols, shape = gate.shape[-1], gate.shape
+                cols = gate.shape[-1]
                 ld = _row_stride(gate)
                 if ld is None or _row_stride(up) != ld:
                     gate, up, ld = gate.contiguous(), up.contiguous(), cols
                 pg, pu = gate.data_ptr(), up.data_ptr()
                 rows = gate.numel() // cols
-            dt = _dt(gate)
-            out = torch.empty(shape, dtype=gate.dtype, device=gate.device)
-            keep = [None] * 4
-            if any(ctx.needs_input_grad):
-                for i in (0, 2):
-                    keep[i] = mxq.empty_codes("mxfp8", rows, cols, gate.device)
-                    keep[i + 1] = mxq.empty_scales("mxfp8", rows, cols, gate.device)
-            _check(mxq_swiglu_forward(pg, pu, dt, rows, cols, ld, out.data_ptr(),
-                                      *(None if t is None else t.data_ptr() for t in keep), _stream(None)),
+                out = torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
+            kept, parts = None, (None,) * 4
+            if ctx.needs_input_grad[0] or ctx.needs_input_grad[1]:
+                kept = _bytes(rows * cols // 32 * 66, gate)
+                parts = _checkpoint(kept, rows, cols)
+            _check(mxq_swiglu_forward(pg, pu, _dt(gate), rows, cols, ld, out.data_ptr(), *parts, _raw_stream(gate)),
                    "mxq_swiglu_forward")
-            ctx.save_for_backward(*keep)
+            ctx.save_for_backward(kept)
             ctx.packed, ctx.rows, ctx.cols = packed, rows, cols
             return out
 
         @staticmethod
-        @once_differentiable
         def backward(ctx, grad):
-            keep = ctx.saved_tensors
-            g, cols, size = grad.contiguous(), ctx.cols, grad.element_size()
-            if ctx.packed:
-                dgate, dup, ld = torch.empty((*g.shape[:-1], 2 * cols), dtype=g.dtype, device=g.device), None, 2 * cols
-                pg, pu = dgate.data_ptr(), dgate.data_ptr() + cols * size
-            else:
-                dgate, dup, ld = torch.empty_like(g), torch.empty_like(g), cols
-                pg, pu = dgate.data_ptr(), dup.data_ptr()
-            _check(mxq_swiglu_backward(g.data_ptr(), _dt(g), *(t.data_ptr() for t in keep), ctx.rows, cols, pg, pu, ld,
-                                       _stream(None)), "mxq_swiglu_backward")
-            return dgate, dup
+            return first_order(swiglu_backward, ctx, grad)
 
     LinearSTE, SwiGLU = Linear, Swiglu
 
@@ -445,7 +550,7 @@ def kv_append(k, v, cache, slots, stream=None):
         raise ValueError("k and v must have one shape and dtype")
     _ints(slots, _torch().int64, "slots", k.shape[0])
     _check(mxq_kv_append(cache._raw(), k.data_ptr(), ks, v.data_ptr(), vs, _dt(k), k.shape[0], slots.data_ptr(),
-                         _stream(stream)), "mxq_kv_append")
+                         _raw_stream(k) if stream is None else stream.cuda_stream), "mxq_kv_append")
 
 
 def kv_read(cache, slots, dtype=None, stream=None):
@@ -458,7 +563,7 @@ def kv_read(cache, slots, dtype=None, stream=None):
         k, v = (torch.empty((slots.numel(), cache.kv_heads, cache.head_dim), dtype=dtype or torch.bfloat16,
                             device=cache.device) for _ in range(2))
         _check(mxq_kv_read(cache._raw(), slots.data_ptr(), slots.numel(), k.data_ptr(), v.data_ptr(), _dt(k),
-                           _stream(None)), "mxq_kv_read")
+                           _raw_stream(slots)), "mxq_kv_read")
         return k, v
 
     return _on(stream, call)
@@ -471,12 +576,12 @@ def kv_attention(q, cache, block_table, seq_lens, q_starts=None, max_q=None, sca
     q            [rows, heads, head_dim] (row and head strides free, multiples of 8); heads a multiple of kv_heads
     block_table  int32 [batch, pages]: page of keys page_size * i .. of a sequence
     seq_lens     int32 [batch]: keys of each sequence, the new tokens' among them
-    q_starts     int32 [batch + 1]: sequence b's queries are rows q_starts[b] .. q_starts[b + 1], at most max_q (default:
-                 rows); None: rows / batch queries each
+    q_starts     int32 [batch + 1]: sequence b's queries are rows q_starts[b] .. q_starts[b + 1] (starts do not
+                 decrease), at most max_q of them (default: rows); None: rows / batch queries each
     scale        of the scores (default head_dim ** -0.5); window: keys a query sees at most (0: all)
     max_keys     an upper bound of seq_lens, if known, for a better split of the work (longer sequences are cut)
     Returns out [rows, heads, head_dim]; with lse=True (out, log-sum-exp fp32 [rows, heads]). A query that sees no key
-    gives 0 (and -inf). Rows of no sequence are 0, or left as they are in a given `out`."""
+    gives 0 (and -inf), and so do rows of no sequence and queries beyond max_q, which a given `out` keeps."""
     torch = _torch()
     _on_gpu(q, "q")
     if q.dim() != 3 or q.shape[2] != cache.head_dim or q.dtype != torch.bfloat16:
@@ -511,21 +616,27 @@ def kv_attention(q, cache, block_table, seq_lens, q_starts=None, max_q=None, sca
     def call():
         o = out
         if o is None:
-            o = (torch.empty if q_starts is None else torch.zeros)((rows, heads, d), dtype=q.dtype, device=q.device)
+            o = torch.empty((rows, heads, d), dtype=q.dtype, device=q.device)
+            if batch == 0 or max_q == 0:
+                o.zero_()
         elif o.shape != q.shape or o.dtype != q.dtype:
             raise ValueError(f"out must be {q.dtype} {tuple(q.shape)}")
         _on_gpu(o, "out")
         _fits(o, 0, "out")
-        s = torch.full((rows, heads), -math.inf, dtype=torch.float32, device=q.device) if lse else None
+        s = None
+        if lse and (out is not None or batch == 0 or max_q == 0):
+            s = torch.full((rows, heads), -math.inf, dtype=torch.float32, device=q.device)
+        elif lse:
+            s = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
         raw = cache._raw()
         need = mxq_kv_attention_workspace_bytes(raw, batch, rows, max_q, heads, max_keys)
         ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
         _check(mxq_kv_attention(raw, q.data_ptr(), rows, q.stride(0) if rows > 1 else 0, q.stride(1) if heads > 1 else 0,
                                 heads, batch, None if q_starts is None else q_starts.data_ptr(), max_q,
                                 seq_lens.data_ptr(), max_keys, block_table.data_ptr(), block_table.shape[1],
-                                d ** -0.5 if scale is None else scale, window, o.data_ptr(),
+                                d ** -0.5 if scale is None else scale, window, out is None, o.data_ptr(),
                                 None if s is None else s.data_ptr(), None if ws is None else ws.data_ptr(), need,
-                                _stream(None)), "mxq_kv_attention")
+                                _raw_stream(q)), "mxq_kv_attention")
         return (o, s) if lse else o
 
     return _on(stream, call)

@@ -57,6 +57,19 @@ MXQ_API mxq_status mxq_quantize_both(mxq_format row_fmt, mxq_format col_fmt, con
                                      void* col_scales, mxq_stream stream);
 
 /*
+ * Linear layer on a converted weight: x [m, k] of type dtype rounded to fmt along
+ * its rows (as mxq_quantize_mma), times b [n, k] (as mxq_matmul):
+ *   out [m, n] of type dtype.
+ * workspace: mxq_linear_workspace_bytes(fmt, m, k) bytes, 16-byte aligned, for x's
+ * codes and scales; used by this call alone until it has finished. Other rules
+ * and errors as mxq_quantize_mma and mxq_matmul.
+ */
+MXQ_API size_t mxq_linear_workspace_bytes(mxq_format fmt, int64_t m, int64_t k);
+MXQ_API mxq_status mxq_linear(mxq_format fmt, const void* x, mxq_dtype dtype, int64_t m, int64_t k,
+                              const void* b_codes, const void* b_scales, int64_t n, void* out, void* workspace,
+                              size_t workspace_bytes, mxq_stream stream);
+
+/*
  * out = silu(gate) * up, with gate and up kept as MXFP8 E4M3 checkpoints (as
  * mxq_quantize writes them: codes [rows, cols], scales [rows, cols/32]):
  *   out[i, j] = g * sigmoid(g) * u, computed in fp32 from the unrounded inputs.
@@ -135,9 +148,10 @@ MXQ_API mxq_status mxq_kv_read(const mxq_kv_cache* cache, const int64_t* slots, 
  * q head h reads key/value head h / (q_heads / kv_heads). A query that sees no
  * key gives out = 0 and lse = -inf. Keys that a query does not see do not enter
  * it, whatever bytes they hold; a key whose page number is outside [0, pages)
- * is seen by no query. Rows of q outside every sequence's range are left as
- * they are in out and lse; starts are taken as given but clamped to [0, q_rows],
- * and queries of a sequence beyond max_q are not computed.
+ * is seen by no query. Starts do not decrease; each is clamped to [0, q_rows].
+ * Rows of q that belong to no sequence, and queries of a sequence beyond max_q,
+ * are not computed: with fill == 0 they are left as they are in out and lse,
+ * otherwise they get 0 and -inf.
  *   q      row r, head h at r * q_row_stride + h * q_head_stride (values; strides
  *          multiples of 8, q 16-byte aligned); out [q_rows, q_heads, head_dim]
  *          bf16 contiguous, 16-byte aligned; lse fp32 [q_rows, q_heads] or NULL.
@@ -155,7 +169,7 @@ MXQ_API mxq_status mxq_kv_attention(const mxq_kv_cache* cache, const void* q, in
                                     int64_t q_head_stride, int32_t q_heads, int64_t batch, const int32_t* q_starts,
                                     int32_t max_q, const int32_t* seq_lens, int64_t max_keys,
                                     const int32_t* block_table, int64_t table_stride, float scale, int32_t window,
-                                    void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                    int32_t fill, void* out, float* lse, void* workspace, size_t workspace_bytes,
                                     mxq_stream stream);
 
 #ifdef __cplusplus

@@ -306,6 +306,9 @@ def test_rows_of_no_sequence_stay_and_starts_are_clamped():
     assert torch.equal(out[1:5], ops.kv_attention(q[1:5], c, table, dev(lens)))
     wild = ops.kv_attention(q, c, table, dev(lens), q_starts=dev([-100, 4, 1 << 30]), max_q=9)
     assert torch.equal(wild, ops.kv_attention(q, c, table, dev(lens), q_starts=dev([0, 4, 9]), max_q=9))
+    # before the first sequence and behind the last: zeros in a fresh output
+    fresh, lse = ops.kv_attention(q, c, table, dev(lens), q_starts=dev([1, 3, 5]), max_q=2, lse=True)
+    assert torch.equal(fresh[1:5], out[1:5]) and (fresh[~mine] == 0).all() and (lse[~mine] == -math.inf).all()
     # queries beyond max_q are left out; the others keep their positions
     part = ops.kv_attention(q, c, table, dev(lens), q_starts=dev([0, 4, 9]), max_q=3)
     full = ops.kv_attention(q, c, table, dev(lens), q_starts=dev([0, 4, 9]), max_q=5)
@@ -354,7 +357,7 @@ def test_no_queries_and_errors():
     raw, st = c._raw(), torch.cuda.current_stream().cuda_stream
     out = torch.empty_like(q)
     call = lambda o, ws=None, n=0, keys=32, t=table, qq=q: ops.mxq_kv_attention(  # noqa: E731
-        raw, qq.data_ptr(), 2, 256, 64, 4, 2, None, 1, lens.data_ptr(), keys, t.data_ptr(), t.shape[1], 1.0, 0, o, None, ws, n, st)
+        raw, qq.data_ptr(), 2, 256, 64, 4, 2, None, 1, lens.data_ptr(), keys, t.data_ptr(), t.shape[1], 1.0, 0, 0, o, None, ws, n, st)
     assert call(out.data_ptr()) == 0
     assert call(q.data_ptr()) == 1                       # out over q
     assert call(c.v_codes.data_ptr()) == 1               # out over the cache

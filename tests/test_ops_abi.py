@@ -78,6 +78,13 @@ def test_product_statuses_before_any_cuda_call():
     assert mm(FP8, None, None, None, None, 0, 5, 32, None, BF16, None) == 0     # empty
     assert mm(FP8, None, None, None, None, 5, 0, 32, None, BF16, None) == 0
     assert mm(FP8, None, None, None, None, 5, 5, 32, None, BF16, None) == 1     # null
+    li = lambda fmt=FP4, m=4, n=4, k=32, dt=BF16: ops.mxq_linear(fmt, None, dt, m, k, None, None, n, None, None, 0, None)  # noqa: E731
+    assert [li(fmt=1), li(fmt=9), li(k=40), li(m=-1), li(dt=2), li(m=0), li(n=0), li()] == [4, 1, 2, 2, 1, 0, 0, 1]
+    assert ops.mxq_linear_workspace_bytes(FP4, 5, 64) == 5 * 32 + mxq.mxq_mma_scales_bytes(5, 64)
+    assert ops.mxq_linear_workspace_bytes(FP8, 130, 96) == 130 * 96 + mxq.mxq_mma_scales_bytes(130, 96)
+    assert [ops.mxq_linear_workspace_bytes(f, 5, k) for f, k in ((1, 64), (9, 64), (FP4, 40))] == [0, 0, 0]
+    for rows, cols in ((1, 32), (5, 64), (128, 128), (130, 96), (257, 4128)):
+        assert ops._operand_bytes("mxfp4", rows, cols) == ops.mxq_linear_workspace_bytes(FP4, rows, cols)
     qb = ops.mxq_quantize_both
     assert qb(FP4, FP8, None, BF16, 5, 48, None, None, None, None, None) == 2
     assert qb(FP4, FP8, None, BF16, 5, 64, None, None, None, None, None) == 1   # neither direction
@@ -126,7 +133,7 @@ def test_cache_statuses_before_any_cuda_call():
     assert ap(cache(), ks=120) == 2            # stride below a token
     assert ap(cache(), vs=132) == 3            # misaligned stride
     at = lambda c=cache(), rows=2, rs=512, hs=64, heads=4, batch=2, starts=None, mq=1, ts=4, win=0, keys=64: ops.mxq_kv_attention(  # noqa: E731
-        c, None, rows, rs, hs, heads, batch, starts, mq, None, keys, None, ts, 1.0, win, None, None, None, 0, None)
+        c, None, rows, rs, hs, heads, batch, starts, mq, None, keys, None, ts, 1.0, win, 0, None, None, None, 0, None)
     assert at(cache(dim=32)) == 4
     assert at(heads=3) == 2
     assert at(heads=0) == 2

@@ -86,6 +86,14 @@ def test_linear_ste_without_tokens():
     assert dx.shape == (0, 64) and (dw == 0).all() and dw.shape == w.shape
 
 
+def test_a_second_derivative_is_refused():
+    x, w = values(1, 4, 64).requires_grad_(), values(2, 32, 64).requires_grad_()
+    for y in (ops.linear_ste(x, w), ops.swiglu(x)):
+        d, = torch.autograd.grad(y.sum(), x, create_graph=True)
+        with pytest.raises(RuntimeError):
+            d.sum().backward()
+
+
 def test_linear_ste_keeps_33_64ths_of_the_input():
     x, w = values(1, 4096, 2560).requires_grad_(), values(2, 32, 2560).requires_grad_()
     kept = []
