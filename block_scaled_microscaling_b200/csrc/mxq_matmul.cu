@@ -6,14 +6,18 @@
 // tcgen05.mma takes the codes as they are stored and the E8M0 scales from tensor memory, so nothing is
 // decoded: kind::mxf4 multiplies 64 values of k per instruction (two scales per row), kind::mxf8f6f4 32 (one).
 //
-// One CTA computes tiles of 128 rows of X by BN rows of Y, (X, Y) = (a, b), or (b, a) when a has at most 128
-// rows: then the weight fills the instruction's 128 rows and the few tokens its narrow side, and the tile is
-// written transposed. Three roles: a producer thread fills a ring of stages (TMA boxes of 128-byte rows with
-// the 128-byte swizzle; the scales of 128 rows are whole 512-byte tiles in memory, plain bulk copies), one
-// thread copies a stage's scale tiles to tensor memory and issues its four MMAs, four warps bring the fp32
-// accumulators from tensor memory to `out`. Where the tiles leave SMs idle, the CTAs of a cluster share a
-// tile's k range and add their partial tiles through distributed shared memory in rank order: no workspace, no
-// atomics, the same bits on every call.
+// Three roles: a producer warp fills a ring of stages (TMA boxes of 128-byte rows with the 128-byte swizzle; the
+// scales of 128 rows are whole 512-byte tiles in memory), a second warp copies a stage's scale tiles to tensor
+// memory and issues its four MMAs, eight warps bring the fp32 accumulators from tensor memory to `out`. Both
+// issuing warps run converged with one elected thread, on operands that are uniform over the warp: with the whole
+// loop under one lane and descriptors built per instruction, issuing took longer than the MMAs (8192 x 9728 x 2560
+// MXFP8 177 us, now 153).
+// - Large products: a pair of CTAs computes 256 x 256 of out (k_matmul_pair).
+// - Others: a CTA computes 128 rows of X by up to 128 rows of Y, (X, Y) = (a, b), or (b, a) when a has at most 128
+//   rows: then the weight fills the instruction's 128 rows, the few tokens its narrow side, in steps of 16, and the
+//   tile is written transposed. Two CTAs fit an SM. Where the tiles leave SMs idle, the CTAs of a cluster share a
+//   tile's k range and add their partial tiles through distributed shared memory in rank order: no workspace, no
+//   atomics, the same bits on every call.
 //
 // Every wait on an mbarrier is bounded; after a timeout every role leaves, copies and MMAs in flight are waited
 // for (bounded too) and tensor memory is freed.
@@ -33,7 +37,7 @@
 namespace mxq {
 namespace {
 
-constexpr int kMmThreads = 192;  // producer warp, MMA warp, four epilogue warps
+constexpr int kMmThreads = 320;  // producer warp, MMA warp, eight epilogue warps
 constexpr int kMmRows = 128;     // rows of X per tile
 constexpr int kMmSplitMax = 8;   // portable cluster size
 
@@ -42,20 +46,40 @@ template <int F> struct MmFmt;
 template <> struct MmFmt<F_E2M1> { static constexpr int VALS = 256, KI = 64, TS = 2; };
 template <> struct MmFmt<F_E4M3> { static constexpr int VALS = 128, KI = 32, TS = 1; };
 
-template <int F, int BN> struct MmCfg {
+// a tile of 128 x bn, bn <= 128 and a multiple of 16
+template <int F> struct MmCfg {
     static constexpr int TS = MmFmt<F>::TS;
-    static constexpr int NB = (BN + 127) / 128;  // scale tiles along Y's rows
-    static constexpr int A_BYTES = kMmRows * 128, B_BYTES = BN * 128;
-    static constexpr int SFA = A_BYTES + B_BYTES, SFB = SFA + TS * 512;
-    static constexpr int STAGE = (SFB + NB * TS * 512 + 1023) / 1024 * 1024;
-    static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-    static constexpr int SMEM = STAGES * STAGE + 1024;  // + alignment slack
-    // tensor memory: BN accumulator columns, then two buffers of scale columns (a stage's copies never write
-    // the buffer that the stage before reads)
-    static constexpr int SF_COLS = TS * 4 * (1 + NB);
-    static constexpr int COLS = BN + 2 * SF_COLS;
-    static constexpr int ALLOC = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-    static_assert(SMEM <= 227 * 1024 && BN * kMmRows * 4 <= STAGES * STAGE, "the stages fit, and the partial tile in them");
+    static constexpr int A_BYTES = kMmRows * 128;
+    static constexpr int SF_BYTES = 2 * TS * 512;  // X's scale tiles, then Y's
+    static constexpr int MAX_STAGES = 8;
+    __host__ __device__ static constexpr int stage_bytes(int bn) { return A_BYTES + bn * 128 + (SF_BYTES + 1023) / 1024 * 1024; }
+    // as many stages as fit the SM, or half of it
+    static constexpr int stages(int bn, bool two) {
+        const int n = ((two ? 112 : 224) * 1024 - 1024) / stage_bytes(bn);
+        return n < MAX_STAGES ? n : MAX_STAGES;
+    }
+    static int smem(int bn, int stages) {
+        const int ring = stages * stage_bytes(bn), part = bn * kMmRows * 4;  // the partial tile takes the stages' place
+        return (ring > part ? ring : part) + 1024;                           // + alignment slack
+    }
+    // tensor memory: 128 accumulator columns, then two buffers of scale columns (a stage's copies never write the
+    // buffer that the stage before reads)
+    static constexpr int SF_COLS = TS * 4 * 2;
+    static constexpr int ALLOC = 256;
+    static_assert(128 + 2 * SF_COLS <= ALLOC && stages(128, true) >= 3, "tensor memory of two CTAs, a ring of three stages");
+};
+
+// position in a ring of n stages: stage and the parity of its current use (counters, since one thread's divisions
+// by a stage count that is no power of two took longer than a stage's MMAs)
+struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++s == n) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
 };
 
 struct MmArgs {
@@ -67,6 +91,7 @@ struct MmArgs {
     int kt4;           // scale tiles along k
     int tiles, xtiles; // output tiles; xtiles along X (the fast direction)
     int split;         // CTAs (of one cluster) per tile
+    int bn, stages;    // rows of Y per tile, stages of the ring
     long long ld;      // row length of out
 };
 
@@ -111,27 +136,87 @@ __device__ __forceinline__ void pack_run(const float* v, uint32_t* w) {
     }
 }
 
-template <int F, int BN, bool SWAP, typename T>
-__global__ void __launch_bounds__(kMmThreads, 1)
+// N accumulator columns of the warp's 32 rows (tensor-memory address `mine`) to row x of out, columns y0 ..; calls
+// `release` once all of them are in registers (bf16: rounded), before the first store
+template <typename T, int N, typename R>
+__device__ __forceinline__ void store_rows(uint32_t mine, T* out, long long ld, int x, int rx, int y0, int ry, bool a32, R release) {
+    constexpr int PER = 32 / (int)sizeof(T);  // columns in 32 bytes
+    uint32_t w[N * (int)sizeof(T) / 4];
+#pragma unroll
+    for (int c = 0; c < N; c += 32) {
+        if constexpr (sizeof(T) == 4) {
+            tmem_ld32(mine + c, w + c);
+        } else {
+            uint32_t v[32];
+            tmem_ld32(mine + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[c / 2 + i] = bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+        }
+    }
+    if constexpr (sizeof(T) == 4) tmem_wait_ld();
+    release();
+    T* const row = out + (long long)x * ld + y0;
+    if (x < rx)
+#pragma unroll
+        for (int c = 0; c < N; c += PER)
+            if (y0 + c < ry) store_run<T>(row + c, w + c / PER * 8, ry - y0 - c, a32);
+}
+
+// the partial tiles [bn][128] of S CTAs, at `part` in each, added in rank order: this CTA's share of the columns to
+// out (256 threads: row e % 128, columns in two halves)
+template <int S, bool SWAP, typename T>
+__device__ __forceinline__ void add_parts(uint32_t part, int e, int rank, int bn, int x, int y0, const MmArgs& p, T* out, bool a32) {
+    constexpr int RUN = SWAP ? 2 : 32 / (int)sizeof(T);  // columns at a time
+    const int r = e & 127, per = bn / S;                 // bn is a multiple of 16, S at most 8
+    for (int c = rank * per + (e >> 7) * RUN; c < (rank + 1) * per && y0 + c < p.ry; c += 2 * RUN) {
+        float v[RUN][S], sum[RUN];
+#pragma unroll
+        for (int i = 0; i < RUN; ++i)
+#pragma unroll
+            for (int q = 0; q < S; ++q) v[i][q] = ld_peer_f32(part + 4u * (uint32_t)((c + i) * 128 + r), (uint32_t)q);
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) {
+            sum[i] = v[i][0];
+#pragma unroll
+            for (int q = 1; q < S; ++q) sum[i] += v[i][q];
+        }
+        if (x + r >= p.rx) continue;
+        if constexpr (SWAP) {
+#pragma unroll
+            for (int i = 0; i < RUN; ++i)
+                if (y0 + c + i < p.ry) out[(long long)(y0 + c + i) * p.ld + x + r] = round_to<T>(sum[i]);
+        } else {
+            uint32_t w[8];
+            pack_run<T>(sum, w);
+            store_run<T>(out + (long long)(x + r) * p.ld + y0 + c, w, p.ry - y0 - c, a32);
+        }
+    }
+}
+
+template <int F, bool SWAP, typename T>
+__global__ void __launch_bounds__(kMmThreads, 2)
     k_matmul(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my, const MmArgs p, unsigned int* err) {
-    using C = MmCfg<F, BN>;
+    using C = MmCfg<F>;
     using FM = MmFmt<F>;
-    constexpr int ST = C::STAGES;
+    constexpr int MS = C::MAX_STAGES;
+    const int bn = SWAP ? p.bn : 128, ST = p.stages, STAGE = C::stage_bytes(bn);
+    const uint32_t sf_at = C::A_BYTES + bn * 128;  // X's scale tiles in a stage
     extern __shared__ uint8_t dsm[];
     uint8_t* const stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) unsigned long long bars[2 * ST + 3];  // full[ST], empty[ST], acc full, acc empty, drained
+    __shared__ __align__(8) unsigned long long bars[2 * MS + 3];  // full[MS], empty[MS], acc full, acc empty, drained
     __shared__ uint32_t tmem_addr;
     __shared__ int abort_flag;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const uint32_t s0 = smem_u32(stages);
     auto full = [&](int s) { return smem_u32(&bars[s]); };
-    auto empty = [&](int s) { return smem_u32(&bars[ST + s]); };
-    const uint32_t acc_full = smem_u32(&bars[2 * ST]), acc_empty = smem_u32(&bars[2 * ST + 1]),
-                   drained = smem_u32(&bars[2 * ST + 2]);
+    auto empty = [&](int s) { return smem_u32(&bars[MS + s]); };
+    const uint32_t acc_full = smem_u32(&bars[2 * MS]), acc_empty = smem_u32(&bars[2 * MS + 1]),
+                   drained = smem_u32(&bars[2 * MS + 2]);
     if (t == 0) {
-        for (int s = 0; s < 2 * ST; ++s) mbar_init(full(s), 1);
+        for (int s = 0; s < 2 * MS; ++s) mbar_init(full(s), 1);
         mbar_init(acc_full, 1);
-        mbar_init(acc_empty, 4);
+        mbar_init(acc_empty, 8);
         mbar_init(drained, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -153,87 +238,83 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const int tile0 = blockIdx.x / p.split, tile_step = gridDim.x / p.split;  // split > 1: one tile per cluster
 
     if (warp == 0) {
-        if (lane == 0) {
-            long long n = 0;  // stages issued
-            bool ok = true;
-            for (int tile = tile0; ok && tile < p.tiles; tile += tile_step) {
-                const int xt = tile % p.xtiles, yt = tile / p.xtiles;
-                for (int ks = ks0; ks < ks1; ++ks, ++n) {
-                    const int s = (int)(n % ST);
-                    if (n >= ST && !mbar_wait(empty(s), (uint32_t)((n / ST - 1) & 1), ab, err)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t base = s0 + s * C::STAGE;
-                    const int c0 = ks * FM::TS;
-                    const uint32_t sf = (uint32_t)min(FM::TS, p.kt4 - c0) * 512u;
-                    int nb = (p.ry + 127) / 128 - yt * BN / 128;  // Y's scale tiles that exist
-                    nb = nb < C::NB ? nb : C::NB;
-                    mbar_expect_tx(full(s), C::A_BYTES + C::B_BYTES + sf * (1 + nb));
-                    tma_box(base, &mx, ks * 128, xt * kMmRows, full(s));
-                    tma_box(base + C::A_BYTES, &my, ks * 128, yt * BN, full(s));
-                    bulk_get(base + C::SFA, p.sx + ((long long)xt * p.kt4 + c0) * 512, sf, full(s));
-                    for (int i = 0; i < nb; ++i)
-                        bulk_get(base + C::SFB + i * FM::TS * 512, p.sy + ((long long)(yt * BN / 128 + i) * p.kt4 + c0) * 512, sf,
-                                 full(s));
+        const bool one = elect_one();
+        Ring at;
+        long long n = 0;  // stages issued
+        bool ok = true;
+        for (int tile = tile0; ok && tile < p.tiles; tile += tile_step) {
+            const int xt = tile % p.xtiles, yt = tile / p.xtiles;
+            const uint8_t* const sx = p.sx + (long long)xt * p.kt4 * 512;
+            const uint8_t* const sy = p.sy + (long long)yt * p.kt4 * 512;  // bn < 128: one tile of Y
+            for (int ks = ks0; ks < ks1; ++ks, ++n, at.next(ST)) {
+                if (n >= ST && !mbar_wait(empty(at.s), at.phase ^ 1u, ab, err)) {
+                    ok = false;
+                    break;
                 }
+                if (!one) continue;
+                const uint32_t base = s0 + at.s * STAGE, bar = full(at.s);
+                const int c0 = ks * FM::TS;
+                const uint32_t sf = (uint32_t)min(FM::TS, p.kt4 - c0) * 512u;
+                mbar_expect_tx(bar, C::A_BYTES + bn * 128 + 2 * sf);
+                tma_box(base, &mx, ks * 128, xt * kMmRows, bar);
+                tma_box(base + C::A_BYTES, &my, ks * 128, yt * bn, bar);
+                bulk_get(base + sf_at, sx + (long long)c0 * 512, sf, bar);
+                bulk_get(base + sf_at + FM::TS * 512, sy + (long long)c0 * 512, sf, bar);
             }
-            // after a timeout: copies in flight land before shared memory goes away
-            if (*ab)
-                for (long long q = n > ST ? n - ST : 0; q < n; ++q) {
-                    const unsigned long long t0 = global_ns();
-                    while (!mbar_test(full((int)(q % ST)), (uint32_t)(q / ST) & 1u) && global_ns() - t0 < kWaitLimitNs) {
-                    }
-                }
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_block_scaled<F>(kMmRows, BN);
-            long long n = 0;
-            int it = 0;
-            bool ok = true;
-            for (int tile = tile0; ok && tile < p.tiles; tile += tile_step, ++it) {
-                if (it > 0 && !mbar_wait(acc_empty, (uint32_t)(it - 1) & 1u, ab, err)) break;
-                tc_fence_after();
-                for (int ks = ks0; ks < ks1; ++ks, ++n) {
-                    const int s = (int)(n % ST);
-                    if (!mbar_wait(full(s), (uint32_t)(n / ST) & 1u, ab, err)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t base = s0 + s * C::STAGE;
-                    const uint32_t sfa = acc + BN + (uint32_t)(n & 1) * C::SF_COLS, sfb = sfa + FM::TS * 4;
-#pragma unroll
-                    for (int c = 0; c < FM::TS; ++c) {
-                        tc_copy_scales(sfa + 4 * c, desc_scales(base + C::SFA + c * 512));
-#pragma unroll
-                        for (int i = 0; i < C::NB; ++i)
-                            tc_copy_scales(sfb + 4 * (c * C::NB + i), desc_scales(base + C::SFB + (i * FM::TS + c) * 512));
-                    }
-                    const int left = p.k - ks * FM::VALS;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (j * FM::KI < left) {
-                            const int c = F == F_E2M1 ? j >> 1 : 0;                          // scale tile
-                            const uint32_t id = F == F_E2M1 ? 2u * (j & 1) : (uint32_t)j;    // first byte of its columns
-                            tc_mma_block_scaled<F>(acc, desc_sw128(base + 32 * j), desc_sw128(base + C::A_BYTES + 32 * j),
-                                                   idesc | (id << 4) | (id << 29), sfa + 4 * c, sfb + 4 * c * C::NB,
-                                                   ks > ks0 || j > 0);
-                        }
-                    tc_commit(empty(s));
-                }
-                if (ok) tc_commit(acc_full);
-            }
-            if (*ab) {  // MMAs in flight end before their shared and tensor memory goes away
-                tc_commit(drained);
+        // after a timeout: copies in flight land before shared memory goes away
+        if (one && *ab)
+            for (long long q = n > ST ? n - ST : 0; q < n; ++q) {
                 const unsigned long long t0 = global_ns();
-                while (!mbar_test(drained, 0) && global_ns() - t0 < kWaitLimitNs) {
+                while (!mbar_test(full((int)(q % ST)), (uint32_t)(q / ST) & 1u) && global_ns() - t0 < kWaitLimitNs) {
                 }
+            }
+    } else if (warp == 1) {
+        const bool one = elect_one();
+        const uint32_t idesc = idesc_block_scaled<F>(kMmRows, bn);
+        const SmemDesc dop = desc_sw128(s0), dsf = desc_scales(s0);
+        Ring at;
+        uint32_t odd = 0;
+        int it = 0;
+        bool ok = true;
+        for (int tile = tile0; ok && tile < p.tiles; tile += tile_step, ++it) {
+            if (it > 0 && !mbar_wait(acc_empty, (uint32_t)(it - 1) & 1u, ab, err)) break;
+            tc_fence_after();
+            for (int ks = ks0; ks < ks1; ++ks, at.next(ST), odd ^= 1u) {
+                if (!mbar_wait(full(at.s), at.phase, ab, err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (!one) continue;
+                const uint32_t step = at.s * STAGE;
+                const uint32_t sfa = acc + 128 + odd * C::SF_COLS, sfb = sfa + FM::TS * 4;
+#pragma unroll
+                for (int c = 0; c < FM::TS; ++c) {
+                    tc_copy_scales(sfa + 4 * c, dsf + (step + sf_at + c * 512));
+                    tc_copy_scales(sfb + 4 * c, dsf + (step + sf_at + (FM::TS + c) * 512));
+                }
+                const int left = p.k - ks * FM::VALS;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j * FM::KI < left) {
+                        const int c = F == F_E2M1 ? j >> 1 : 0;                        // scale tile
+                        const uint32_t id = F == F_E2M1 ? 2u * (j & 1) : (uint32_t)j;  // first byte of its columns
+                        tc_mma_block_scaled<F>(acc, dop + (step + 32 * j), dop + (step + C::A_BYTES + 32 * j),
+                                               idesc | (id << 4) | (id << 29), sfa + 4 * c, sfb + 4 * c, ks > ks0 || j > 0);
+                    }
+                tc_commit(empty(at.s));
+            }
+            if (ok && one) tc_commit(acc_full);
+        }
+        if (one && *ab) {  // MMAs in flight end before their shared and tensor memory goes away
+            tc_commit(drained);
+            const unsigned long long t0 = global_ns();
+            while (!mbar_test(drained, 0) && global_ns() - t0 < kWaitLimitNs) {
             }
         }
     } else {
-        const int quad = warp & 3;  // the warp's lanes of tensor memory
+        const int quad = warp & 3, half = (warp - 2) >> 2;  // the warp's lanes of tensor memory, its part of the columns
         const uint32_t mine = acc + ((uint32_t)(quad * 32) << 16);
         T* const out = static_cast<T*>(p.out);
         const bool a32 = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.ld * (long long)sizeof(T))) & 31) == 0;
@@ -245,12 +326,12 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const int xt = tile % p.xtiles, yt = tile / p.xtiles;
-            const int x = xt * kMmRows + quad * 32 + lane, y0 = yt * BN;
+            const int x = xt * kMmRows + quad * 32 + lane, y0 = yt * bn;
             if (p.split > 1) {
-                // partial tile to shared memory (the stages are consumed), [BN][128]
+                // partial tile to shared memory (the stages are consumed), [bn][128]
                 float* const red = reinterpret_cast<float*>(stages);
 #pragma unroll 1
-                for (int c = 0; c < BN; c += 16) {
+                for (int c = 16 * half; c < bn; c += 32) {
                     uint32_t v[16];
                     tmem_ld16(mine + c, v);
                     tmem_wait_ld();
@@ -259,9 +340,14 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 }
                 break;
             }
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_empty);
+            };
             if constexpr (SWAP) {
 #pragma unroll 1
-                for (int c = 0; c < BN; c += 16) {
+                for (int c = 16 * half; c < bn; c += 32) {
                     uint32_t v[16];
                     tmem_ld16(mine + c, v);
                     tmem_wait_ld();
@@ -270,82 +356,22 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                         for (int i = 0; i < 16; ++i)
                             if (y0 + c + i < p.ry) out[(long long)(y0 + c + i) * p.ld + x] = round_to<T>(__uint_as_float(v[i]));
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(acc_empty);
-            } else if constexpr (sizeof(T) == 2) {
-                // 128 columns at a time to registers, rounded; after the last of them the accumulators are free
-                // for the next tile's MMAs, before the stores
-                T* const row = out + (long long)x * p.ld + y0;
-#pragma unroll 1
-                for (int h = 0; h < BN; h += 128) {
-                    uint32_t w[64];
-#pragma unroll
-                    for (int c = 0; c < 128; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(mine + h + c, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            w[c / 2 + i] = bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                    }
-                    if (h + 128 == BN) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(acc_empty);
-                    }
-                    if (x < p.rx)
-#pragma unroll
-                        for (int c = 0; c < 128; c += 16)
-                            if (y0 + h + c < p.ry) store_run<T>(row + h + c, w + c / 2, p.ry - y0 - h - c, a32);
-                }
+                release();
             } else {
-#pragma unroll 1
-                for (int c = 0; c < BN; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld32(mine + c, v);
-                    tmem_wait_ld();
-                    if (x < p.rx) {
-                        T* const row = out + (long long)x * p.ld + y0 + c;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            if (y0 + c + i < p.ry) store_run<T>(row + i, v + i, p.ry - y0 - c - i, a32);
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(acc_empty);
+                store_rows<T, 64>(mine + half * 64, out, p.ld, x, p.rx, y0 + half * 64, p.ry, a32, release);
             }
         }
     }
     if (p.split > 1) {
-        // each CTA adds its share of the columns over the cluster, in rank order
         __syncwarp();
         cluster_sync();
         if (t >= 64) {
-            const int r = t - 64, xt = tile0 % p.xtiles, y0 = tile0 / p.xtiles * BN, x = xt * kMmRows + r;
+            const int e = t - 64, x = tile0 % p.xtiles * kMmRows, y0 = tile0 / p.xtiles * bn;
             T* const out = static_cast<T*>(p.out);
-            const int per = BN / p.split < 1 ? 1 : BN / p.split;
             const bool a32 = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.ld * (long long)sizeof(T))) & 31) == 0;
-            constexpr int RUN = 32 / (int)sizeof(T);
-            for (int c = rank * per; c < (rank + 1) * per && c < BN && y0 + c < p.ry; c += SWAP ? 1 : RUN) {
-                float v[RUN];
-#pragma unroll
-                for (int i = 0; i < (SWAP ? 1 : RUN); ++i) {
-                    float sum = 0.f;
-                    for (int q = 0; q < p.split; ++q) sum += ld_peer_f32(s0 + 4u * (uint32_t)((c + i) * 128 + r), (uint32_t)q);
-                    v[i] = sum;
-                }
-                if (x < p.rx) {
-                    if constexpr (SWAP) {
-                        out[(long long)(y0 + c) * p.ld + x] = round_to<T>(v[0]);
-                    } else {
-                        uint32_t w[8];
-                        pack_run<T>(v, w);
-                        store_run<T>(out + (long long)x * p.ld + y0 + c, w, p.ry - y0 - c, a32);
-                    }
-                }
-            }
+            if (p.split == 2) add_parts<2, SWAP, T>(s0, e, rank, bn, x, y0, p, out, a32);
+            else if (p.split == 4) add_parts<4, SWAP, T>(s0, e, rank, bn, x, y0, p, out, a32);
+            else add_parts<8, SWAP, T>(s0, e, rank, bn, x, y0, p, out, a32);
         }
         __syncwarp();
         cluster_sync();  // peers have read this CTA's partial tile
@@ -358,8 +384,199 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     }
 }
 
-// tensor map of an operand's codes, [rows, row_bytes]: boxes of box_rows rows x 128 bytes, 128-byte swizzle
-bool encode_codes_map(CUtensorMap* m, const void* base, long long rows, long long row_bytes, int box_rows) {
+// ---- two CTAs on one tile ---------------------------------------------------------------------
+//
+// The CTAs of a pair compute 256 x 256 of out: each stages 128 rows of a and 128 of b, the tensor cores of both
+// read b's rows from both, and each keeps the 128 x 256 accumulators of its rows. A stage moves 32 KB of codes
+// into an SM for the same MMAs that take 48 KB in a tile of 128 x 256; an SM takes about 60 bytes a cycle from L2,
+// so that transfer (0.30 us a stage) and the MMAs (0.27 us) are level. The leader (rank 0) issues the MMAs and owns
+// the barriers that count the stages' bytes; its commits arrive in both CTAs. Eight epilogue warps, so that a tile's
+// accumulators leave tensor memory in one go and the next tile's MMAs start before the stores (four warps: 159 us,
+// eight: 153 at 8192 x 9728 x 2560 MXFP8).
+// Measured, values N(0, 1): 8192 x 9728 x 2560 MXFP8 150 us (2.7 PFLOP/s; one CTA per tile of 128 x 256 163 us),
+// 16384 x 9728 x 2560 MXFP4 165 us (4.9 PFLOP/s; 180 us). The board's power limit bounds them: with all codes zero
+// the same launches take 126 us, and k = 9728 reaches 3.8 (MXFP8) and 7.3 (MXFP4) PFLOP/s.
+template <int F> struct PairCfg {
+    static constexpr int TS = MmFmt<F>::TS;
+    static constexpr int HALF = 128 * 128;  // bytes of 128 staged rows
+    static constexpr int SFA = 2 * HALF, SFB = SFA + TS * 512, BYTES = SFB + 2 * TS * 512;
+    static constexpr int STAGE = (BYTES + 1023) / 1024 * 1024;
+    static constexpr int STAGES = 6;
+    static constexpr int SMEM = STAGES * STAGE + 1024;
+    static constexpr int SF_COLS = TS * 4 * 3;  // a's scales of the CTA's 128 rows, b's of 256
+    static_assert(SMEM <= 227 * 1024 && 256 + 2 * SF_COLS <= 512, "shared and tensor memory");
+};
+
+// 2-D / 3-D boxes into this CTA, their bytes counted on a barrier of the pair (a cluster address)
+__device__ __forceinline__ void pair_box2(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<unsigned long long>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void pair_box3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<unsigned long long>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+template <int F, typename T>
+__global__ void __launch_bounds__(kMmThreads, 1)
+    k_matmul_pair(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+                  const __grid_constant__ CUtensorMap msa, const __grid_constant__ CUtensorMap msb, const MmArgs p,
+                  unsigned int* err) {
+    using C = PairCfg<F>;
+    using FM = MmFmt<F>;
+    constexpr int ST = C::STAGES;
+    extern __shared__ uint8_t dsm[];
+    uint8_t* const stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) unsigned long long bars[2 * ST + 3];  // full[ST], empty[ST], acc full, acc empty, drained
+    __shared__ uint32_t tmem_addr;
+    __shared__ int abort_flag;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const uint32_t rank = cluster_rank(), s0 = smem_u32(stages);
+    auto full = [&](int s) { return smem_u32(&bars[s]); };          // the leader's counts both CTAs' bytes
+    auto empty = [&](int s) { return smem_u32(&bars[ST + s]); };
+    const uint32_t acc_full = smem_u32(&bars[2 * ST]), acc_empty = smem_u32(&bars[2 * ST + 1]),
+                   drained = smem_u32(&bars[2 * ST + 2]);
+    if (t == 0) {
+        for (int s = 0; s < 2 * ST; ++s) mbar_init(full(s), 1);
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 16);  // the epilogue warps of both CTAs
+        mbar_init(drained, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        tmem_alloc<512, true>(smem_u32(&tmem_addr));
+        tc_fence_before();
+    }
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before either signals the other
+    tc_fence_after();
+    const uint32_t acc = tmem_addr;
+    volatile int* ab = &abort_flag;
+    pdl_wait_then_release();
+
+    const int nks = (p.k + FM::VALS - 1) / FM::VALS;
+    const int tile0 = blockIdx.x >> 1, tile_step = gridDim.x >> 1;
+
+    if (warp == 0) {
+        {
+            const bool one = elect_one();
+            Ring at;
+            long long n = 0;  // stages issued
+            bool ok = true;
+            const uint32_t full0 = peer_addr(full(0), 0);
+            for (int tile = tile0; ok && tile < p.tiles; tile += tile_step) {
+                const int xt = tile % p.xtiles, yt = tile / p.xtiles;
+                for (int ks = 0; ks < nks; ++ks, ++n, at.next(ST)) {
+                    const int s = at.s;
+                    if (n >= ST && !mbar_wait<true>(empty(s), at.phase ^ 1u, ab, err)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t base = s0 + s * C::STAGE, bar = full0 + 8u * (uint32_t)s;
+                    if (!one) continue;
+                    if (rank == 0) mbar_expect_tx(full(s), 2 * C::BYTES);
+                    pair_box2(base, &ma, ks * 128, xt * 256 + (int)rank * 128, bar);
+                    pair_box2(base + C::HALF, &mb, ks * 128, yt * 256 + (int)rank * 128, bar);
+                    pair_box3(base + C::SFA, &msa, 0, ks * FM::TS, xt * 2 + (int)rank, bar);
+                    pair_box3(base + C::SFB, &msb, 0, ks * FM::TS, yt * 2, bar);
+                }
+            }
+            if (one && *ab) {  // after a timeout: copies in flight land before shared memory goes away
+                const unsigned long long t0 = global_ns();
+                if (rank == 0)
+                    for (long long q = n > ST ? n - ST : 0; q < n; ++q)
+                        while (!mbar_test(full((int)(q % ST)), (uint32_t)(q / ST) & 1u) && global_ns() - t0 < kWaitLimitNs) {
+                        }
+                else  // their bytes are counted in the leader: give them time
+                    while (global_ns() - t0 < kWaitLimitNs / 100) {
+                    }
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const bool one = elect_one();
+            constexpr uint32_t idesc = idesc_block_scaled<F>(256, 256);
+            Ring at;
+            const SmemDesc dop = desc_sw128(s0), dsf = desc_scales(s0);
+            uint32_t odd = 0;
+            int it = 0;
+            bool ok = true;
+            for (int tile = tile0; ok && tile < p.tiles; tile += tile_step, ++it) {
+                if (it > 0 && !mbar_wait<true>(acc_empty, (uint32_t)(it - 1) & 1u, ab, err)) break;
+                tc_fence_after();
+                for (int ks = 0; ks < nks; ++ks, at.next(ST), odd ^= 1u) {
+                    const int s = at.s;
+                    if (!mbar_wait<true>(full(s), at.phase, ab, err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (!one) continue;
+                    const uint32_t step = s * C::STAGE;
+                    const uint32_t sfa = acc + 256 + odd * C::SF_COLS, sfb = sfa + FM::TS * 4;
+#pragma unroll
+                    for (int c = 0; c < FM::TS; ++c) {
+                        tc_copy_scales<true>(sfa + 4 * c, dsf + (step + C::SFA + c * 512));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            tc_copy_scales<true>(sfb + 4 * (c * 2 + i), dsf + (step + C::SFB + (i * FM::TS + c) * 512));
+                    }
+                    const int left = p.k - ks * FM::VALS;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j * FM::KI < left) {
+                            const int c = F == F_E2M1 ? j >> 1 : 0;
+                            const uint32_t id = F == F_E2M1 ? 2u * (j & 1) : (uint32_t)j;
+                            tc_mma_block_scaled<F, true>(acc, dop + (step + 32 * j), dop + (step + C::HALF + 32 * j),
+                                                         idesc | (id << 4) | (id << 29), sfa + 4 * c, sfb + 8 * c, ks > 0 || j > 0);
+                        }
+                    tc_commit<true>(empty(s));
+                }
+                if (ok && one) tc_commit<true>(acc_full);
+            }
+            if (one && *ab) {  // MMAs in flight end before their shared and tensor memory goes away
+                tc_commit<true>(drained);
+                const unsigned long long t0 = global_ns();
+                while (!mbar_test(drained, 0) && global_ns() - t0 < kWaitLimitNs) {
+                }
+            }
+        }
+    } else {
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t mine = acc + ((uint32_t)(quad * 32) << 16), leader_empty = peer_addr(acc_empty, 0);
+        T* const out = static_cast<T*>(p.out);
+        const bool a32 = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.ld * (long long)sizeof(T))) & 31) == 0;
+        int it = 0;
+        for (int tile = tile0; tile < p.tiles; tile += tile_step, ++it) {
+            bool ok = lane != 0 || mbar_wait<true>(acc_full, (uint32_t)it & 1u, ab, err);
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (!ok) break;
+            tc_fence_after();
+            const int xt = tile % p.xtiles, yt = tile / p.xtiles;
+            const int x = xt * 256 + (int)rank * 128 + quad * 32 + lane, y0 = yt * 256 + half * 128;
+            store_rows<T, 128>(mine + half * 128, out, p.ld, x, p.rx, y0, p.ry, a32, [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(leader_empty);
+            });
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();  // neither CTA is signalled or read by the other any more
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free<512, true>(acc);
+    }
+}
+
+// the driver's tensor-map encoder, fetched once through the runtime (null if it cannot be had)
+PFN_cuTensorMapEncodeTiled map_encoder() {
     static PFN_cuTensorMapEncodeTiled fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -371,6 +588,11 @@ bool encode_codes_map(CUtensorMap* m, const void* base, long long rows, long lon
         else
             cudaGetLastError();
     });
+    return fn;
+}
+// tensor map of an operand's codes, [rows, row_bytes]: boxes of box_rows rows x 128 bytes, 128-byte swizzle
+bool encode_codes_map(CUtensorMap* m, const void* base, long long rows, long long row_bytes, int box_rows) {
+    const PFN_cuTensorMapEncodeTiled fn = map_encoder();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
@@ -378,6 +600,19 @@ bool encode_codes_map(CUtensorMap* m, const void* base, long long rows, long lon
     const cuuint32_t estr[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// tensor map of an operand's scale tiles, [tile rows, kt4, 128 words]: boxes of tile_rows x ts tiles
+bool encode_scales_map(CUtensorMap* m, const void* base, long long rows, long long kt4, int ts, int tile_rows) {
+    const PFN_cuTensorMapEncodeTiled fn = map_encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {128, (cuuint64_t)kt4, (cuuint64_t)((rows + 127) / 128)};
+    const cuuint64_t strides[2] = {512, (cuuint64_t)kt4 * 512};
+    const cuuint32_t box[3] = {128, (cuuint32_t)ts, (cuuint32_t)tile_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -390,19 +625,65 @@ struct MmCall {
     cudaStream_t st;
 };
 
-template <int F, int BN, bool SWAP, typename T> cudaError_t go(const MmCall& c) {
-    using C = MmCfg<F, BN>;
-    auto* kern = k_matmul<F, BN, SWAP, T>;
-    static std::atomic<unsigned long long> ready{0};  // devices whose shared-memory limit is raised
-    const unsigned long long bit = c.dev < 64 ? 1ull << c.dev : 0;
-    if (!(ready.load(std::memory_order_acquire) & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-        if (e != cudaSuccess) return e;
-        ready.fetch_or(bit, std::memory_order_release);
-    }
+// raise a kernel's shared-memory limit, once per device (`ready`: the kernel's devices done)
+template <typename K> cudaError_t allow_smem(K* kern, int bytes, int dev, std::atomic<unsigned long long>& ready) {
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+template <int F, typename T> cudaError_t go_pair(const MmCall& c) {
+    using C = PairCfg<F>;
+    auto* kern = k_matmul_pair<F, T>;
+    static std::atomic<unsigned long long> ready{0};
+    const cudaError_t e = allow_smem(kern, C::SMEM, c.dev, ready);
+    if (e != cudaSuccess) return e;
+    const long long row_bytes = F == F_E2M1 ? c.k / 2 : c.k;
+    MmArgs a{};
+    a.out = c.out;
+    a.rx = (int)c.rx;
+    a.ry = (int)c.ry;
+    a.k = (int)c.k;
+    a.kt4 = (int)((c.k / 32 + 3) / 4);
+    const long long xt = (c.rx + 255) / 256, yt = (c.ry + 255) / 256;
+    if (xt * yt > 0x3FFFFFFFLL) return cudaErrorInvalidValue;
+    a.xtiles = (int)xt;
+    a.tiles = (int)(xt * yt);
+    a.split = 1;
+    a.ld = c.ld;
+    CUtensorMap ma, mb, msa, msb;
+    if (!encode_codes_map(&ma, c.xc, c.rx, row_bytes, 128) || !encode_codes_map(&mb, c.yc, c.ry, row_bytes, 128) ||
+        !encode_scales_map(&msa, c.xs, c.rx, a.kt4, C::TS, 1) || !encode_scales_map(&msb, c.ys, c.ry, a.kt4, C::TS, 2))
+        return cudaErrorUnknown;
+    cudaLaunchConfig_t cfg = {};
+    const int pairs = c.sms / 2;
+    cfg.gridDim = dim3((unsigned)(2 * (a.tiles < pairs ? a.tiles : pairs)));
+    cfg.blockDim = dim3(kMmThreads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = c.st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, ma, mb, msa, msb, (const MmArgs)a, c.err);
+}
+
+template <int F, bool SWAP, typename T> cudaError_t go(const MmCall& c, int bn) {
+    using C = MmCfg<F>;
+    auto* kern = k_matmul<F, SWAP, T>;
+    static std::atomic<unsigned long long> ready{0};
+    const cudaError_t e = allow_smem(kern, 225 * 1024, c.dev, ready);
+    if (e != cudaSuccess) return e;
     const long long row_bytes = F == F_E2M1 ? c.k / 2 : c.k;
     CUtensorMap mx, my;
-    if (!encode_codes_map(&mx, c.xc, c.rx, row_bytes, kMmRows) || !encode_codes_map(&my, c.yc, c.ry, row_bytes, BN))
+    if (!encode_codes_map(&mx, c.xc, c.rx, row_bytes, kMmRows) || !encode_codes_map(&my, c.yc, c.ry, row_bytes, bn))
         return cudaErrorUnknown;
     MmArgs a{};
     a.sx = static_cast<const uint8_t*>(c.xs);
@@ -412,20 +693,26 @@ template <int F, int BN, bool SWAP, typename T> cudaError_t go(const MmCall& c) 
     a.ry = (int)c.ry;
     a.k = (int)c.k;
     a.kt4 = (int)((c.k / 32 + 3) / 4);
-    const long long xt = (c.rx + kMmRows - 1) / kMmRows, yt = (c.ry + BN - 1) / BN;
+    const long long xt = (c.rx + kMmRows - 1) / kMmRows, yt = (c.ry + bn - 1) / bn;
     if (xt * yt > 0x7FFFFFFFLL / kMmSplitMax) return cudaErrorInvalidValue;
     a.xtiles = (int)xt;
     a.tiles = (int)(xt * yt);
     a.ld = c.ld;
-    // idle SMs take part of a tile's k range, at least two stages each
+    a.bn = bn;
+    // Idle SMs take part of a tile's k range, at least two stages each. One CTA per SM with the whole ring is faster than
+    // two with half each (MXFP8 77 x 9728 x 2560 10.7 us against 12.4, 333 x 1024 x 2560 7.8 against 11.0), except where
+    // more tiles than SMs would take a second wave of several stages (2048 x 2048 x 2048 12.9 against 11.3; with three
+    // stages, 1024 x 2560 x 352, 5.6 against 6.1).
     const int nks = (int)((c.k + MmFmt<F>::VALS - 1) / MmFmt<F>::VALS);
+    const bool two = a.tiles > c.sms && nks > 4;
     a.split = 1;
-    if (BN <= 128)
-        while (a.split < kMmSplitMax && a.tiles * a.split * 2 <= c.sms && nks >= a.split * 4) a.split *= 2;
+    while (!two && a.split < kMmSplitMax && a.tiles * a.split * 2 <= c.sms && nks >= a.split * 4) a.split *= 2;
+    a.stages = C::stages(bn, two);
+    const int places = two ? 2 * c.sms : c.sms;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.split > 1 ? a.tiles * a.split : (a.tiles < c.sms ? a.tiles : c.sms)));
+    cfg.gridDim = dim3((unsigned)(a.split > 1 ? a.tiles * a.split : (a.tiles < places ? a.tiles : places)));
     cfg.blockDim = dim3(kMmThreads);
-    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.dynamicSmemBytes = C::smem(bn, a.stages);
     cfg.stream = c.st;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -444,16 +731,13 @@ template <int F, typename T> cudaError_t pick(MmCall c, const void* ac, const vo
     if (m <= 128) {  // few tokens: the weight's rows on the 128-row side
         c.xc = bc; c.xs = bs; c.rx = n;
         c.yc = ac; c.ys = as; c.ry = m;
-        if (m <= 16) return go<F, 16, true, T>(c);
-        if (m <= 32) return go<F, 32, true, T>(c);
-        if (m <= 64) return go<F, 64, true, T>(c);
-        return go<F, 128, true, T>(c);
+        return go<F, true, T>(c, (int)((m + 15) / 16 * 16));
     }
     c.xc = ac; c.xs = as; c.rx = m;
     c.yc = bc; c.ys = bs; c.ry = n;
-    // tiles of 128 x 256 move the fewest operand bytes; narrower ones where those would leave SMs idle
-    if (((m + 127) / 128) * ((n + 255) / 256) >= c.sms) return go<F, 256, false, T>(c);
-    return go<F, 128, false, T>(c);
+    // 256 x 256 per pair of SMs moves the fewest operand bytes, if that gives every pair a tile
+    if (((m + 255) / 256) * ((n + 255) / 256) >= c.sms / 2) return go_pair<F, T>(c);
+    return go<F, false, T>(c, 128);
 }
 
 }  // namespace
@@ -477,3 +761,4 @@ cudaError_t launch_matmul(int fmt, const void* ac, const void* as, const void* b
 }
 
 }  // namespace mxq
+

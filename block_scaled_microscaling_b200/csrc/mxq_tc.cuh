@@ -10,13 +10,22 @@ namespace mxq {
 
 // ---- tensor memory ------------------------------------------------------------------------
 
-// a whole warp allocates / frees NCOL columns (a power of two, 32 .. 512); the address goes to shared memory
-template <int NCOL> __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "n"(NCOL) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+// PAIR: the two CTAs of a cluster work on one tile (cta_group::2); one value throughout a kernel.
+
+// a whole warp (PAIR: of each CTA) allocates / frees NCOL columns (a power of two, 32 .. 512); the address goes
+// to shared memory
+template <int NCOL, bool PAIR = false> __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst) {
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "n"(NCOL) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "n"(NCOL) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
 }
-template <int NCOL> __device__ __forceinline__ void tmem_free(uint32_t taddr) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(NCOL));
+template <int NCOL, bool PAIR = false> __device__ __forceinline__ void tmem_free(uint32_t taddr) {
+    if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(NCOL));
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(NCOL));
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -43,14 +52,24 @@ __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.
 
 // ---- descriptors --------------------------------------------------------------------------
 
-// operand tile in shared memory, K-major rows of 128 bytes with the 128-byte swizzle (1024-byte aligned
-// groups of eight rows, 1024 bytes apart)
-__device__ __forceinline__ unsigned long long desc_sw128(uint32_t saddr) {
-    return (unsigned long long)((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+// A shared-memory descriptor is a constant high word and a low word that is the address / 16 (and a constant), so a
+// step along the operand is one 32-bit addition.
+struct SmemDesc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ SmemDesc operator+(uint32_t bytes) const { return {lo + (bytes >> 4), hi}; }
+};
+// operand tile, K-major rows of 128 bytes with the 128-byte swizzle (1024-byte aligned groups of eight rows, 1024
+// bytes apart)
+__device__ __forceinline__ SmemDesc desc_sw128(uint32_t saddr) {
+    return {((saddr >> 4) & 0x3FFFu) | (1u << 16), 64u | (1u << 14) | (2u << 29)};
 }
 // 512-byte scale tile: 32 rows of 16 bytes, no swizzle (groups of eight rows 128 bytes apart)
-__device__ __forceinline__ unsigned long long desc_scales(uint32_t saddr) {
-    return (unsigned long long)((saddr >> 4) & 0x3FFFu) | (8ull << 32) | (1ull << 46);
+__device__ __forceinline__ SmemDesc desc_scales(uint32_t saddr) { return {(saddr >> 4) & 0x3FFFu, 8u | (1u << 14)}; }
+// one thread of a converged warp; the operands that the whole warp computes stay in uniform registers
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
 }
 // instruction descriptor of the block-scaled kinds: both operands of element format F, K-major, E8M0 scales
 template <int F> __host__ __device__ constexpr uint32_t idesc_block_scaled(int m, int n) {
@@ -61,36 +80,65 @@ template <int F> __host__ __device__ constexpr uint32_t idesc_block_scaled(int m
 // ---- instructions (one thread issues) -------------------------------------------------------
 
 // scale tile -> four tensor-memory columns: row r of 128 at lane r % 32, column r / 32 (copied to all four
-// lane groups), its four block scales in the column's four bytes
-__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, unsigned long long desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
-// D += A B^T with the scales of A's rows at tensor-memory column sfa and of B's rows at sfb
-template <int F>
-__device__ __forceinline__ void tc_mma_block_scaled(uint32_t d, unsigned long long a, unsigned long long b,
-                                                    uint32_t idesc, uint32_t sfa, uint32_t sfb, bool accumulate) {
-    if constexpr (F == F_E2M1)
-        asm volatile(
-            "{ .reg .pred p; setp.ne.u32 p, %6, 0;\n"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)accumulate)
-            : "memory");
+// lane groups), its four block scales in the column's four bytes (PAIR: in both CTAs, each from its own tile)
+template <bool PAIR = false> __device__ __forceinline__ void tc_copy_scales(uint32_t taddr, SmemDesc d) {
+    if constexpr (PAIR)
+        asm volatile("{ .reg .b64 d; mov.b64 d, {%1, %2};\n tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d; }" ::"r"(taddr),
+                     "r"(d.lo), "r"(d.hi)
+                     : "memory");
     else
-        asm volatile(
-            "{ .reg .pred p; setp.ne.u32 p, %6, 0;\n"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)accumulate)
-            : "memory");
+        asm volatile("{ .reg .b64 d; mov.b64 d, {%1, %2};\n tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d; }" ::"r"(taddr),
+                     "r"(d.lo), "r"(d.hi)
+                     : "memory");
 }
-// arrive on an mbarrier once everything this thread issued to the tensor core has completed
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// D += A B^T with the scales of A's rows at tensor-memory column sfa and of B's rows at sfb (PAIR: each CTA holds
+// half of A's and of B's rows, and all of B's scales)
+#define MXQ_MMA(GROUP, KIND, VEC)                                                                                      \
+    asm volatile("{ .reg .pred p; .reg .b64 a, b; setp.ne.u32 p, %8, 0;\n"                                            \
+                 "mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"                                                       \
+                 "tcgen05.mma.cta_group::" GROUP ".kind::" KIND ".block_scale.scale_vec::" VEC                         \
+                 " [%0], a, b, %5, [%6], [%7], p; }" ::"r"(d),                                                         \
+                 "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)accumulate) \
+                 : "memory")
+template <int F, bool PAIR = false>
+__device__ __forceinline__ void tc_mma_block_scaled(uint32_t d, SmemDesc a, SmemDesc b, uint32_t idesc,
+                                                    uint32_t sfa, uint32_t sfb, bool accumulate) {
+    if constexpr (F == F_E2M1 && PAIR) MXQ_MMA("2", "mxf4", "2X");
+    else if constexpr (F == F_E2M1) MXQ_MMA("1", "mxf4", "2X");
+    else if constexpr (PAIR) MXQ_MMA("2", "mxf8f6f4", "1X");
+    else MXQ_MMA("1", "mxf8f6f4", "1X");
+}
+#undef MXQ_MMA
+// arrive on an mbarrier once everything this thread issued to the tensor core has completed (PAIR: on the barrier
+// at this address in both CTAs)
+template <bool PAIR = false> __device__ __forceinline__ void tc_commit(uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                     "h"((uint16_t)3)
+                     : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // ---- clusters -----------------------------------------------------------------------------
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// cluster address of this CTA's shared address `saddr` in the CTA of rank `rank`
+__device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
+    uint32_t p;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(saddr), "r"(rank));
+    return p;
+}
+// arrive on an mbarrier of any CTA of the cluster (a cluster address)
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t caddr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
 // a float at this CTA's shared address `saddr`, read from the CTA of rank `rank`
 __device__ __forceinline__ float ld_peer_f32(uint32_t saddr, uint32_t rank) {

@@ -29,14 +29,36 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+// CLUSTER: the barrier is also arrived on from another CTA of the cluster
+template <bool CLUSTER = false> __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{ .reg .pred p;\n"
+            "  mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+            "  selp.u32 %0, 1, 0, p; }"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(kSuspendNs)
+            : "memory");
+    else
+        asm volatile(
+            "{ .reg .pred p;\n"
+            "  mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            "  selp.u32 %0, 1, 0, p; }"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(kSuspendNs)
+            : "memory");
+    return ok != 0;
+}
+// the phase's state now, without waiting
+__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{ .reg .pred p;\n"
-        "  mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        "  mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
         "  selp.u32 %0, 1, 0, p; }"
         : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(kSuspendNs)
+        : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
 }
@@ -47,12 +69,13 @@ __device__ __forceinline__ unsigned long long global_ns() {
 }
 // wait for the phase of `parity` to complete; false after the time limit or once
 // another warp of the CTA has given up (then the device error word is set)
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned int* err,
                                           unsigned long long limit_ns = kWaitLimitNs) {
-    if (mbar_test(bar, parity)) return true;
+    if (mbar_test<CLUSTER>(bar, parity)) return true;
     const unsigned long long t0 = global_ns();
     for (;;) {
-        if (mbar_test(bar, parity)) return true;
+        if (mbar_test<CLUSTER>(bar, parity)) return true;
         if (*abort_flag || global_ns() - t0 > limit_ns) {
             *abort_flag = 1;
             atomicOr(err, 1u);

@@ -17,7 +17,8 @@ FMTS = ["mxfp4", "mxfp8"]
 # tiles (k shared by a cluster), more tiles than SMs (a CTA walks several)
 SHAPES = [(1, 32, 32), (1, 128, 64), (1, 4096, 4096), (3, 130, 96), (16, 257, 160), (17, 64, 224), (33, 100, 288), (64, 129, 512),
           (65, 640, 1056), (77, 1000, 2560), (128, 300, 512), (129, 31, 544), (200, 520, 1056), (257, 385, 96),
-          (300, 1000, 2048), (1000, 2300, 320), (2100, 2600, 288), (130, 1, 32)]
+          (300, 1000, 2048), (1000, 2300, 320), (2100, 2600, 288), (130, 1, 32), (4700, 2400, 352),
+          (5000, 4000, 2080)]
 
 
 def values(seed, rows, cols, dtype=torch.bfloat16):
@@ -57,7 +58,7 @@ def test_product(m, n, k, fmt, dtype):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("m,n,k", [(5, 200, 416), (150, 300, 416), (2100, 2600, 256)])
+@pytest.mark.parametrize("m,n,k", [(5, 200, 416), (150, 300, 416), (2100, 2600, 256), (4700, 2400, 416)])
 def test_product_of_small_integers_is_exact(m, n, k, fmt):
     """Codes of 0, 1, 2, 3, 4 and scales 1: every sum is an integer below 2^24, whatever the order."""
     g = torch.Generator(device="cuda").manual_seed(k)
@@ -83,7 +84,7 @@ def test_product_extreme_scales_and_zero_blocks(fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("m", [3, 200])
+@pytest.mark.parametrize("m", [3, 200, 10000])
 def test_product_nan_blocks_stay_in_their_rows(m, fmt):
     a, b = values(1, m, 512), values(2, 300, 512)
     a[1, 100] = float("nan")
@@ -95,7 +96,7 @@ def test_product_nan_blocks_stay_in_their_rows(m, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (77, 300, 2560), (200, 300, 2048)])
+@pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (77, 300, 2560), (200, 300, 2048), (4700, 2400, 352)])
 def test_product_repeats_bit_for_bit(m, n, k, fmt):
     a, b = mxq.quantize_mma(values(1, m, k), fmt), mxq.quantize_mma(values(2, n, k), fmt)
     first = ops.matmul(*a, *b, fmt)
