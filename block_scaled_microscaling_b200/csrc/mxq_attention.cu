@@ -5,11 +5,13 @@
 // over the keys j that row r sees. 17 bytes hold 32 cached values, so at the copy bandwidth 12 values arrive per
 // picosecond and the SMs have about three lane instructions for each: what bounds the kernel is turning codes into
 // operands. Hence:
-// - codes go from global memory to registers in the layout of mma.sync's fragments, without shared memory or
-//   shuffles. The summed index may be permuted freely, so the lane that holds key g's part of an operand owns a
-//   contiguous quarter of the key (16 bytes of codes and one scale at head_dim 128), and four lanes share it; for
-//   V, whose operand pairs two keys, a lane takes the same 8 bytes of four neighbouring keys and interleaves the
-//   nibbles of two keys with shifts and masks before the conversion.
+// - each warp takes groups of 16 keys (a group lies within a page) through its own ring of stages in shared memory,
+//   filled by 16-byte asynchronous copies three groups ahead: no registers hold data in flight and no warp waits for
+//   another. Codes leave the stage in the layout of mma.sync's fragments. The summed index may be permuted freely,
+//   so the lane that holds key g's part of an operand owns a contiguous quarter of the key (16 bytes of codes and one
+//   scale at head_dim 128), and four lanes share it; for V, whose operand pairs two keys, a lane takes the same 8
+//   bytes of four neighbouring keys and interleaves the nibbles of two keys with shifts and masks before the
+//   conversion. V's rows are stored permuted, so that these reads touch every bank once.
 // - cvt.rn.f16x2.e2m1x2 converts two codes; one f16x2 product applies the block scale. Both products run in f16
 //   with fp32 sums (m16n8k16): keys (then head dimensions) fill the instruction's 16 rows and the queries its 8
 //   columns, so one query of up to 8 heads per key head (a decoding step) wastes nothing.
@@ -19,9 +21,9 @@
 //   two for the same reason. Scores return to their true size in fp32.
 // - the running maximum m_r is raised only when a score exceeds it by 2^8 (one vote per 16 keys); the weights
 //   then are at most 2^8 and round to f16 (relative error 2^-12; below 2^-14 absolute, 2^-25).
-// Each warp takes every fourth group of 16 keys (a group lies within a page; page numbers are fetched 32 groups
-// at a time), with the next group's loads in flight; the four warps' results are joined through shared memory, and
-// a long sequence is split over several CTAs whose partial sums a second kernel joins in order.
+// The four warps of a CTA take every fourth group (page numbers are fetched 32 groups at a time); their results are
+// joined through shared memory, and a long sequence is split over several CTAs whose partial sums a second kernel
+// joins in order.
 #include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -30,12 +32,14 @@
 
 #include "mxq_device.cuh"
 #include "mxq_internal.h"
+#include "mxq_tma.cuh"
 
 namespace mxq {
 namespace {
 
 constexpr int kAtWarps = 4, kAtThreads = 32 * kAtWarps;
 constexpr int kAtMinGroups = 8;    // groups of 16 keys that a split has at least
+constexpr int kAtStages = 4;       // groups in a warp's ring
 constexpr int kAtMaxSplits = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -134,6 +138,10 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// log2 of a weight: score * mk - m
+__device__ __forceinline__ float weight_exponent(float score, float mk, float m) { return fmaf(score, mk, -m); }
+// byte 0x4440 + j of x, zero-extended
+__device__ __forceinline__ uint32_t prmt(uint32_t x, uint32_t sel) { return __byte_perm(x, 0u, sel); }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
@@ -146,76 +154,57 @@ __device__ __forceinline__ void e2m1_to_h2(uint32_t x, uint32_t* r) {
         "cvt.rn.f16x2.e2m1x2 %2, c2;\n cvt.rn.f16x2.e2m1x2 %3, c3; }"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(x));
 }
-// 2^(byte - ref) as fp32 (0 far below 1; the conversion to f16 rounds small ones)
-__device__ __forceinline__ float rel_scale(int byte, int ref) { return __uint_as_float((uint32_t)max(byte - ref + 127, 0) << 23); }
+// 2^(byte - ref) as fp32 (2^-126 far below 1, which the conversion to f16 makes 0; it rounds small ones)
+__device__ __forceinline__ float rel_scale(int byte, int ref) {
+    return __uint_as_float((uint32_t)(max(byte, ref - 126) - (ref - 127)) << 23);
+}
 // 2^e for any integer e (clamped to the fp32 range, subnormals flushed)
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)min(max(e + 127, 0), 255) << 23); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
 
-// one group's bytes, in the lane's share
-template <int D> struct Loads {
-    uint32_t k[2][D / 32];  // keys 4 (g / 2) + g % 2 and + 2: codes of dimensions t D/4 ..
-    uint32_t v[4][D / 64];  // keys 4 t + i: codes of dimensions g D/8 ..
-    uint32_t ks[2];         // their scale bytes
-    uint32_t vs[4];
+// a stage: codes of 16 keys and values, then their scales
+template <int D> struct AtStage {
+    static constexpr int ROW = D / 2, SROW = D / 32;  // bytes of a key's codes, of its scales
+    static constexpr int K = 0, V = 16 * ROW, KS = 2 * V, VS = KS + 16 * SROW, BYTES = VS + 16 * SROW;
+    // place of 16-byte piece c of V's row r: a lane quad's four rows 4t + i fall on different banks
+    static __device__ __forceinline__ uint32_t v_at(int r, int c) {
+        if (D == 128) return (uint32_t)(V + (r ^ ((r >> 2) & 1)) * ROW + 16 * (c ^ ((r >> 3) << 1)));
+        return (uint32_t)(V + (r ^ (r >> 2)) * ROW + 16 * c);
+    }
 };
-
-template <int D> __device__ __forceinline__ void fetch(const KvCache& c, int head, int page, int off, int g, int t, Loads<D>& L) {
-    if (page < 0) {
+// the lane's share of the copies of a group whose first row of the cache is `row`
+template <int D> __device__ __forceinline__ void fetch(const KvCache& c, long long row, uint32_t stage, int lane) {
+    using S = AtStage<D>;
+    constexpr int PIECES = S::ROW / 16;  // 16-byte pieces of a row
+    const long long at = row * S::ROW;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) L.k[i][j] = 0;
-            L.ks[i] = 0;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int j = 0; j < D / 64; ++j) L.v[i][j] = 0;
-            L.vs[i] = 0;
-        }
-        return;
+    for (int i = 0; i < PIECES / 2; ++i) {
+        const int j = i * 32 + lane;
+        copy16(stage + S::K + 16 * j, c.kc + at + 16 * j);
+        copy16(stage + S::v_at(j / PIECES, j % PIECES), c.vc + at + 16 * j);
     }
-    const long long row = ((long long)page * c.heads + head) * c.page + off;
-    const int ka = 4 * (g >> 1) + (g & 1);
-    const uint8_t* pk = reinterpret_cast<const uint8_t*>(c.kc) + (row + ka) * (D / 2) + t * (D / 8);
-    const uint8_t* pv = reinterpret_cast<const uint8_t*>(c.vc) + (row + 4 * t) * (D / 2) + g * (D / 16);
-    const uint8_t* sk = c.ks + (row + ka) * (D / 32) + (D == 128 ? t : t >> 1);
-    const uint8_t* sv = c.vs + (row + 4 * t) * (D / 32);
-    if constexpr (D == 128) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(pk + i * D));
-            L.k[i][0] = x.x;
-            L.k[i][1] = x.y;
-            L.k[i][2] = x.z;
-            L.k[i][3] = x.w;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint2 x = __ldg(reinterpret_cast<const uint2*>(pv + i * (D / 2)));
-            L.v[i][0] = x.x;
-            L.v[i][1] = x.y;
-        }
-        const uint4 s = __ldg(reinterpret_cast<const uint4*>(sv));
-        const uint32_t w[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) L.vs[i] = (w[i] >> (8 * (g >> 1))) & 0xFFu;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint2 x = __ldg(reinterpret_cast<const uint2*>(pk + i * D));
-            L.k[i][0] = x.x;
-            L.k[i][1] = x.y;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) L.v[i][0] = __ldg(reinterpret_cast<const uint32_t*>(pv + i * (D / 2)));
-        const uint2 s = __ldg(reinterpret_cast<const uint2*>(sv));
-        const uint32_t w[2] = {s.x, s.y};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) L.vs[i] = (w[i >> 1] >> (16 * (i & 1) + 8 * (g >> 2))) & 0xFFu;
+    if (lane < 2 * S::SROW) {  // scales: SROW pieces of 16 bytes each of K and V
+        const bool v = lane >= S::SROW;
+        const int j = lane - (v ? S::SROW : 0);
+        copy16(stage + (v ? S::VS : S::KS) + 16 * j, (v ? c.vs : c.ks) + row * S::SROW + 16 * j);
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) L.ks[i] = __ldg(sk + i * (D / 16));
 }
 
 // float offset of dimension d of row r in a warp's result: rows D + 4 floats apart, so that the lanes' 16-byte
@@ -223,10 +212,11 @@ template <int D> __device__ __forceinline__ void fetch(const KvCache& c, int hea
 template <int D> __device__ __forceinline__ int res_off(int r, int d) { return r * (D + 4) + d; }
 
 // NQ: groups of eight rows that a warp handles together (their Q operands in shared memory when NQ is 4)
-template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ? 2 : 3) k_kv_attention(const AtArgs p) {
+template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ? 2 : NQ == 2 ? 3 : 4) k_kv_attention(const AtArgs p) {
     constexpr int ROWS = 8 * NQ, STEPS = D / 16, TILES = D / 16;
     constexpr bool QS = NQ == 4;
-    extern __shared__ __align__(16) float dsm[];
+    using S = AtStage<D>;
+    extern __shared__ __align__(16) float dsm[];  // stages of the warps, Q's operands; later the warps' results
     __shared__ float sm_m[kAtWarps][ROWS], sm_l[kAtWarps][ROWS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     pdl_wait_then_release();
@@ -250,7 +240,7 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
 
     // ---- the rows' queries: lane (g, t) holds row g of each eight, dimensions t D/4 .., divided by 2^e ----
     uint32_t qf[QS ? 1 : NQ][STEPS][2];
-    uint2* const qsm = reinterpret_cast<uint2*>(dsm);
+    uint2* const qsm = reinterpret_cast<uint2*>(reinterpret_cast<char*>(dsm) + kAtWarps * kAtStages * S::BYTES);
     float mul[NQ][2];  // per column of the score tiles (rows 2t, 2t + 1): scale * log2(e) * 2^e
     int pos[NQ][2];    // last key that the row sees (-1: no row)
 #pragma unroll
@@ -303,7 +293,8 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
     }
     if constexpr (QS) __syncthreads();
 
-    float o[NQ][TILES][4], m[NQ][2], l[NQ][2];
+    float o[NQ][TILES][4], l[NQ][2];
+    float m[NQ][2], thr[NQ][2];  // running maximum (0 before the first key) and what a score may exceed it by
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
 #pragma unroll
@@ -312,97 +303,127 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
             for (int k = 0; k < 4; ++k) o[n][u][k] = 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            m[n][k] = -INFINITY;
-            l[n][k] = 0.f;
+            m[n][k] = l[n][k] = 0.f;
+            thr[n][k] = -INFINITY;
         }
     }
-    int kref = -1000, vref = -1000;  // block scales are taken relative to these bytes
-    float kmul = 1.f;                // 2^(kref - 127)
-    uint32_t vnan = 0;               // bit 2n + k: a value block that row sees is NaN
+    int kref = -1000, vref = -1000;   // block scales are taken relative to these bytes
+    int klim = -1, vlim = -1;         // and may be at most these
+    float mk[NQ][2];                  // mul * 2^(kref - 127)
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) mk[n][0] = mk[n][1] = 0.f;
+    uint32_t vnan = 0;                // bit 2n + k: a value block that row sees is NaN
 
+    // groups of which every row sees every key (in a page of the cache)
     const int pos_lo = s.len - s.n + i0, pos_hi = s.len - s.n + i1;
-    int pages = -1, offs = 0;  // lane j: page and first row of the warp's group number base + j
-    auto page_of = [&](int grp) {
-        pages = -1;
-        offs = 0;
-        if (grp < last) {
-            const uint32_t key = 16u * (uint32_t)grp, at = key / (uint32_t)p.c.page;
-            offs = (int)(key - at * (uint32_t)p.c.page);
-            const int pg = __ldg(p.table + b * p.table_stride + at);
-            pages = pg >= 0 && pg < p.c.pages ? pg : -1;
+    const int whole_hi = min(s.len, pos_lo + 1) >> 4, whole_lo = p.window > 0 ? ((pos_hi - p.window) >> 4) + 1 : 0;
+    const uint32_t ring = smem_u32(dsm) + warp * kAtStages * S::BYTES;
+    int pages = -1, offs = 0;   // lane j: page and first row of the warp's group 32 * (issued / 32) + j
+    int issued = 0;             // groups of this warp whose copies are issued
+    uint32_t there = 0;         // bit j: the group issued j before the last is in a page of the cache
+    uint32_t put = ring;
+    auto issue = [&] {
+        if ((issued & 31) == 0) {
+            const int grp = first + warp + (issued + lane) * kAtWarps;
+            pages = -1;
+            if (grp < last) {
+                const uint32_t key = 16u * (uint32_t)grp, at = key / (uint32_t)p.c.page;
+                offs = (int)(key - at * (uint32_t)p.c.page);
+                const int pg = __ldg(p.table + b * p.table_stride + at);
+                pages = pg >= 0 && pg < p.c.pages ? pg : -1;
+            }
         }
+        const int pg = __shfl_sync(0xFFFFFFFFu, pages, issued & 31), off = __shfl_sync(0xFFFFFFFFu, offs, issued & 31);
+        if (pg >= 0) fetch<D>(p.c, ((long long)pg * p.c.heads + head) * p.c.page + off, put, lane);
+        there = (there << 1) | (pg >= 0 ? 1u : 0u);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ++issued;
+        put = put + S::BYTES == ring + kAtStages * S::BYTES ? ring : put + S::BYTES;
     };
-    Loads<D> next;
-    int grp = first + warp, it = 0;
-    page_of(grp + lane * kAtWarps);
-    int page = __shfl_sync(0xFFFFFFFFu, pages, 0);
-    if (grp < last) fetch<D>(p.c, head, page, __shfl_sync(0xFFFFFFFFu, offs, 0), g, t, next);
-    for (; grp < last; grp += kAtWarps) {
-        Loads<D> cur = next;
-        const bool in_page = page >= 0;
-        ++it;
-        if ((it & 31) == 0) page_of(grp + (1 + lane) * kAtWarps);
-        if (grp + kAtWarps < last) {
-            page = __shfl_sync(0xFFFFFFFFu, pages, it & 31);
-            fetch<D>(p.c, head, page, __shfl_sync(0xFFFFFFFFu, offs, it & 31), g, t, next);
-        }
+#pragma unroll
+    for (int i = 0; i < kAtStages - 1; ++i) issue();
+    uint32_t stage = ring;
+    const int kr = 4 * (g >> 1) + (g & 1);  // the lane's keys of the score tiles: kr, kr + 2
+    const uint32_t k_at = S::K + kr * S::ROW + t * (S::ROW / 4), ks_at = S::KS + kr * S::SROW + (D == 128 ? t : t >> 1);
+    const uint32_t vs_at = S::VS + 4 * t * S::SROW, v_sel = 0x4440u + (D == 128 ? g >> 1 : g >> 2);
+    for (int grp = first + warp; grp < last; grp += kAtWarps) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAtStages - 2) : "memory");
+        __syncwarp();  // every lane's copies of this group have landed, and the group before is read by every lane
+        issue();
+        const bool in_page = (there >> (kAtStages - 1)) & 1u;
         const int key0 = 16 * grp;
-        const int ka = key0 + 4 * (g >> 1) + (g & 1);  // the lane's keys of the score tiles: ka, ka + 2
-        // every row sees every key of the group?
-        const bool whole = in_page && key0 + 15 < s.len && key0 + 15 <= pos_lo && (p.window <= 0 || key0 > pos_hi - p.window);
+        uint32_t ks[2], vs[4];
+        ks[0] = lds8(stage + ks_at);
+        ks[1] = lds8(stage + ks_at + 2 * S::SROW);
+        if constexpr (D == 128) {
+            const uint4 w = lds128u(stage + vs_at);
+            vs[0] = prmt(w.x, v_sel);
+            vs[1] = prmt(w.y, v_sel);
+            vs[2] = prmt(w.z, v_sel);
+            vs[3] = prmt(w.w, v_sel);
+        } else {
+            const uint2 w = lds64(stage + vs_at);
+            vs[0] = prmt(w.x, v_sel);
+            vs[1] = prmt(w.x, v_sel + 2);
+            vs[2] = prmt(w.y, v_sel);
+            vs[3] = prmt(w.y, v_sel + 2);
+        }
+        const bool whole = in_page && grp < whole_hi && grp >= whole_lo;
         if (!whole) {  // bytes of keys that nobody sees count as zeros
-            const int end = in_page ? s.len : 0;
+            const int end = in_page ? s.len - key0 : 0;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (ka + 2 * i >= end) cur.ks[i] = 0;
+                if (kr + 2 * i >= end) ks[i] = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (key0 + 4 * t + i >= end) cur.vs[i] = 0;
+                if (4 * t + i >= end) vs[i] = 0;
         }
-        // raise the references where a block (NaN blocks aside) exceeds 2^13 of them
-        {
+        if (__any_sync(0xFFFFFFFFu, (int)max(ks[0], ks[1]) > klim || (int)max(max(vs[0], vs[1]), max(vs[2], vs[3])) > vlim)) {
+            // raise the references where a block (NaN blocks aside) exceeds 2^13 of them
             int kt = -1, vt = -1;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) kt = max(kt, cur.ks[i] == 0xFFu ? -1 : (int)cur.ks[i]);
+            for (int i = 0; i < 2; ++i) kt = max(kt, ks[i] == 0xFFu ? -1 : (int)ks[i]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) vt = max(vt, cur.vs[i] == 0xFFu ? -1 : (int)cur.vs[i]);
-            const bool vbad = (cur.vs[0] == 0xFFu) | (cur.vs[1] == 0xFFu) | (cur.vs[2] == 0xFFu) | (cur.vs[3] == 0xFFu);
-            if (__any_sync(0xFFFFFFFFu, kt > kref + 13 || vt > vref + 13 || vbad)) {
-                kt = __reduce_max_sync(0xFFFFFFFFu, kt);
-                if (kt > kref + 13) {
-                    kref = kt - 6;
-                    kmul = pow2i(kref - 127);
-                }
-                vt = __reduce_max_sync(0xFFFFFFFFu, vt);
-                if (vt > vref + 13) {
-                    const float f = pow2i(vref - (vt - 6));  // 0 the first time: the sums are 0
+            for (int i = 0; i < 4; ++i) vt = max(vt, vs[i] == 0xFFu ? -1 : (int)vs[i]);
+            kt = __reduce_max_sync(0xFFFFFFFFu, kt);
+            if (kt > kref + 13) {
+                kref = kt - 6;
+                klim = min(kref + 13, 254);
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n)
+                for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                        for (int u = 0; u < TILES; ++u)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) o[n][u][k] *= f;
-                    vref = vt - 6;
-                }
-                // a NaN block of V makes its 32 dimensions NaN for the rows that see its key, and for no others
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                    for (int tt = 0; tt < 4; ++tt) {
-                        const bool bad = __shfl_sync(0xFFFFFFFFu, cur.vs[i], (lane & ~3) | tt) == 0xFFu;
-                        const int key = key0 + 4 * tt + i;
-                        if (bad)
-#pragma unroll
-                            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                                for (int k = 0; k < 2; ++k)
-                                    if (key <= pos[n][k] && (p.window <= 0 || key > pos[n][k] - p.window)) vnan |= 1u << (2 * n + k);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (cur.vs[i] == 0xFFu) cur.vs[i] = 0;
+                    for (int k = 0; k < 2; ++k) mk[n][k] = mul[n][k] * pow2i(kref - 127);
             }
+            vt = __reduce_max_sync(0xFFFFFFFFu, vt);
+            if (vt > vref + 13) {
+                const float f = pow2i(vref - (vt - 6));  // 0 the first time: the sums are 0
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int u = 0; u < TILES; ++u)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) o[n][u][k] *= f;
+                vref = vt - 6;
+                vlim = min(vref + 13, 254);
+            }
+            // a NaN block of V makes its 32 dimensions NaN for the rows that see its key, and for no others
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt) {
+                    const bool bad = __shfl_sync(0xFFFFFFFFu, vs[i], (lane & ~3) | tt) == 0xFFu;
+                    const int key = key0 + 4 * tt + i;
+                    if (bad)
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                if (key <= pos[n][k] && (p.window <= 0 || key > pos[n][k] - p.window)) vnan |= 1u << (2 * n + k);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (vs[i] == 0xFFu) vs[i] = 0;
         }
         // ---- scores: keys x rows ----
         float sc[NQ][4];
@@ -414,14 +435,29 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
             uint32_t f[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float x = cur.ks[i] == 0xFFu ? __uint_as_float(0x7FC00000u) : rel_scale((int)cur.ks[i], kref);
+                const float x = ks[i] == 0xFFu ? __uint_as_float(0x7FC00000u) : rel_scale((int)ks[i], kref);
                 f[i] = pack_h2(x, x);
+            }
+            uint32_t kw[2][D / 32];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (D == 128) {
+                    const uint4 x = lds128u(stage + k_at + 2 * i * S::ROW);
+                    kw[i][0] = x.x;
+                    kw[i][1] = x.y;
+                    kw[i][2] = x.z;
+                    kw[i][3] = x.w;
+                } else {
+                    const uint2 x = lds64(stage + k_at + 2 * i * S::ROW);
+                    kw[i][0] = x.x;
+                    kw[i][1] = x.y;
+                }
             }
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
                 uint32_t a[4], c[4];
-                e2m1_to_h2(cur.k[0][j], a);
-                e2m1_to_h2(cur.k[1][j], c);
+                e2m1_to_h2(kw[0][j], a);
+                e2m1_to_h2(kw[1][j], c);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     a[k] = mul_h2(a[k], f[0]);
@@ -445,66 +481,78 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
             }
         }
         // ---- weights ----
+        float w[NQ][4];
         bool up = false;
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                sc[n][k] *= mul[n][k & 1] * kmul;
+                w[n][k] = weight_exponent(sc[n][k], mk[n][k & 1], m[n][k & 1]);
                 if (!whole) {
-                    const int key = ka + (k & 2);
+                    const int key = key0 + kr + (k & 2);
                     const bool seen = in_page && key < s.len && key <= pos[n][k & 1] && (p.window <= 0 || key > pos[n][k & 1] - p.window);
-                    if (!seen) sc[n][k] = -INFINITY;
+                    if (!seen) w[n][k] = -INFINITY;
                 }
             }
-            up |= fmaxf(sc[n][0], sc[n][2]) > m[n][0] + 8.f || fmaxf(sc[n][1], sc[n][3]) > m[n][1] + 8.f;
+            up |= fmaxf(w[n][0], w[n][2]) > thr[n][0] || fmaxf(w[n][1], w[n][3]) > thr[n][1];
         }
         if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    float x = fmaxf(sc[n][k], sc[n][k + 2]);
+                    float x = fmaxf(w[n][k], w[n][k + 2]);
 #pragma unroll
                     for (int d = 4; d < 32; d *= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
-                    x = fmaxf(m[n][k], x);
-                    const float f = m[n][k] == -INFINITY ? 0.f : ex2(m[n][k] - x);
-                    m[n][k] = x;
+                    // x is relative to the maximum so far; before the first key there is none
+                    const bool begun = thr[n][k] > 0.f;
+                    if (x == -INFINITY || (begun && x <= 0.f)) continue;
+                    const float f = begun ? ex2(-x) : 0.f;
+                    m[n][k] += x;
+                    thr[n][k] = 8.f;
                     l[n][k] *= f;
 #pragma unroll
                     for (int u = 0; u < TILES; ++u) {
                         o[n][u][k] *= f;
                         o[n][u][k + 2] *= f;
                     }
+                    if (w[n][k] != -INFINITY) w[n][k] = weight_exponent(sc[n][k], mk[n][k], m[n][k]);
+                    if (w[n][k + 2] != -INFINITY) w[n][k + 2] = weight_exponent(sc[n][k + 2], mk[n][k], m[n][k]);
                 }
             }
         }
         uint32_t pb[NQ][2];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-            float w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                // a row without a key so far: every score is -inf (or NaN, which stays)
-                const float base = m[n][k & 1] == -INFINITY ? 0.f : m[n][k & 1];
-                w[k] = ex2(sc[n][k] - base);
-            }
-            l[n][0] += w[0] + w[2];
-            l[n][1] += w[1] + w[3];
-            pb[n][0] = transpose8x8(pack_h2(w[0], w[1]));
-            pb[n][1] = transpose8x8(pack_h2(w[2], w[3]));
+            for (int k = 0; k < 4; ++k) w[n][k] = ex2(w[n][k]);
+            l[n][0] += w[n][0] + w[n][2];
+            l[n][1] += w[n][1] + w[n][3];
+            pb[n][0] = transpose8x8(pack_h2(w[n][0], w[n][1]));
+            pb[n][1] = transpose8x8(pack_h2(w[n][2], w[n][3]));
         }
         // ---- sums: dimensions x rows ----
         {
-            const uint32_t f0 = pack_h2(rel_scale((int)cur.vs[0], vref), rel_scale((int)cur.vs[1], vref));
-            const uint32_t f1 = pack_h2(rel_scale((int)cur.vs[2], vref), rel_scale((int)cur.vs[3], vref));
+            const uint32_t f0 = pack_h2(rel_scale((int)vs[0], vref), rel_scale((int)vs[1], vref));
+            const uint32_t f1 = pack_h2(rel_scale((int)vs[2], vref), rel_scale((int)vs[3], vref));
+            uint32_t vw[4][D / 64];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (D == 128) {
+                    const uint2 x = lds64(stage + S::v_at(4 * t + i, g >> 1) + 8 * (g & 1));
+                    vw[i][0] = x.x;
+                    vw[i][1] = x.y;
+                } else {
+                    vw[i][0] = lds32(stage + S::v_at(4 * t + i, g >> 2) + 4 * (g & 3));
+                }
+            }
 #pragma unroll
             for (int j = 0; j < D / 64; ++j) {
                 uint32_t e0[4], e1[4], d0[4], d1[4];  // even, odd dimensions of keys 4t, 4t + 1 and 4t + 2, 4t + 3
-                e2m1_to_h2((cur.v[0][j] & 0x0F0F0F0Fu) | ((cur.v[1][j] << 4) & 0xF0F0F0F0u), e0);
-                e2m1_to_h2((cur.v[2][j] & 0x0F0F0F0Fu) | ((cur.v[3][j] << 4) & 0xF0F0F0F0u), e1);
-                e2m1_to_h2(((cur.v[0][j] >> 4) & 0x0F0F0F0Fu) | (cur.v[1][j] & 0xF0F0F0F0u), d0);
-                e2m1_to_h2(((cur.v[2][j] >> 4) & 0x0F0F0F0Fu) | (cur.v[3][j] & 0xF0F0F0F0u), d1);
+                e2m1_to_h2((vw[0][j] & 0x0F0F0F0Fu) | ((vw[1][j] << 4) & 0xF0F0F0F0u), e0);
+                e2m1_to_h2((vw[2][j] & 0x0F0F0F0Fu) | ((vw[3][j] << 4) & 0xF0F0F0F0u), e1);
+                e2m1_to_h2(((vw[0][j] >> 4) & 0x0F0F0F0Fu) | (vw[1][j] & 0xF0F0F0F0u), d0);
+                e2m1_to_h2(((vw[2][j] >> 4) & 0x0F0F0F0Fu) | (vw[3][j] & 0xF0F0F0F0u), d1);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t a0 = mul_h2(e0[k], f0), a1 = mul_h2(d0[k], f0), a2 = mul_h2(e1[k], f1), a3 = mul_h2(d1[k], f1);
@@ -513,11 +561,18 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
                 }
             }
         }
+        stage = stage + S::BYTES == ring + kAtStages * S::BYTES ? ring : stage + S::BYTES;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");  // (the last ones are empty)
+    // from here on a row without a key has the maximum -inf
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (!(thr[n][k] > 0.f)) m[n][k] = -INFINITY;
 
     // ---- join the warps ----
     const float vtrue = vref > -1000 ? pow2i(vref - 127) : 0.f;
-    if constexpr (QS) __syncthreads();  // every warp is done with the queries: their memory takes the results
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -619,25 +674,30 @@ struct Plan {
     int nq, row_tiles, splits;
     long long tiles;
 };
-// rows of a key head in eights, and the keys in as many splits as give each SM about four CTAs, none below
-// kAtMinGroups groups of 16 keys
+// Rows of a key head in eights, and the keys in splits. Where few tiles have few keys, one wave of CTAs of at least
+// kAtMinGroups groups of 16 keys; otherwise about four waves of CTAs of 32 groups or more, so that sequences of
+// different lengths even out.
 Plan plan_of(const KvCache& c, long long batch, int max_q, int heads, long long max_keys, int sms) {
     Plan p;
     const long long rows = (long long)max_q * (heads / c.heads);
     p.nq = nq_of(rows);
     p.row_tiles = (int)((rows + 8 * p.nq - 1) / (8 * p.nq));
     p.tiles = batch * c.heads * p.row_tiles;
-    const long long groups = (max_keys + 15) / 16;
-    long long want = (long long)sms * (p.nq == 4 ? 2 : 4) / (p.tiles > 0 ? p.tiles : 1);
-    if (want > groups / kAtMinGroups) want = groups / kAtMinGroups;
+    const long long groups = (max_keys + 15) / 16, tiles = p.tiles > 0 ? p.tiles : 1;
+    const long long places = (long long)sms * (p.nq == 4 ? 2 : p.nq == 2 ? 3 : 4);
+    long long one = places / tiles, four = 4 * places / tiles;
+    if (one > groups / kAtMinGroups) one = groups / kAtMinGroups;
+    if (four > groups / 32) four = groups / 32;
+    long long want = one > four ? one : four;
     if (want > kAtMaxSplits) want = kAtMaxSplits;
     p.splits = want < 1 ? 1 : (int)want;
     return p;
 }
 
 template <int D, int NQ> cudaError_t go(const AtArgs& a, long long tiles, int dev, cudaStream_t st) {
-    constexpr int RES = kAtWarps * 8 * NQ * (D + 4) * 4, QB = NQ == 4 ? NQ * (D / 16) * 32 * 8 : 0;
-    constexpr int SMEM = RES > QB ? RES : QB;
+    constexpr int RES = kAtWarps * 8 * NQ * (D + 4) * 4;
+    constexpr int IN = kAtWarps * kAtStages * AtStage<D>::BYTES + (NQ == 4 ? NQ * (D / 16) * 32 * 8 : 0);
+    constexpr int SMEM = RES > IN ? RES : IN;
     auto* kern = k_kv_attention<D, NQ>;
     if (SMEM > 47 * 1024) {
         static std::atomic<unsigned long long> ready{0};
