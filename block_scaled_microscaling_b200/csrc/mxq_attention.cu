@@ -22,8 +22,10 @@
 // - the running maximum m_r is raised only when a score exceeds it by 2^8 (one vote per 16 keys); the weights
 //   then are at most 2^8 and round to f16 (relative error 2^-12; below 2^-14 absolute, 2^-25).
 // The four warps of a CTA take every fourth group (page numbers are fetched 32 groups at a time); their results are
-// joined through shared memory, and a long sequence is split over several CTAs whose partial sums a second kernel
-// joins in order.
+// joined through shared memory. Where one row tile holds a sequence's queries (decoding), the groups of all sequences
+// and heads are cut into equal shares, one per resident CTA, whatever the lengths: a CTA walks the pieces of its
+// share, and the at most two of them that are part of a split sequence leave their sums to a second kernel, which
+// joins them in order. Otherwise a long sequence is split over a fixed number of CTAs, joined the same way.
 #include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -41,10 +43,25 @@ constexpr int kAtWarps = 4, kAtThreads = 32 * kAtWarps;
 constexpr int kAtMinGroups = 8;    // groups of 16 keys that a split has at least
 constexpr int kAtStages = 4;       // groups in a warp's ring
 constexpr int kAtMaxSplits = 256;
+constexpr int kAtMaxEven = 512;    // sequences whose shares are worked out by every CTA
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// n / d for 0 <= n < 2^31: with l = ceil(log2 d) and mul = ceil(2^(31 + l) / d), n * mul >> (31 + l) is exact
+struct FastDiv {
+    uint32_t mul, sh;
+    FastDiv() : mul(1u << 31), sh(31) {}
+    explicit FastDiv(uint32_t d) {
+        uint32_t l = 0;
+        while ((1ull << l) < d) ++l;
+        sh = 31 + l;
+        mul = (uint32_t)(((1ull << sh) + d - 1) / d);
+    }
+    __device__ __forceinline__ int operator()(int n) const { return (int)(((unsigned long long)(uint32_t)n * mul) >> sh); }
+};
 
 struct AtArgs {
     KvCache c;
+    FastDiv by_group, by_page, by_splits, by_tiles, by_heads;
     const __nv_bfloat16* q;
     long long q_rows, q_row_stride, q_head_stride;
     const int* starts;
@@ -54,10 +71,14 @@ struct AtArgs {
     long long max_keys;
     int batch, heads, group, max_q, window, splits, row_tiles;
     bool fill;
+    bool even;     // equal shares of all groups (one row tile per sequence and head)
+    int4* info;    // even: of each share's first piece if its sequence began in an earlier share: sequence, head, whether
+                   // that was the share just before, last share of the sequence; else sequence -1
     float scale;   // already times log2(e)
     __nv_bfloat16* out;
     float* lse;
-    float* part;   // [(sequence, key head, row tile)][split][rows][D] sums, then their [..][rows][2] maximum and total
+    float* part;   // pieces' [rows][D] sums, then their [rows][2] maximum and total; piece of split s of tile t: t * splits
+                   // + s; even: 2 c for the first piece of share c if its sequence began earlier, 2 c + 1 for its last
     long long part_ml;  // offset of the latter
 };
 
@@ -95,26 +116,21 @@ __device__ __forceinline__ Groups groups_of(const AtArgs& p, const Span& s, int 
     return g;
 }
 
-// zeros (and -inf) for the rows of this key head's queries that no CTA computes: before the first sequence, beyond
-// max_q in each, behind the last
-template <int D> __device__ void fill_rows(const AtArgs& p, const Span& s, int b, int head) {
-    for (int part = 0; part < 3; ++part) {
-        int lo = s.q0 + s.nq, hi = s.q0 + s.n;
-        if (part == 1) {
-            lo = 0;
-            hi = b == 0 ? s.q0 : 0;
-        } else if (part == 2) {
-            lo = s.q0 + s.n;
-            hi = b == p.batch - 1 ? (int)p.q_rows : lo;
-        }
-        for (int r = lo; r < hi; ++r) {
-            const long long at = (long long)r * p.heads + head * p.group;
-            for (int i = threadIdx.x; i < p.group * (D / 8); i += kAtThreads)
-                reinterpret_cast<uint4*>(p.out + at * D)[i] = make_uint4(0, 0, 0, 0);
-            if (p.lse)
-                for (int i = threadIdx.x; i < p.group; i += kAtThreads) p.lse[at + i] = -INFINITY;
-        }
+// zeros (and -inf) for rows lo .. hi of out, `nh` heads from h0 on
+template <int D> __device__ void zero_rows(const AtArgs& p, int lo, int hi, int h0, int nh) {
+    for (int r = lo; r < hi; ++r) {
+        const long long at = (long long)r * p.heads + h0;
+        for (int i = threadIdx.x; i < nh * (D / 8); i += kAtThreads)
+            reinterpret_cast<uint4*>(p.out + at * D)[i] = make_uint4(0, 0, 0, 0);
+        if (p.lse)
+            for (int i = threadIdx.x; i < nh; i += kAtThreads) p.lse[at + i] = -INFINITY;
     }
+}
+// the rows that no CTA computes: beyond max_q in each sequence, before the first sequence, behind the last
+template <int D> __device__ void fill_rows(const AtArgs& p, const Span& s, int b, int h0, int nh) {
+    zero_rows<D>(p, s.q0 + s.nq, s.q0 + s.n, h0, nh);
+    if (b == 0) zero_rows<D>(p, 0, s.q0, h0, nh);
+    if (b == p.batch - 1) zero_rows<D>(p, s.q0 + s.n, (int)p.q_rows, h0, nh);
 }
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -211,32 +227,26 @@ template <int D> __device__ __forceinline__ void fetch(const KvCache& c, long lo
 // writes (dimensions g D/8 .., rows 2t, 2t + 1) meet in a bank at most in pairs
 template <int D> __device__ __forceinline__ int res_off(int r, int d) { return r * (D + 4) + d; }
 
+// keys 16 first .. 16 last of one sequence and head for the rows of a tile
+struct Piece {
+    Span s;
+    int b, head, r0;
+    int first, last;
+    bool alone;       // all of the tile's keys: the output itself is written
+    long long slot;   // else the place of the partial sums
+};
+
 // NQ: groups of eight rows that a warp handles together (their Q operands in shared memory when NQ is 4)
-template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ? 2 : NQ == 2 ? 3 : 4) k_kv_attention(const AtArgs p) {
+template <int D, int NQ> __device__ __forceinline__ void attend(const AtArgs& p, const Piece& w) {
     constexpr int ROWS = 8 * NQ, STEPS = D / 16, TILES = D / 16;
     constexpr bool QS = NQ == 4;
     using S = AtStage<D>;
     extern __shared__ __align__(16) float dsm[];  // stages of the warps, Q's operands; later the warps' results
     __shared__ float sm_m[kAtWarps][ROWS], sm_l[kAtWarps][ROWS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    pdl_wait_then_release();
-    int id = blockIdx.x;
-    const int sp = id % p.splits;
-    id /= p.splits;
-    const int tile_id = id;
-    const int rt = id % p.row_tiles;
-    id /= p.row_tiles;
-    const int head = id % p.c.heads, b = id / p.c.heads;
-
-    const Span s = span_of(p, b);
-    const int rows = s.nq * p.group, r0 = rt * ROWS;
-    if (p.fill && rt == 0 && sp == 0) fill_rows<D>(p, s, b, head);
-    if (r0 >= rows) return;
-    const int i0 = r0 / p.group, i1 = (min(r0 + ROWS, rows) - 1) / p.group;
-    const Groups gr = groups_of(p, s, i0, i1);
-    const int first = gr.lo + sp * gr.per, last = min(first + gr.per, gr.hi);
-    const bool alone = gr.hi - gr.lo <= gr.per;  // one split holds all keys: it writes the output itself
-    if (first >= last && sp > 0) return;
+    const Span& s = w.s;
+    const int b = w.b, head = w.head, r0 = w.r0, rows = s.nq * p.group, first = w.first, last = w.last;
+    const int i0 = p.by_group(r0), i1 = p.by_group(min(r0 + ROWS, rows) - 1);
 
     // ---- the rows' queries: lane (g, t) holds row g of each eight, dimensions t D/4 .., divided by 2^e ----
     uint32_t qf[QS ? 1 : NQ][STEPS][2];
@@ -246,25 +256,25 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
         const int r = r0 + 8 * n + g;
-        uint32_t w[D / 8];
+        uint32_t x8[D / 8];
         if (r < rows) {
-            const int i = r / p.group, h = head * p.group + (r - i * p.group);
+            const int i = p.by_group(r), h = head * p.group + (r - i * p.group);
             const uint4* src = reinterpret_cast<const uint4*>(p.q + (s.q0 + i) * p.q_row_stride + h * p.q_head_stride + t * (D / 4));
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
                 const uint4 x = __ldg(src + j);
-                w[4 * j] = x.x;
-                w[4 * j + 1] = x.y;
-                w[4 * j + 2] = x.z;
-                w[4 * j + 3] = x.w;
+                x8[4 * j] = x.x;
+                x8[4 * j + 1] = x.y;
+                x8[4 * j + 2] = x.z;
+                x8[4 * j + 3] = x.w;
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j) w[j] = 0;
+            for (int j = 0; j < D / 8; ++j) x8[j] = 0;
         }
         uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) top = max(top, max((w[j] & 0x7FFFu) << 16, w[j] & 0x7FFF0000u));
+        for (int j = 0; j < D / 8; ++j) top = max(top, max((x8[j] & 0x7FFFu) << 16, x8[j] & 0x7FFF0000u));
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
         const int e = min(max((int)(top >> 23), 1), 253) - 127;
@@ -274,7 +284,7 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
             uint32_t f[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const uint32_t x = w[2 * st + k];
+                const uint32_t x = x8[2 * st + k];
                 f[k] = pack_h2(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xFFFF0000u) * down);
             }
             if constexpr (QS) {
@@ -288,7 +298,7 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
         for (int k = 0; k < 2; ++k) {
             const int col = 2 * t + k, rr = r0 + 8 * n + col;
             mul[n][k] = p.scale * pow2i(__shfl_sync(0xFFFFFFFFu, e, 4 * col));
-            pos[n][k] = rr < rows ? s.len - s.n + rr / p.group : -1;
+            pos[n][k] = rr < rows ? s.len - s.n + p.by_group(rr) : -1;
         }
     }
     if constexpr (QS) __syncthreads();
@@ -327,8 +337,8 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
             const int grp = first + warp + (issued + lane) * kAtWarps;
             pages = -1;
             if (grp < last) {
-                const uint32_t key = 16u * (uint32_t)grp, at = key / (uint32_t)p.c.page;
-                offs = (int)(key - at * (uint32_t)p.c.page);
+                const int key = 16 * grp, at = p.by_page(key);
+                offs = key - at * p.c.page;
                 const int pg = __ldg(p.table + b * p.table_stride + at);
                 pages = pg >= 0 && pg < p.c.pages ? pg : -1;
             }
@@ -481,27 +491,27 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
             }
         }
         // ---- weights ----
-        float w[NQ][4];
+        float e[NQ][4];
         bool up = false;
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                w[n][k] = weight_exponent(sc[n][k], mk[n][k & 1], m[n][k & 1]);
+                e[n][k] = weight_exponent(sc[n][k], mk[n][k & 1], m[n][k & 1]);
                 if (!whole) {
                     const int key = key0 + kr + (k & 2);
                     const bool seen = in_page && key < s.len && key <= pos[n][k & 1] && (p.window <= 0 || key > pos[n][k & 1] - p.window);
-                    if (!seen) w[n][k] = -INFINITY;
+                    if (!seen) e[n][k] = -INFINITY;
                 }
             }
-            up |= fmaxf(w[n][0], w[n][2]) > thr[n][0] || fmaxf(w[n][1], w[n][3]) > thr[n][1];
+            up |= fmaxf(e[n][0], e[n][2]) > thr[n][0] || fmaxf(e[n][1], e[n][3]) > thr[n][1];
         }
         if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    float x = fmaxf(w[n][k], w[n][k + 2]);
+                    float x = fmaxf(e[n][k], e[n][k + 2]);
 #pragma unroll
                     for (int d = 4; d < 32; d *= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
                     // x is relative to the maximum so far; before the first key there is none
@@ -516,8 +526,8 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
                         o[n][u][k] *= f;
                         o[n][u][k + 2] *= f;
                     }
-                    if (w[n][k] != -INFINITY) w[n][k] = weight_exponent(sc[n][k], mk[n][k], m[n][k]);
-                    if (w[n][k + 2] != -INFINITY) w[n][k + 2] = weight_exponent(sc[n][k + 2], mk[n][k], m[n][k]);
+                    if (e[n][k] != -INFINITY) e[n][k] = weight_exponent(sc[n][k], mk[n][k], m[n][k]);
+                    if (e[n][k + 2] != -INFINITY) e[n][k + 2] = weight_exponent(sc[n][k + 2], mk[n][k], m[n][k]);
                 }
             }
         }
@@ -525,11 +535,11 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[n][k] = ex2(w[n][k]);
-            l[n][0] += w[n][0] + w[n][2];
-            l[n][1] += w[n][1] + w[n][3];
-            pb[n][0] = transpose8x8(pack_h2(w[n][0], w[n][1]));
-            pb[n][1] = transpose8x8(pack_h2(w[n][2], w[n][3]));
+            for (int k = 0; k < 4; ++k) e[n][k] = ex2(e[n][k]);
+            l[n][0] += e[n][0] + e[n][2];
+            l[n][1] += e[n][1] + e[n][3];
+            pb[n][0] = transpose8x8(pack_h2(e[n][0], e[n][1]));
+            pb[n][1] = transpose8x8(pack_h2(e[n][2], e[n][3]));
         }
         // ---- sums: dimensions x rows ----
         {
@@ -593,7 +603,7 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
             const int r = 8 * n + 2 * t + k;
             float top = sm_m[0][r];
 #pragma unroll
-            for (int w = 1; w < kAtWarps; ++w) top = fmaxf(top, sm_m[w][r]);
+            for (int q = 1; q < kAtWarps; ++q) top = fmaxf(top, sm_m[q][r]);
             // a warp without a visible key has sums of 0 (or NaN, which stays)
             float f = (m[n][k] == -INFINITY ? 1.f : ex2(m[n][k] - top)) * vtrue;
             if (vnan & (1u << (2 * n + k))) f = __uint_as_float(0x7FC00000u);
@@ -609,30 +619,173 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
         if (r0 + r >= rows) break;
         float top = sm_m[0][r];
 #pragma unroll
-        for (int w = 1; w < kAtWarps; ++w) top = fmaxf(top, sm_m[w][r]);
+        for (int q = 1; q < kAtWarps; ++q) top = fmaxf(top, sm_m[q][r]);
         float total = 0.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kAtWarps; ++w) {
-            total += sm_l[w][r] * (sm_m[w][r] == -INFINITY ? 1.f : ex2(sm_m[w][r] - top));
-            const float4 x = *reinterpret_cast<const float4*>(dsm + w * ROWS * (D + 4) + res_off<D>(r, d));
+        for (int q = 0; q < kAtWarps; ++q) {
+            total += sm_l[q][r] * (sm_m[q][r] == -INFINITY ? 1.f : ex2(sm_m[q][r] - top));
+            const float4 x = *reinterpret_cast<const float4*>(dsm + q * ROWS * (D + 4) + res_off<D>(r, d));
             a.x += x.x;
             a.y += x.y;
             a.z += x.z;
             a.w += x.w;
         }
-        if (alone) {
+        if (w.alone) {
             const float inv = total == 0.f ? 0.f : 1.f / total;
-            const int tok = (r0 + r) / p.group, h = head * p.group + (r0 + r - tok * p.group);
+            const int tok = p.by_group(r0 + r), h = head * p.group + (r0 + r - tok * p.group);
             const long long at = (long long)(s.q0 + tok) * p.heads + h;
             *reinterpret_cast<uint2*>(p.out + at * D + d) = make_uint2(bf16x2(a.x * inv, a.y * inv), bf16x2(a.z * inv, a.w * inv));
             if (p.lse && d == 0) p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
         } else {
-            const long long at = ((long long)tile_id * p.splits + sp) * ROWS + r;
+            const long long at = w.slot * ROWS + r;
             *reinterpret_cast<float4*>(p.part + at * D + d) = a;
             if (d == 0) *reinterpret_cast<float2*>(p.part + p.part_ml + at * 2) = make_float2(top, total);
         }
     }
+}
+
+// groups that the queries of sequence b see
+__device__ __forceinline__ Groups groups_in(const AtArgs& p, const Span& s) {
+    if (s.nq > 0) return groups_of(p, s, 0, s.nq - 1);
+    return {0, 0, 0};
+}
+
+// the share of CTA blockIdx.x of all groups, (sequence, head, group) in order
+template <int D, int NQ> __device__ __forceinline__ void attend_share(const AtArgs& p) {
+    __shared__ long long pre[kAtMaxEven + 1];  // groups of the sequences before, one head
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    constexpr int PER = kAtMaxEven / kAtThreads;
+    int n[PER], sum = 0;  // 2^27 groups a sequence at most; the sums below are 64-bit where they can pass 32
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int b = t * PER + i;
+        n[i] = 0;
+        if (b < p.batch) {
+            const Groups g = groups_in(p, span_of(p, b));
+            n[i] = g.hi - g.lo;
+        }
+        sum += n[i];
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += x;
+    }
+    __shared__ long long warp_total[kAtWarps];
+    if (lane == 31) warp_total[warp] = incl;
+    __syncthreads();
+    long long at = incl - sum;
+    for (int w = 0; w < warp; ++w) at += warp_total[w];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int b = t * PER + i;
+        if (b <= p.batch) pre[b] = at;
+        at += n[i];
+    }
+    if (t == kAtThreads - 1 && p.batch == kAtMaxEven) pre[kAtMaxEven] = at;
+    __syncthreads();
+    // sequences without a key, and rows that nobody computes
+    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+        const bool none = pre[b + 1] == pre[b];
+        if (none || p.fill) {
+            const Span s = span_of(p, b);
+            if (none) zero_rows<D>(p, s.q0, s.q0 + s.nq, 0, p.heads);
+            if (p.fill) fill_rows<D>(p, s, b, 0, p.heads);
+        }
+    }
+    const long long total = pre[p.batch] * p.c.heads;
+    const long long shares = min((long long)gridDim.x, (total + kAtMinGroups - 1) / kAtMinGroups), c = blockIdx.x;
+    int4 info = make_int4(-1, 0, 0, 0);
+    if (c < shares) {
+        const long long end = total * (c + 1) / shares;
+        long long u = total * c / shares;
+        for (bool begin = true; u < end; begin = false) {
+            int lo = 0, hi = p.batch - 1;  // the last sequence that begins at or before u (those without a group lie before it)
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (pre[mid] * p.c.heads <= u) lo = mid;
+                else hi = mid - 1;
+            }
+            Piece w;
+            w.b = lo;
+            const int len = (int)(pre[lo + 1] - pre[lo]);
+            const long long rel = u - pre[lo] * p.c.heads;
+            w.head = (int)(rel / len);
+            const int g0 = (int)(rel - (long long)w.head * len), g1 = (int)min((long long)len, g0 + (end - u));
+            w.s = span_of(p, lo);
+            w.r0 = 0;
+            const Groups g = groups_in(p, w.s);
+            w.first = g.lo + g0;
+            w.last = g.lo + g1;
+            w.alone = g0 == 0 && g1 == len;
+            w.slot = 2 * c + (g0 > 0 ? 0 : 1);
+            if (begin && g0 > 0) {
+                const long long t0 = u - g0, t1 = t0 + len;  // the tile's units; shares c' with total c' / shares <= unit
+                info = make_int4(lo, w.head, total * (c - 1) / shares <= t0, (int)((t1 * shares - 1) / total));
+            }
+            if (!begin) __syncthreads();  // the piece before is out of shared memory
+            attend<D, NQ>(p, w);
+            u += g1 - g0;
+        }
+    }
+    if (t == 0) p.info[c] = info;
+}
+
+template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ? 2 : NQ == 2 ? 3 : 4) k_kv_attention(const AtArgs p) {
+    pdl_wait_then_release();
+    if (NQ < 4 && p.even) {
+        attend_share<D, NQ>(p);
+        return;
+    }
+    Piece w;
+    const int tile = p.by_splits(blockIdx.x), sp = blockIdx.x - tile * p.splits;
+    const int bh = p.by_tiles(tile), rt = tile - bh * p.row_tiles;
+    w.b = p.by_heads(bh);
+    w.head = bh - w.b * p.c.heads;
+    w.s = span_of(p, w.b);
+    const int rows = w.s.nq * p.group;
+    w.r0 = rt * 8 * NQ;
+    if (p.fill && rt == 0 && sp == 0) fill_rows<D>(p, w.s, w.b, w.head * p.group, p.group);
+    if (w.r0 >= rows) return;
+    const Groups gr = groups_of(p, w.s, p.by_group(w.r0), p.by_group(min(w.r0 + 8 * NQ, rows) - 1));
+    w.first = gr.lo + sp * gr.per;
+    w.last = min(w.first + gr.per, gr.hi);
+    w.alone = gr.hi - gr.lo <= gr.per;  // one split holds all keys
+    w.slot = blockIdx.x;
+    if (w.first >= w.last && sp > 0) return;
+    attend<D, NQ>(p, w);
+}
+
+// the sequences that shares split: share c's first piece names one; the share where it was split first joins it.
+// 256 threads take 256 / D rows, one dimension each.
+template <int D, int NQ> __global__ void __launch_bounds__(256) k_kv_attention_join_shares(const AtArgs p) {
+    constexpr int ROWS = 8 * NQ;
+    pdl_wait_then_release();
+    const int c = blockIdx.x + 1;
+    const int4 info = __ldcg(p.info + c);
+    if (info.x < 0 || !info.z) return;
+    const int d = threadIdx.x % D, row = blockIdx.y * (256 / D) + threadIdx.x / D;
+    const Span s = span_of(p, info.x);
+    if (row >= s.nq * p.group) return;
+    // pieces: the last of share c - 1, the first of shares c .. info.w
+    auto slot = [&](int q) { return (q < c ? 2LL * q + 1 : 2LL * q) * ROWS + row; };
+    const float* const ml = p.part + p.part_ml;
+    float top = -INFINITY;
+    for (int q = c - 1; q <= info.w; ++q) top = fmaxf(top, __ldcg(ml + slot(q) * 2));
+    float total = 0.f, sum = 0.f;
+#pragma unroll 4
+    for (int q = c - 1; q <= info.w; ++q) {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(ml + slot(q) * 2));
+        const float f = x.x == -INFINITY ? 1.f : ex2(x.x - top);
+        total += x.y * f;
+        sum += __ldcg(p.part + slot(q) * D + d) * f;
+    }
+    const int i = p.by_group(row), h = info.y * p.group + row - i * p.group;
+    const long long at = (long long)(s.q0 + i) * p.heads + h;
+    p.out[at * D + d] = __float2bfloat16_rn(total == 0.f ? 0.f : sum / total);
+    if (p.lse && d == 0) p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
 }
 
 // join the splits of one row: CTA (sequence, query, head), one thread per dimension
@@ -671,46 +824,54 @@ template <int D, int NQ> __global__ void __launch_bounds__(D) k_kv_attention_joi
 int nq_of(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 struct Plan {
-    int nq, row_tiles, splits;
-    long long tiles;
+    int nq, row_tiles, splits, shares;  // shares > 0: equal shares instead of splits
+    long long tiles, pieces;            // places for partial sums
 };
-// Rows of a key head in eights, and the keys in splits. Where few tiles have few keys, one wave of CTAs of at least
-// kAtMinGroups groups of 16 keys; otherwise about four waves of CTAs of 32 groups or more, so that sequences of
-// different lengths even out.
+// Rows of a key head in eights. One row tile per sequence: equal shares, one per place (16 sequences of 24576 to 32768
+// keys: 145 us, 156 with splits). Otherwise, and for one sequence, where working out the shares only takes time (4000
+// keys: 14.4 us against 20.2), the keys in splits of at least kAtMinGroups groups of 16 keys for one wave of CTAs, or of
+// 32 groups or more for about two.
 Plan plan_of(const KvCache& c, long long batch, int max_q, int heads, long long max_keys, int sms) {
-    Plan p;
+    Plan p{};
     const long long rows = (long long)max_q * (heads / c.heads);
     p.nq = nq_of(rows);
     p.row_tiles = (int)((rows + 8 * p.nq - 1) / (8 * p.nq));
     p.tiles = batch * c.heads * p.row_tiles;
+    p.splits = 1;
     const long long groups = (max_keys + 15) / 16, tiles = p.tiles > 0 ? p.tiles : 1;
     const long long places = (long long)sms * (p.nq == 4 ? 2 : p.nq == 2 ? 3 : 4);
-    long long one = places / tiles, four = 4 * places / tiles;
+    if (p.nq < 4 && batch > 1 && batch <= kAtMaxEven && groups > kAtMinGroups) {
+        const long long most = (tiles * groups + kAtMinGroups - 1) / kAtMinGroups;
+        p.shares = (int)(most < places ? most : places);
+        p.pieces = 2LL * p.shares;
+        return p;
+    }
+    long long one = places / tiles, two = 2 * places / tiles;
     if (one > groups / kAtMinGroups) one = groups / kAtMinGroups;
-    if (four > groups / 32) four = groups / 32;
-    long long want = one > four ? one : four;
+    if (two > groups / 32) two = groups / 32;
+    long long want = one > two ? one : two;
     if (want > kAtMaxSplits) want = kAtMaxSplits;
-    p.splits = want < 1 ? 1 : (int)want;
+    if (want > 1) p.splits = (int)want;
+    p.pieces = p.splits > 1 ? p.tiles * p.splits : 0;
     return p;
 }
 
-template <int D, int NQ> cudaError_t go(const AtArgs& a, long long tiles, int dev, cudaStream_t st) {
+template <int D, int NQ> cudaError_t go(const AtArgs& a, const Plan& pl, int dev, cudaStream_t st) {
     constexpr int RES = kAtWarps * 8 * NQ * (D + 4) * 4;
     constexpr int IN = kAtWarps * kAtStages * AtStage<D>::BYTES + (NQ == 4 ? NQ * (D / 16) * 32 * 8 : 0);
     constexpr int SMEM = RES > IN ? RES : IN;
     auto* kern = k_kv_attention<D, NQ>;
-    if (SMEM > 47 * 1024) {
-        static std::atomic<unsigned long long> ready{0};
-        const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-        if (!(ready.load(std::memory_order_acquire) & bit)) {
-            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-            if (e != cudaSuccess) return e;
-            ready.fetch_or(bit, std::memory_order_release);
-        }
+    static std::atomic<unsigned long long> ready{0};
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
     }
-    if (tiles * a.splits > 0x7FFFFFFFLL || (long long)a.batch * a.max_q * a.heads > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    const long long rows = (long long)a.batch * a.max_q * a.heads;
+    if (pl.tiles * a.splits > 0x7FFFFFFFLL || rows > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * a.splits));
+    cfg.gridDim = dim3((unsigned)(pl.shares > 0 ? pl.shares : pl.tiles * a.splits));
     cfg.blockDim = dim3(kAtThreads);
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = st;
@@ -720,10 +881,15 @@ template <int D, int NQ> cudaError_t go(const AtArgs& a, long long tiles, int de
     cfg.attrs = at;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
-    if (e != cudaSuccess || a.splits == 1) return e;
-    cfg.gridDim = dim3((unsigned)((long long)a.batch * a.max_q * a.heads));
-    cfg.blockDim = dim3(D);
+    if (e != cudaSuccess || pl.pieces == 0 || pl.shares == 1) return e;
     cfg.dynamicSmemBytes = 0;
+    if (pl.shares > 0) {
+        cfg.gridDim = dim3((unsigned)(pl.shares - 1), (unsigned)((a.max_q * a.group + 256 / D - 1) / (256 / D)));
+        cfg.blockDim = dim3(256);
+        return cudaLaunchKernelEx(&cfg, k_kv_attention_join_shares<D, NQ>, a);
+    }
+    cfg.gridDim = dim3((unsigned)rows);
+    cfg.blockDim = dim3(D);
     return cudaLaunchKernelEx(&cfg, k_kv_attention_join<D, NQ>, a);
 }
 
@@ -742,8 +908,7 @@ long long kv_attention_workspace(const KvCache& c, long long batch, int max_q, i
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
     const Plan p = plan_of(c, batch, max_q, heads, max_keys, sm_count(dev));
-    if (p.splits == 1) return 0;
-    return p.tiles * p.splits * 8 * p.nq * (c.db * 32 + 2) * 4;
+    return p.pieces * 8 * p.nq * (c.db * 32 + 2) * 4 + p.shares * (long long)sizeof(int4);
 }
 
 cudaError_t launch_kv_attention(const KvAttention& x, cudaStream_t st) {
@@ -774,15 +939,22 @@ cudaError_t launch_kv_attention(const KvAttention& x, cudaStream_t st) {
     a.out = static_cast<__nv_bfloat16*>(x.out);
     a.lse = x.lse;
     a.part = static_cast<float*>(x.workspace);
-    a.part_ml = pl.tiles * pl.splits * 8 * pl.nq * (x.c.db * 32);
+    a.part_ml = pl.pieces * 8 * pl.nq * (x.c.db * 32);
+    a.even = pl.shares > 0;
+    a.info = reinterpret_cast<int4*>(a.part + pl.pieces * 8 * pl.nq * (x.c.db * 32 + 2));
+    a.by_group = FastDiv((uint32_t)a.group);
+    a.by_page = FastDiv((uint32_t)x.c.page);
+    a.by_splits = FastDiv((uint32_t)pl.splits);
+    a.by_tiles = FastDiv((uint32_t)pl.row_tiles);
+    a.by_heads = FastDiv((uint32_t)x.c.heads);
     if (x.c.db == 4) {
-        if (pl.nq == 1) return go<128, 1>(a, pl.tiles, dev, st);
-        if (pl.nq == 2) return go<128, 2>(a, pl.tiles, dev, st);
-        return go<128, 4>(a, pl.tiles, dev, st);
+        if (pl.nq == 1) return go<128, 1>(a, pl, dev, st);
+        if (pl.nq == 2) return go<128, 2>(a, pl, dev, st);
+        return go<128, 4>(a, pl, dev, st);
     }
-    if (pl.nq == 1) return go<64, 1>(a, pl.tiles, dev, st);
-    if (pl.nq == 2) return go<64, 2>(a, pl.tiles, dev, st);
-    return go<64, 4>(a, pl.tiles, dev, st);
+    if (pl.nq == 1) return go<64, 1>(a, pl, dev, st);
+    if (pl.nq == 2) return go<64, 2>(a, pl, dev, st);
+    return go<64, 4>(a, pl, dev, st);
 }
 
 }  // namespace mxq

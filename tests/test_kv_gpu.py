@@ -181,9 +181,9 @@ def check(q, c, table, lens, starts=None, window=0, scale=None, max_q=None, **kw
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("kv,group", [(1, 1), (2, 4), (1, 8), (3, 3), (2, 12), (1, 32)])
-@pytest.mark.parametrize("lens", [[1], [16], [17, 0, 5], [130, 64, 1, 200]])
+@pytest.mark.parametrize("lens", [[1], [16], [333], [17, 0, 5], [130, 64, 1, 200], [0, 0], [0, 129, 0, 0, 140, 0]])
 def test_single_tokens(lens, kv, group, d):
-    page, pages = 16, 40
+    page, pages = 16, 44
     c = filled(len(lens) + d, pages, kv, page, d)
     table = tables(lens, page, pages)
     spoil_tails(c, table, lens)
@@ -227,6 +227,32 @@ def test_long_sequences_are_split_and_joined(news, d, group):
     assert ops.mxq_kv_attention_workspace_bytes(c._raw(), 3, 3 * news, news, 2 * group, table.shape[1] * page) > 0
     for _ in range(3):  # the same bits every time
         assert torch.equal(got, check(q, c, table, lens, [0, news, 2 * news, 3 * news]))
+
+
+@pytest.mark.parametrize("batch", [500, 512, 513, 700])
+def test_many_sequences(batch):
+    """Up to 512 sequences share the CTAs evenly, more are split one by one; some have no key, some one, some many."""
+    page, width = 16, 12
+    g = torch.Generator().manual_seed(batch)
+    lens = torch.randint(0, 60, (batch,), generator=g)
+    lens[::7], lens[5::50] = 0, page * width - 3
+    pages = 900
+    c = filled(3, pages, 2, page, 64)
+    table = torch.randint(0, pages, (batch, width), generator=g).int().cuda()
+    check(rand(4, batch, 4, 64).bfloat16(), c, table, lens.tolist())
+
+
+@pytest.mark.parametrize("max_q,group", [(1, 1), (2, 4), (3, 4), (1, 16)])
+def test_shares_end_anywhere(max_q, group):
+    """Lengths around multiples of a share, with rows of no sequence on both sides."""
+    page, lens = 16, [1300, 128, 0, 2049, 127, 16, 700]
+    pages = sum(-(-n // page) for n in lens) + 1
+    c = filled(6, pages, 2, page, 128)
+    table = tables(lens, page, pages)
+    spoil_tails(c, table, lens)
+    starts = [2 + max_q * i for i in range(len(lens) + 1)]
+    check(rand(5, starts[-1] + 3, 2 * group, 128).bfloat16(), c, table, lens, starts)
+    check(rand(5, starts[-1] + 3, 2 * group, 128).bfloat16(), c, table, lens, starts, window=333)
 
 
 @pytest.mark.parametrize("k_scale,v_scale", [(2.0 ** -40, 2.0 ** -60), (2.0 ** 10, 2.0 ** 70), (30.0, 1e-4)])
