@@ -28,131 +28,23 @@
 // joins them in order. Otherwise a long sequence is split over a fixed number of CTAs, joined the same way.
 #include <atomic>
 #include <cstdint>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include "mxq_device.cuh"
-#include "mxq_internal.h"
-#include "mxq_tma.cuh"
+#include "mxq_attention.cuh"
 
 namespace mxq {
 namespace {
 
 constexpr int kAtWarps = 4, kAtThreads = 32 * kAtWarps;
-constexpr int kAtMinGroups = 8;    // groups of 16 keys that a split has at least
 constexpr int kAtStages = 4;       // groups in a warp's ring
 constexpr int kAtMaxSplits = 256;
 constexpr int kAtMaxEven = 512;    // sequences whose shares are worked out by every CTA
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-// n / d for 0 <= n < 2^31: with l = ceil(log2 d) and mul = ceil(2^(31 + l) / d), n * mul >> (31 + l) is exact
-struct FastDiv {
-    uint32_t mul, sh;
-    FastDiv() : mul(1u << 31), sh(31) {}
-    explicit FastDiv(uint32_t d) {
-        uint32_t l = 0;
-        while ((1ull << l) < d) ++l;
-        sh = 31 + l;
-        mul = (uint32_t)(((1ull << sh) + d - 1) / d);
-    }
-    __device__ __forceinline__ int operator()(int n) const { return (int)(((unsigned long long)(uint32_t)n * mul) >> sh); }
-};
-
-struct AtArgs {
-    KvCache c;
-    FastDiv by_group, by_page, by_splits, by_tiles, by_heads;
-    const __nv_bfloat16* q;
-    long long q_rows, q_row_stride, q_head_stride;
-    const int* starts;
-    const int* lens;
-    const int* table;
-    long long table_stride;
-    long long max_keys;
-    int batch, heads, group, max_q, window, splits, row_tiles;
-    bool fill;
-    bool even;     // equal shares of all groups (one row tile per sequence and head)
-    int4* info;    // even: of each share's first piece if its sequence began in an earlier share: sequence, head, whether
-                   // that was the share just before, last share of the sequence; else sequence -1
-    float scale;   // already times log2(e)
-    __nv_bfloat16* out;
-    float* lse;
-    float* part;   // pieces' [rows][D] sums, then their [rows][2] maximum and total; piece of split s of tile t: t * splits
-                   // + s; even: 2 c for the first piece of share c if its sequence began earlier, 2 c + 1 for its last
-    long long part_ml;  // offset of the latter
-};
-
-// what a CTA (and the joining kernel) works out about its sequence and rows
-struct Span {
-    int q0, n, nq;   // first row of q, queries of the sequence, of which computed
-    int len;         // keys
-};
-__device__ __forceinline__ Span span_of(const AtArgs& p, int b) {
-    Span s;
-    if (p.starts) {
-        const int rows = (int)p.q_rows;
-        s.q0 = min(max(__ldg(p.starts + b), 0), rows);
-        s.n = min(max(__ldg(p.starts + b + 1), s.q0), rows) - s.q0;
-    } else {
-        s.q0 = b * p.max_q;
-        s.n = p.max_q;
-    }
-    s.nq = min(s.n, p.max_q);
-    s.len = (int)min((long long)max(__ldg(p.lens + b), 0), p.max_keys);
-    return s;
-}
-// groups of 16 keys that the queries i0 .. i1 see together, and groups per split
-struct Groups {
-    int lo, hi, per;
-};
-__device__ __forceinline__ Groups groups_of(const AtArgs& p, const Span& s, int i0, int i1) {
-    const int hi = min(s.len, max(s.len - s.n + i1 + 1, 0));
-    const int lo = p.window > 0 ? min(max(s.len - s.n + i0 - p.window + 1, 0), hi) : 0;
-    Groups g;
-    g.lo = lo >> 4;
-    g.hi = (hi + 15) >> 4;
-    const int n = g.hi - g.lo;
-    g.per = max((n + p.splits - 1) / p.splits, kAtMinGroups);
-    return g;
-}
-
-// zeros (and -inf) for rows lo .. hi of out, `nh` heads from h0 on
-template <int D> __device__ void zero_rows(const AtArgs& p, int lo, int hi, int h0, int nh) {
-    for (int r = lo; r < hi; ++r) {
-        const long long at = (long long)r * p.heads + h0;
-        for (int i = threadIdx.x; i < nh * (D / 8); i += kAtThreads)
-            reinterpret_cast<uint4*>(p.out + at * D)[i] = make_uint4(0, 0, 0, 0);
-        if (p.lse)
-            for (int i = threadIdx.x; i < nh; i += kAtThreads) p.lse[at + i] = -INFINITY;
-    }
-}
-// the rows that no CTA computes: beyond max_q in each sequence, before the first sequence, behind the last
-template <int D> __device__ void fill_rows(const AtArgs& p, const Span& s, int b, int h0, int nh) {
-    zero_rows<D>(p, s.q0 + s.nq, s.q0 + s.n, h0, nh);
-    if (b == 0) zero_rows<D>(p, 0, s.q0, h0, nh);
-    if (b == p.batch - 1) zero_rows<D>(p, s.q0 + s.n, (int)p.q_rows, h0, nh);
-}
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
 }
 // log2 of a weight: score * mk - m
 __device__ __forceinline__ float weight_exponent(float score, float mk, float m) { return fmaf(score, mk, -m); }
@@ -163,38 +55,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
     return r;
 }
-// the four bytes of x, each two E2M1 codes, as f16 pairs (low nibble in the low half)
-__device__ __forceinline__ void e2m1_to_h2(uint32_t x, uint32_t* r) {
-    asm("{ .reg .b8 c0, c1, c2, c3;\n mov.b32 {c0, c1, c2, c3}, %4;\n"
-        "cvt.rn.f16x2.e2m1x2 %0, c0;\n cvt.rn.f16x2.e2m1x2 %1, c1;\n"
-        "cvt.rn.f16x2.e2m1x2 %2, c2;\n cvt.rn.f16x2.e2m1x2 %3, c3; }"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(x));
-}
 // 2^(byte - ref) as fp32 (2^-126 far below 1, which the conversion to f16 makes 0; it rounds small ones)
 __device__ __forceinline__ float rel_scale(int byte, int ref) {
     return __uint_as_float((uint32_t)(max(byte, ref - 126) - (ref - 127)) << 23);
 }
-// 2^e for any integer e (clamped to the fp32 range, subnormals flushed)
-__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)min(max(e + 127, 0), 255) << 23); }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-
 // a stage: codes of 16 keys and values, then their scales
 template <int D> struct AtStage {
     static constexpr int ROW = D / 2, SROW = D / 32;  // bytes of a key's codes, of its scales
@@ -789,8 +653,7 @@ template <int D, int NQ> __global__ void __launch_bounds__(256) k_kv_attention_j
 }
 
 // join the splits of one row: CTA (sequence, query, head), one thread per dimension
-template <int D, int NQ> __global__ void __launch_bounds__(D) k_kv_attention_join(const AtArgs p) {
-    constexpr int ROWS = 8 * NQ;
+template <int D, int ROWS> __global__ void __launch_bounds__(D) k_kv_attention_join(const AtArgs p) {
     const int d = threadIdx.x;
     pdl_wait_then_release();
     int id = blockIdx.x;
@@ -800,7 +663,9 @@ template <int D, int NQ> __global__ void __launch_bounds__(D) k_kv_attention_joi
     const Span s = span_of(p, b);
     if (i >= s.nq) return;
     const int head = h / p.group, row = i * p.group + h - head * p.group, rt = row / ROWS, r0 = rt * ROWS;
-    const Groups gr = groups_of(p, s, r0 / p.group, (min(r0 + ROWS, s.nq * p.group) - 1) / p.group);
+    constexpr bool TC = ROWS == kTileRows128;
+    const Groups gr = groups_of<TC ? kTileKeysShift : 4, TC ? kTileMinBlocks : kAtMinGroups>(
+        p, s, p.by_group(r0), p.by_group(min(r0 + ROWS, s.nq * p.group) - 1));
     const int n = (gr.hi - gr.lo + gr.per - 1) / gr.per;
     if (n <= 1) return;  // written by its split
     const long long first = (((long long)b * p.c.heads + head) * p.row_tiles + rt) * p.splits * ROWS + (row - r0);
@@ -821,7 +686,9 @@ template <int D, int NQ> __global__ void __launch_bounds__(D) k_kv_attention_joi
     if (p.lse && d == 0) p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
 }
 
-int nq_of(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+// eights of rows per tile; 16: the kernel of 128 rows. That one decodes a block of keys once for 128 rows at about the
+// cost of this one's 32
+int nq_of(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 16; }
 
 struct Plan {
     int nq, row_tiles, splits, shares;  // shares > 0: equal shares instead of splits
@@ -839,11 +706,29 @@ Plan plan_of(const KvCache& c, long long batch, int max_q, int heads, long long 
     p.tiles = batch * c.heads * p.row_tiles;
     p.splits = 1;
     const long long groups = (max_keys + 15) / 16, tiles = p.tiles > 0 ? p.tiles : 1;
-    const long long places = (long long)sms * (p.nq == 4 ? 2 : p.nq == 2 ? 3 : 4);
+    const long long places = (long long)sms * (p.nq == 4 ? 2 : p.nq == 2 ? 3 : 4);  // resident CTAs
     if (p.nq < 4 && batch > 1 && batch <= kAtMaxEven && groups > kAtMinGroups) {
         const long long most = (tiles * groups + kAtMinGroups - 1) / kAtMinGroups;
         p.shares = (int)(most < places ? most : places);
         p.pieces = 2LL * p.shares;
+        return p;
+    }
+    if (p.nq == 16) {
+        // one CTA per SM: the number of splits that fills whole waves best, with few waves
+        const long long blocks = (max_keys + 127) / 128;
+        long long most = blocks / kTileMinBlocks;
+        if (most > kAtMaxSplits) most = kAtMaxSplits;
+        double best = 0;
+        for (long long n = 1; n <= most || n == 1; ++n) {
+            const long long waves = (tiles * n + sms - 1) / sms;
+            if (n > 1 && waves > 4) break;
+            const double fill = (double)(tiles * n) / (double)(waves * sms) - 0.02 * (double)waves;
+            if (n == 1 || fill > best) {
+                best = fill;
+                p.splits = (int)n;
+            }
+        }
+        p.pieces = p.splits > 1 ? p.tiles * p.splits : 0;
         return p;
     }
     long long one = places / tiles, two = 2 * places / tiles;
@@ -854,6 +739,12 @@ Plan plan_of(const KvCache& c, long long batch, int max_q, int heads, long long 
     if (want > 1) p.splits = (int)want;
     p.pieces = p.splits > 1 ? p.tiles * p.splits : 0;
     return p;
+}
+
+template <int D, int ROWS> cudaError_t join(const AtArgs& a, cudaStream_t st) {
+    const long long rows = (long long)a.batch * a.max_q * a.heads;
+    if (rows > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    return launch_pdl(k_kv_attention_join<D, ROWS>, (unsigned)rows, D, st, a);
 }
 
 template <int D, int NQ> cudaError_t go(const AtArgs& a, const Plan& pl, int dev, cudaStream_t st) {
@@ -868,8 +759,7 @@ template <int D, int NQ> cudaError_t go(const AtArgs& a, const Plan& pl, int dev
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    const long long rows = (long long)a.batch * a.max_q * a.heads;
-    if (pl.tiles * a.splits > 0x7FFFFFFFLL || rows > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    if (pl.tiles * a.splits > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pl.shares > 0 ? pl.shares : pl.tiles * a.splits));
     cfg.blockDim = dim3(kAtThreads);
@@ -883,14 +773,15 @@ template <int D, int NQ> cudaError_t go(const AtArgs& a, const Plan& pl, int dev
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
     if (e != cudaSuccess || pl.pieces == 0 || pl.shares == 1) return e;
     cfg.dynamicSmemBytes = 0;
-    if (pl.shares > 0) {
-        cfg.gridDim = dim3((unsigned)(pl.shares - 1), (unsigned)((a.max_q * a.group + 256 / D - 1) / (256 / D)));
-        cfg.blockDim = dim3(256);
-        return cudaLaunchKernelEx(&cfg, k_kv_attention_join_shares<D, NQ>, a);
-    }
-    cfg.gridDim = dim3((unsigned)rows);
-    cfg.blockDim = dim3(D);
-    return cudaLaunchKernelEx(&cfg, k_kv_attention_join<D, NQ>, a);
+    if (pl.shares == 0) return join<D, 8 * NQ>(a, st);
+    cfg.gridDim = dim3((unsigned)(pl.shares - 1), (unsigned)((a.max_q * a.group + 256 / D - 1) / (256 / D)));
+    cfg.blockDim = dim3(256);
+    return cudaLaunchKernelEx(&cfg, k_kv_attention_join_shares<D, NQ>, a);
+}
+template <int D> cudaError_t go_tiles(const AtArgs& a, const Plan& pl, int dev, cudaStream_t st) {
+    if (pl.tiles * a.splits > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    const cudaError_t e = launch_kv_attention_tiles(a, pl.tiles, dev, st);
+    return e != cudaSuccess || pl.pieces == 0 ? e : join<D, kTileRows128>(a, st);
 }
 
 int sm_count(int dev) {
@@ -950,11 +841,13 @@ cudaError_t launch_kv_attention(const KvAttention& x, cudaStream_t st) {
     if (x.c.db == 4) {
         if (pl.nq == 1) return go<128, 1>(a, pl, dev, st);
         if (pl.nq == 2) return go<128, 2>(a, pl, dev, st);
-        return go<128, 4>(a, pl, dev, st);
+        if (pl.nq == 4) return go<128, 4>(a, pl, dev, st);
+        return go_tiles<128>(a, pl, dev, st);
     }
     if (pl.nq == 1) return go<64, 1>(a, pl, dev, st);
     if (pl.nq == 2) return go<64, 2>(a, pl, dev, st);
-    return go<64, 4>(a, pl, dev, st);
+    if (pl.nq == 4) return go<64, 4>(a, pl, dev, st);
+    return go_tiles<64>(a, pl, dev, st);
 }
 
 }  // namespace mxq

@@ -1,0 +1,590 @@
+// mxq_attention_tc.cu -- attention over the paged MXFP4 cache for many queries, on the 5th-generation tensor cores
+// (sm_100a).
+//
+// A CTA takes 128 rows (query x head of one key head's group) and walks blocks of 128 keys:
+//   S = Q K^T (fp32 in tensor memory),  P = 2^(S - m) (f16, tensor memory),  O += P V (fp32, tensor memory),
+// with the formulas, the relative block scales and the masks of mxq_attention.cu. Decoding 128 keys then serves 128
+// rows, not 32 as in a warp's registers there. Roles:
+// - four decoding warps bring a block's codes to shared memory (16-byte asynchronous copies, two blocks ahead), turn
+//   them into f16 operands in the 128-byte swizzle and hand them to the tensor core: K as [key][dimension], V
+//   transposed, [dimension][key], by interleaving the nibbles of two keys before the conversion, so that both
+//   products have the summed index contiguous. The places of the raw codes are permuted so that these reads, like the
+//   16-byte writes, touch every bank once.
+// - four softmax warps own a row per thread: its 128 scores at a time come from tensor memory, the weights go back as
+//   the A operand of the second product. The maximum is raised (and O rescaled, in tensor memory) only when a score
+//   exceeds it by 2^8, or when a value block exceeds 2^13 of the reference scale.
+// - one warp issues the MMAs, S of the next block before O of this one, so that the tensor core works while the
+//   softmax does. S, P and the operands have two buffers each.
+// Per block and SM: 1024 cycles of 2^x (16 a cycle), 1024 of tensor work, about 900 issue slots of each scheduler.
+//
+// Every wait on an mbarrier is bounded; after a timeout every role runs to its end without waiting.
+#include <atomic>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "mxq_attention.cuh"
+#include "mxq_tc.cuh"
+
+namespace mxq {
+namespace {
+
+constexpr int kTcThreads = 288;  // softmax warps 0 .. 3, decoding warps 4 .. 7, MMA warp 8
+constexpr int kTcRaw = 3;        // blocks in the ring of raw codes
+
+template <int D> struct TcCfg {
+    static constexpr int ROW = D / 2, SROW = D / 32;
+    static constexpr int Q = 128 * D * 2, K = 128 * D * 2, V = K;  // bytes of an operand
+    static constexpr int RV = 128 * ROW, RKS = 2 * RV, RVS = RKS + 128 * SROW, RAW = RVS + 128 * SROW;
+    static constexpr int AT_K = Q, AT_V = AT_K + 2 * K, AT_RAW = AT_V + 2 * V, BYTES = AT_RAW + kTcRaw * RAW;
+    static constexpr int SMEM = BYTES + 1024;  // + alignment slack
+    static_assert(SMEM <= 224 * 1024, "shared memory");
+    // place of 16-byte piece c of row r of the raw codes of K and of V
+    static __device__ __forceinline__ uint32_t k_at(int r, int c) {
+        return D == 128 ? (uint32_t)(r * ROW + 16 * (c ^ ((r >> 1) & 3))) : (uint32_t)(r * ROW + 16 * (c ^ ((r >> 2) & 1)));
+    }
+    static __device__ __forceinline__ uint32_t v_at(int r, int c) {
+        const int kg = r >> 3;
+        return D == 128 ? (uint32_t)((r ^ ((kg >> 2) & 1)) * ROW + 16 * (c ^ (kg & 3)))
+                        : (uint32_t)((r ^ (kg & 3)) * ROW + 16 * (c ^ ((kg >> 2) & 1)));
+    }
+};
+// tensor memory columns
+constexpr int kColS = 0, kColP = 256, kColO = 384;
+
+// what the decoding warps tell the softmax warps about a block
+struct BlockInfo {
+    int kref, vref;      // reference scale bytes
+    uint32_t pages;      // bit j: keys 16 j .. are in a page of the cache
+    uint32_t nan;        // a value block of the block of keys is NaN: nan_keys holds which
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ void group_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// f16 factors 2^(byte - ref) of two scale bytes (in the halves of x), 0 below 2^-14: the exponent fields byte - ref + 15,
+// with floor2 = ref - 15 in both halves and minus2 the number that takes it off both
+__device__ __forceinline__ uint32_t scale_pair(uint32_t x, uint32_t floor2, uint32_t minus2) {
+    uint32_t m;
+    asm("max.s16x2 %0, %1, %2;" : "=r"(m) : "r"(x), "r"(floor2));
+    return (m + minus2) << 10;
+}
+// largest scale byte of the 16 bytes w that are not NaN (0xFF), or -1; sets `nan` if one is
+__device__ __forceinline__ int max_byte(const uint32_t* w, bool& nan) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t bad = __vcmpeq4(w[i], 0xFFFFFFFFu);
+        nan |= bad != 0;
+        m = __vmaxu4(m, w[i] & ~bad);
+    }
+    m = __vmaxu4(m, m >> 16);
+    m = __vmaxu4(m, m >> 8);
+    return (int)(m & 0xFFu);
+}
+
+template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention_tiles(const AtArgs p, unsigned int* err) {
+    using C = TcCfg<D>;
+    extern __shared__ uint8_t dsm8[];
+    uint8_t* const base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm8) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(base);
+    __shared__ __align__(8) unsigned long long bars[18];
+    __shared__ uint32_t tmem_addr;
+    __shared__ int abort_flag;
+    __shared__ BlockInfo infos[4];
+    __shared__ uint8_t nan_keys[4][128];  // of a block with NaN values: bit b of key's byte: its block b is NaN
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    const uint32_t q_full = bar(0), drained = bar(17);
+    auto k_full = [&](int i) { return bar(1 + (i & 1)); };
+    auto k_empty = [&](int i) { return bar(3 + (i & 1)); };
+    auto v_full = [&](int i) { return bar(5 + (i & 1)); };
+    auto v_empty = [&](int i) { return bar(7 + (i & 1)); };
+    auto s_full = [&](int i) { return bar(9 + (i & 1)); };
+    auto s_empty = [&](int i) { return bar(11 + (i & 1)); };
+    auto p_full = [&](int i) { return bar(13 + (i & 1)); };
+    // the product of block i that adds to O is complete, and with it P's buffer free (two barriers: a wait may come
+    // after the next block's)
+    auto pv_done = [&](int i) { return bar(15 + (i & 1)); };
+    if (t == 0) {
+        mbar_init(q_full, 128);
+        mbar_init(drained, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(k_full(i), 128);
+            mbar_init(k_empty(i), 1);
+            mbar_init(v_full(i), 128);
+            mbar_init(v_empty(i), 1);
+            mbar_init(s_full(i), 1);
+            mbar_init(s_empty(i), 128);
+            mbar_init(p_full(i), 128);
+            mbar_init(pv_done(i), 1);
+        }
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) {
+        tmem_alloc<512>(smem_u32(&tmem_addr));
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tmem_addr;
+    volatile int* ab = &abort_flag;
+    pdl_wait_then_release();
+
+    const int tile = p.by_splits(blockIdx.x), sp = blockIdx.x - tile * p.splits;
+    const int bh = p.by_tiles(tile), rt = tile - bh * p.row_tiles;
+    const int b = p.by_heads(bh), head = bh - b * p.c.heads;
+    const Span s = span_of(p, b);
+    const int rows = s.nq * p.group, r0 = rt * 128;
+    if (p.fill && rt == 0 && sp == 0) fill_rows<D>(p, s, b, head * p.group, p.group);
+    Groups gr{0, 0, 1};
+    if (r0 < rows) gr = groups_of<kTileKeysShift, kTileMinBlocks>(p, s, p.by_group(r0), p.by_group(min(r0 + 128, rows) - 1));
+    const int first = gr.lo + sp * gr.per, n = max(min(first + gr.per, gr.hi) - first, 0);  // blocks of this CTA
+    const bool alone = gr.hi - gr.lo <= gr.per;  // one split holds all keys
+    const bool work = r0 < rows && (n > 0 || sp == 0);
+
+    if (work && warp < 4) {
+        // ---- softmax: thread t owns row r0 + t ----
+        const int r = r0 + t, i = p.by_group(min(r, rows - 1)), h = head * p.group + (min(r, rows - 1) - i * p.group);
+        const int pos = r < rows ? s.len - s.n + i : -1;
+        const int see_hi = min(pos + 1, s.len), see_lo = p.window > 0 ? pos - p.window + 1 : 0;  // keys see_lo .. see_hi - 1
+        const uint32_t lanes = tm + ((uint32_t)(warp * 32) << 16);
+        float mul;
+        {
+            // Q's row over a power of two, in f16
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + (s.q0 + i) * p.q_row_stride + h * p.q_head_stride);
+            uint32_t x[D / 2], top = 0;
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+                const uint4 v = __ldg(src + j);
+                x[4 * j] = v.x;
+                x[4 * j + 1] = v.y;
+                x[4 * j + 2] = v.z;
+                x[4 * j + 3] = v.w;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 2; ++j) top = max(top, max((x[j] & 0x7FFFu) << 16, x[j] & 0x7FFF0000u));
+            const int e = min(max((int)(top >> 23), 1), 253) - 127;
+            const float down = pow2i(-e);
+            mul = p.scale * pow2i(e);
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+                uint32_t f[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    f[k] = pack_h2(__uint_as_float(x[4 * j + k] << 16) * down, __uint_as_float(x[4 * j + k] & 0xFFFF0000u) * down);
+                sts128(sb + (j >> 3) * 16384 + t * 128 + (((j & 7) ^ (t & 7)) << 4), f[0], f[1], f[2], f[3]);
+            }
+            fence_proxy_async();
+            mbar_arrive(q_full);
+        }
+        float m = 0.f, thr = -INFINITY, l = 0.f;
+        int vref = 0;
+        uint32_t vnan = 0;  // bit j: dimensions 32 j .. of the row are NaN
+        bool ok = true;
+        for (int it = 0; it < n; ++it) {
+            const uint32_t ph = (uint32_t)(it >> 1) & 1u;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full(it), ph, ab, err));
+            if (!ok) break;
+            tc_fence_after();
+            const BlockInfo bi = infos[it & 3];
+            const int key0 = (first + it) * 128;
+            uint32_t sv[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(lanes + kColS + 128 * (it & 1) + 32 * c, sv + 32 * c);
+            tmem_wait_ld();
+            if (bi.nan) {
+                for (int j = 0; j < 128; ++j) {
+                    const int key = key0 + j;
+                    if (nan_keys[it & 3][j] && key < see_hi && key >= see_lo) vnan |= nan_keys[it & 3][j];
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(s_empty(it));
+            const float mk = mul * pow2i(bi.kref - 127);
+            unsigned long long* const e2 = reinterpret_cast<unsigned long long*>(sv);
+            const unsigned long long mk2 = dup2(mk);
+#pragma unroll
+            for (int j = 0; j < 64; ++j) e2[j] = f2fma(e2[j], mk2, dup2(-m));
+            float* const e = reinterpret_cast<float*>(sv);
+            // keys that the row does not see (no row of the warp sees all: the mask is worked out)
+            if (!__all_sync(0xFFFFFFFFu, bi.pages == 0xFFu && key0 >= see_lo && key0 + 128 <= see_hi)) {
+#pragma unroll
+                for (int j = 0; j < 128; ++j) {
+                    const int key = key0 + j;
+                    if (key >= see_hi || key < see_lo || !((bi.pages >> (j >> 4)) & 1u)) e[j] = -INFINITY;
+                }
+            }
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < 128; j += 8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top[k] = max3(top[k], e[j + 2 * k], e[j + 2 * k + 1]);
+            const float x = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            // raise the maximum, or follow the reference scale of V
+            const bool raise = x > thr, follow = it > 0 && bi.vref != vref;
+            if (__any_sync(0xFFFFFFFFu, raise || follow)) {
+                float f = 1.f, dx = 0.f;
+                if (raise) {
+                    const bool begun = thr > 0.f;
+                    f = begun ? ex2(-x) : 0.f;
+                    dx = x;
+                    m += x;
+                    thr = 8.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 128; ++j)
+                    if (raise && e[j] != -INFINITY) e[j] -= dx;
+                l *= f;
+                if (it > 0) {
+                    if (follow) f *= pow2i(vref - bi.vref);
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(pv_done(it - 1), (uint32_t)((it - 1) >> 1) & 1u, ab, err));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(lanes + kColO + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_st32(lanes + kColO + c, o);
+                    }
+                    tmem_wait_st();
+                }
+            }
+            vref = bi.vref;
+            // weights, and P's buffer when the product of block it - 2 has read it
+            unsigned long long sum2 = dup2(0.f);
+            uint32_t pk16[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) {
+                const float a = ex2(e[2 * j]), c = ex2(e[2 * j + 1]);
+                sum2 = f2add(sum2, pk(a, c));
+                pk16[j] = pack_h2(a, c);
+            }
+            float sa, sc;
+            upk(sum2, sa, sc);
+            l += sa + sc;
+            if (it > 1) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(pv_done(it), (uint32_t)((it >> 1) - 1) & 1u, ab, err));
+                if (!ok) break;
+                tc_fence_after();
+            }
+            tmem_st32(lanes + kColP + 64 * (it & 1), pk16);
+            tmem_st32(lanes + kColP + 64 * (it & 1) + 32, pk16 + 32);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(p_full(it));
+        }
+        if (n > 0 && ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(pv_done(n - 1), (uint32_t)((n - 1) >> 1) & 1u, ab, err));
+        tc_fence_after();
+        if (!(thr > 0.f)) m = -INFINITY;
+        if (ok) {
+            const long long at = (long long)(s.q0 + i) * p.heads + h, slot = (long long)blockIdx.x * 128 + t;
+            const float vtrue = pow2i(vref - 127), f = alone ? (l == 0.f ? 0.f : vtrue / l) : vtrue;
+            const float nan = __uint_as_float(0x7FC00000u);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld32(lanes + kColO + c, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = 0;
+                }
+                const float g = (vnan >> (c >> 5)) & 1u ? nan : f;
+                if (r < rows) {
+                    if (alone) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[j] = bf16x2(__uint_as_float(o[2 * j]) * g, __uint_as_float(o[2 * j + 1]) * g);
+                        uint4* const dst = reinterpret_cast<uint4*>(p.out + at * D + c);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                    } else {
+                        float4* const dst = reinterpret_cast<float4*>(p.part + slot * D + c);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            dst[j] = make_float4(__uint_as_float(o[4 * j]) * g, __uint_as_float(o[4 * j + 1]) * g,
+                                                 __uint_as_float(o[4 * j + 2]) * g, __uint_as_float(o[4 * j + 3]) * g);
+                    }
+                }
+            }
+            if (r < rows) {
+                if (!alone) *reinterpret_cast<float2*>(p.part + p.part_ml + slot * 2) = make_float2(m, l);
+                else if (p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            }
+        }
+    } else if (work && warp < 8) {
+        // ---- decoding ----
+        const int d = t - 128, w = warp - 4;
+        bool live = true;
+        int pg = -1, off = 0;   // lane j < 8: page and row of keys 16 j of the block to be copied next
+        uint32_t valid[3] = {0, 0, 0};  // groups in pages, of the blocks in the raw ring (the oldest first)
+        auto lookup = [&](int blk) {
+            pg = -1;
+            const int key = (first + blk) * 128 + 16 * lane;
+            if (lane < 8 && blk < n && key < s.len) {
+                const int at = p.by_page(key), x = __ldg(p.table + b * p.table_stride + at);
+                off = key - at * p.c.page;
+                pg = x >= 0 && x < p.c.pages ? x : -1;
+            }
+        };
+        auto copy = [&](int blk) -> uint32_t {  // copies of block blk; returns its groups in pages
+            const uint32_t raw = sb + C::AT_RAW + (uint32_t)(blk % kTcRaw) * C::RAW;
+            constexpr int PIECES = C::ROW / 16;
+#pragma unroll
+            for (int j = 0; j < PIECES; ++j) {
+                const int c = j * 128 + d, r = c / PIECES, src = r >> 4;
+                const int x = __shfl_sync(0xFFFFFFFFu, pg, src), o = __shfl_sync(0xFFFFFFFFu, off, src);
+                if (x >= 0) {
+                    const long long at = (((long long)x * p.c.heads + head) * p.c.page + o + (r & 15)) * C::ROW + 16 * (c % PIECES);
+                    copy16(raw + C::k_at(r, c % PIECES), p.c.kc + at);
+                    copy16(raw + C::RV + C::v_at(r, c % PIECES), p.c.vc + at);
+                }
+            }
+            // scales: 16 bytes are 16 / SROW keys; warp 0 K's, warp 1 V's
+            constexpr int PER = 16 / C::SROW;
+            const int src = min(lane, 128 / PER - 1) * PER >> 4;
+            const int x = __shfl_sync(0xFFFFFFFFu, pg, src), o = __shfl_sync(0xFFFFFFFFu, off, src);
+            if (w < 2 && lane < 128 / PER && x >= 0) {
+                const long long at = (((long long)x * p.c.heads + head) * p.c.page + o + (lane * PER & 15)) * C::SROW;
+                copy16(raw + (w ? C::RVS : C::RKS) + 16 * lane, (w ? p.c.vs : p.c.ks) + at);
+            }
+            return __ballot_sync(0xFFFFFFFFu, pg >= 0) & 0xFFu;
+        };
+        lookup(0);
+        valid[0] = copy(0);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        lookup(1);
+        valid[1] = copy(1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        lookup(2);
+        int vref = -1000;
+        for (int it = 0; it < n; ++it) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            group_barrier();  // block it has landed for all, and nobody reads block it - 1 any more
+            valid[2] = copy(it + 2);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            lookup(it + 3);
+            const uint32_t raw = sb + C::AT_RAW + (uint32_t)(it % kTcRaw) * C::RAW;
+            const int key0 = (first + it) * 128;
+            const uint32_t pages = valid[0];
+            const bool edge = pages != 0xFFu || key0 + 128 > s.len;
+            // the block's largest scales, by every warp for itself
+            bool nan = false;
+            int top[2];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                uint32_t x[4] = {0, 0, 0, 0};
+                constexpr int PER = 16 / C::SROW;
+                if (lane < 128 / PER) {
+                    const uint4 y = lds128u(raw + (v ? C::RVS : C::RKS) + 16 * lane);
+                    x[0] = y.x;
+                    x[1] = y.y;
+                    x[2] = y.z;
+                    x[3] = y.w;
+                    if (edge) {
+                        const int key = lane * PER;
+                        const bool there = (pages >> (key >> 4)) & 1u;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if constexpr (D == 128) {
+                                if (!there || key0 + key + i >= s.len) x[i] = 0;
+                            } else {
+                                if (!there || key0 + key + 2 * i >= s.len) x[i] = 0;
+                                else if (key0 + key + 2 * i + 1 >= s.len) x[i] &= 0xFFFFu;
+                            }
+                        }
+                    }
+                }
+                top[v] = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)max_byte(x, nan));
+            }
+            nan = __any_sync(0xFFFFFFFFu, nan);
+            const int kref = top[0] - 13;
+            if (top[1] > vref + 13) vref = top[1] - 6;
+            if (live && it > 1) live = mbar_wait(k_empty(it), (uint32_t)((it >> 1) - 1) & 1u, ab, err);
+            if (d == 0) infos[it & 3] = {kref, vref, pages, nan ? 1u : 0u};
+            if (nan) {
+                // value blocks that are NaN, of key d
+                uint32_t bits = 0;
+#pragma unroll
+                for (int j = 0; j < C::SROW; ++j)
+                    if (lds8(raw + C::RVS + d * C::SROW + j) == 0xFFu) bits |= 1u << j;
+                if (key0 + d >= s.len || !((pages >> (d >> 4)) & 1u)) bits = 0;
+                nan_keys[it & 3][d] = (uint8_t)bits;
+            }
+            {
+                // K: thread d decodes key d
+                const int c0 = kref - 15;
+                const uint32_t floor2 = (uint32_t)(c0 & 0xFFFF) * 0x10001u, minus2 = (uint32_t)(-c0 * 0x10001);
+                uint32_t sw;
+                if constexpr (D == 128) sw = lds32(raw + C::RKS + 4 * d);
+                else sw = (lds32(raw + C::RKS + 4 * (d >> 1)) >> (16 * (d & 1))) & 0xFFFFu;
+                const uint32_t kb = sb + C::AT_K + (uint32_t)(it & 1) * C::K + d * 128;
+#pragma unroll
+                for (int j = 0; j < C::SROW; ++j) {
+                    const uint32_t byte = (sw >> (8 * j)) & 0xFFu;
+                    uint32_t f = scale_pair(byte * 0x10001u, floor2, minus2);
+                    if (byte == 0xFFu) f = 0x7E007E00u;
+                    const uint4 x = lds128u(raw + C::k_at(d, j));
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t o[4];
+                        e2m1_to_h2(xs[k], o);
+                        const int ch = (j & 1) * 4 + k;
+                        sts128(kb + (j >> 1) * 16384 + ((ch ^ (d & 7)) << 4), mul_h2(o[0], f), mul_h2(o[1], f), mul_h2(o[2], f),
+                               mul_h2(o[3], f));
+                    }
+                }
+                fence_proxy_async();
+                if (live) mbar_arrive(k_full(it));
+            }
+            if (live && it > 1) live = mbar_wait(v_empty(it), (uint32_t)((it >> 1) - 1) & 1u, ab, err);
+            {
+                // V: keys 64 u + 8 kg .. + 7, eight dimensions of one 32-value block
+                const int c0 = vref - 15;
+                const uint32_t floor2 = (uint32_t)(c0 & 0xFFFF) * 0x10001u, minus2 = (uint32_t)(-c0 * 0x10001);
+                const int kg = lane & 7, dg = lane >> 3, blk = D == 128 ? w : w & 1;
+                const uint32_t vb = sb + C::AT_V + (uint32_t)(it & 1) * C::V;
+#pragma unroll
+                for (int uu = 0; uu < (D == 128 ? 2 : 1); ++uu) {
+                    const int u = D == 128 ? uu : w >> 1, k0 = u * 64 + kg * 8;
+                    uint32_t x[8], sc[4];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = lds32(raw + C::RV + C::v_at(k0 + j, blk) + 4 * dg);
+                    {
+                        uint32_t sw[8];  // low halves: the keys' scale of the block
+                        if constexpr (D == 128) {
+                            const uint4 a = lds128u(raw + C::RVS + 4 * k0), c = lds128u(raw + C::RVS + 4 * k0 + 16);
+                            const uint32_t y[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) sw[j] = (y[j] >> (8 * blk)) & 0xFFu;
+                        } else {
+                            const uint4 a = lds128u(raw + C::RVS + 2 * k0);
+                            const uint32_t y[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) sw[j] = (y[j >> 1] >> (16 * (j & 1) + 8 * blk)) & 0xFFu;
+                        }
+                        if (edge || nan) {
+                            const bool there = (pages >> (k0 >> 4)) & 1u;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (!there || key0 + k0 + j >= s.len || sw[j] == 0xFFu) sw[j] = 0;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) sc[j] = scale_pair(sw[2 * j] | (sw[2 * j + 1] << 16), floor2, minus2);
+                    }
+                    uint32_t ev[4][4], od[4][4];  // [pair of keys][dimension / 2]
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        e2m1_to_h2((x[2 * j] & 0x0F0F0F0Fu) | ((x[2 * j + 1] << 4) & 0xF0F0F0F0u), ev[j]);
+                        e2m1_to_h2(((x[2 * j] >> 4) & 0x0F0F0F0Fu) | (x[2 * j + 1] & 0xF0F0F0F0u), od[j]);
+                    }
+                    const uint32_t row = vb + (uint32_t)u * (D * 128) + (uint32_t)(blk * 32 + dg * 8) * 128;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        sts128(row + (2 * k) * 128 + ((kg ^ (2 * k)) << 4), mul_h2(ev[0][k], sc[0]), mul_h2(ev[1][k], sc[1]),
+                               mul_h2(ev[2][k], sc[2]), mul_h2(ev[3][k], sc[3]));
+                        sts128(row + (2 * k + 1) * 128 + ((kg ^ (2 * k + 1)) << 4), mul_h2(od[0][k], sc[0]), mul_h2(od[1][k], sc[1]),
+                               mul_h2(od[2][k], sc[2]), mul_h2(od[3][k], sc[3]));
+                    }
+                }
+                fence_proxy_async();
+                if (live) mbar_arrive(v_full(it));
+            }
+            valid[0] = valid[1];
+            valid[1] = valid[2];
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    } else if (work && n > 0) {
+        // ---- MMAs ----
+        const bool one = elect_one();
+        constexpr uint32_t id_s = idesc_f16(128, 128), id_o = idesc_f16(128, D);
+        const SmemDesc dq = desc_sw128(sb);
+        bool ok = mbar_wait(q_full, 0, ab, err);
+        tc_fence_after();
+        for (int it = 0; ok && it <= n; ++it) {
+            if (it < n) {
+                ok = mbar_wait(k_full(it), (uint32_t)(it >> 1) & 1u, ab, err);
+                if (ok && it > 1) ok = mbar_wait(s_empty(it), (uint32_t)((it >> 1) - 1) & 1u, ab, err);
+                if (!ok) break;
+                tc_fence_after();
+                if (one) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
+                        tc_mma_f16(tm + kColS + 128 * (it & 1), dq + at, dq + (C::AT_K + (it & 1) * C::K + at), id_s, k > 0);
+                    }
+                    tc_commit(k_empty(it));
+                    tc_commit(s_full(it));
+                }
+            }
+            if (it > 0) {
+                const int j = it - 1;
+                ok = mbar_wait(v_full(j), (uint32_t)(j >> 1) & 1u, ab, err) && mbar_wait(p_full(j), (uint32_t)(j >> 1) & 1u, ab, err);
+                if (!ok) break;
+                tc_fence_after();
+                if (one) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        tc_mma_f16_ts(tm + kColO, tm + kColP + 64 * (j & 1) + 8 * k,
+                                      dq + (C::AT_V + (j & 1) * C::V + (k >> 2) * (D * 128) + (k & 3) * 32), id_o, j > 0 || k > 0);
+                    tc_commit(v_empty(j));
+                    tc_commit(pv_done(j));
+                }
+            }
+        }
+        if (one && *ab) {  // MMAs in flight end before their shared and tensor memory goes away
+            tc_commit(drained);
+            const unsigned long long t0 = global_ns();
+            while (!mbar_test(drained, 0) && global_ns() - t0 < kWaitLimitNs) {
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_free<512>(tm);
+    }
+}
+
+template <int D> cudaError_t go(const AtArgs& a, long long tiles, int dev, cudaStream_t st) {
+    auto* kern = k_kv_attention_tiles<D>;
+    static std::atomic<unsigned long long> ready{0};
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<D>::SMEM);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
+    unsigned int* err = nullptr;
+    cudaError_t e = device_error_word(&err);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * a.splits));
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = TcCfg<D>::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, err);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_attention_tiles(const AtArgs& a, long long tiles, int dev, cudaStream_t st) {
+    return a.c.db == 4 ? go<128>(a, tiles, dev, st) : go<64>(a, tiles, dev, st);
+}
+
+}  // namespace mxq

@@ -48,6 +48,17 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // ---- descriptors --------------------------------------------------------------------------
@@ -75,6 +86,11 @@ __device__ __forceinline__ bool elect_one() {
 template <int F> __host__ __device__ constexpr uint32_t idesc_block_scaled(int m, int n) {
     const uint32_t fmt = F == F_E2M1 ? 1u : 0u;  // mxf4: E2M1 = 1; mxf8f6f4: E4M3 = 0
     return (fmt << 7) | (fmt << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 4) << 24);
+}
+
+// kind::f16, f16 operands, fp32 accumulators, both K-major
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // ---- instructions (one thread issues) -------------------------------------------------------
@@ -109,6 +125,23 @@ __device__ __forceinline__ void tc_mma_block_scaled(uint32_t d, SmemDesc a, Smem
     else MXQ_MMA("1", "mxf8f6f4", "1X");
 }
 #undef MXQ_MMA
+// D (+)= A B^T, f16: A from shared memory, or from tensor memory (row per lane, two values of k per column)
+__device__ __forceinline__ void tc_mma_f16(uint32_t d, SmemDesc a, SmemDesc b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{ .reg .pred p; .reg .b64 a, b; setp.ne.u32 p, %6, 0;\n"
+        "mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p; }" ::"r"(d),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, SmemDesc b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{ .reg .pred p; .reg .b64 b; setp.ne.u32 p, %5, 0;\n"
+        "mov.b64 b, {%2, %3};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p; }" ::"r"(d),
+        "r"(a), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
 // arrive on an mbarrier once everything this thread issued to the tensor core has completed (PAIR: on the barrier
 // at this address in both CTAs)
 template <bool PAIR = false> __device__ __forceinline__ void tc_commit(uint32_t bar) {

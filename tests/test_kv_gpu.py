@@ -242,6 +242,23 @@ def test_many_sequences(batch):
     check(rand(4, batch, 4, 64).bfloat16(), c, table, lens.tolist())
 
 
+@pytest.mark.parametrize("d,kv,group", [(128, 2, 4), (64, 1, 8), (128, 1, 1)])
+@pytest.mark.parametrize("lens,news", [([5000, 900, 0, 130], [100, 37, 5, 70]), ([3333], [129]), ([128 * 9], [40])])
+def test_many_queries_over_long_prefixes(lens, news, d, kv, group):
+    page = 32
+    pages = sum(-(-n // page) for n in lens) + 1
+    c = filled(7, pages, kv, page, d)
+    table = tables(lens, page, pages)
+    spoil_tails(c, table, lens)
+    starts = [0]
+    for n in news:
+        starts.append(starts[-1] + n)
+    q = rand(5, starts[-1] + 2, kv * group, d).bfloat16()
+    got = check(q, c, table, lens, starts)
+    assert torch.equal(got, check(q, c, table, lens, starts))
+    check(q, c, table, lens, starts, window=500)
+
+
 @pytest.mark.parametrize("max_q,group", [(1, 1), (2, 4), (3, 4), (1, 16)])
 def test_shares_end_anywhere(max_q, group):
     """Lengths around multiples of a share, with rows of no sequence on both sides."""
@@ -260,6 +277,7 @@ def test_block_scales_far_from_one(k_scale, v_scale):
     lens, page = [200, 70], 16
     c = filled(5, 20, 2, page, 128, k_scale, v_scale)
     check((rand(11, 2, 8, 128) / k_scale).bfloat16(), c, tables(lens, page, 20), lens)
+    check((rand(11, 60, 8, 128) / k_scale).bfloat16(), c, tables(lens, page, 20), lens)
 
 
 def test_block_scales_that_grow_and_shrink_along_a_sequence():
@@ -268,7 +286,8 @@ def test_block_scales_that_grow_and_shrink_along_a_sequence():
     size = torch.exp2(torch.tensor([-30.0, 0, 14, -9, 21, 22, 3, -20], device="cuda")).repeat_interleave(32)[:, None, None]
     ops.kv_append((rand(1, n, 1, 64) * size.clamp(max=8)).bfloat16(), (rand(2, n, 1, 64) * size).bfloat16(), c, torch.arange(n, device="cuda"))
     table = torch.arange(16, dtype=torch.int32, device="cuda")[None]
-    check(rand(12, 8, 4, 64).bfloat16(), c, table, [n], [0, 8])
+    for rows in (1, 8, 60):
+        check(rand(12, rows, 4, 64).bfloat16(), c, table, [n], [0, rows])
 
 
 def test_large_scores_and_a_given_scale():
@@ -278,6 +297,8 @@ def test_large_scores_and_a_given_scale():
     check(rand(13, 1, 8, 128).bfloat16(), c, tables(lens, page, 10), lens, scale=0.01)
     check(rand(13, 1, 8, 128).bfloat16(), c, tables(lens, page, 10), lens, scale=0.0)
     check((rand(13, 1, 8, 128) * 2.0 ** 100).bfloat16(), c, tables(lens, page, 10), lens, scale=2.0 ** -104)
+    for scale in (None, 0.01, 0.0, -0.05):
+        check((rand(13, 50, 8, 128) * 20).bfloat16(), c, tables(lens, page, 10), lens, scale=scale)
 
 
 def test_nan_blocks_reach_only_the_queries_that_see_them():
@@ -302,6 +323,7 @@ def test_pages_outside_the_cache_are_not_seen():
     table = tables(lens, page, 12)
     table[0, 2], table[0, 6], table[1, 0] = -1, 12, 2 ** 31 - 1
     check(rand(15, 2, 4, 64).bfloat16(), c, table, lens)
+    check(rand(15, 60, 4, 64).bfloat16(), c, table, lens)
     table[:] = -1
     got, lse = ops.kv_attention(rand(15, 2, 4, 64).bfloat16(), c, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), lse=True)
     assert (got == 0).all() and (lse == -math.inf).all()
