@@ -663,7 +663,7 @@ template <int D, int ROWS> __global__ void __launch_bounds__(D) k_kv_attention_j
     const Span s = span_of(p, b);
     if (i >= s.nq) return;
     const int head = h / p.group, row = i * p.group + h - head * p.group, rt = row / ROWS, r0 = rt * ROWS;
-    constexpr bool TC = ROWS == kTileRows128;
+    constexpr bool TC = ROWS == kTileRows;
     const Groups gr = groups_of<TC ? kTileKeysShift : 4, TC ? kTileMinBlocks : kAtMinGroups>(
         p, s, p.by_group(r0), p.by_group(min(r0 + ROWS, s.nq * p.group) - 1));
     const int n = (gr.hi - gr.lo + gr.per - 1) / gr.per;
@@ -686,9 +686,9 @@ template <int D, int ROWS> __global__ void __launch_bounds__(D) k_kv_attention_j
     if (p.lse && d == 0) p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
 }
 
-// eights of rows per tile; 16: the kernel of 128 rows. That one decodes a block of keys once for 128 rows at about the
-// cost of this one's 32
-int nq_of(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 16; }
+// eights of rows per tile; more than 32 rows: the kernel that decodes a block of keys for 256 of them at once
+constexpr int kNqTiles = kTileRows / 8;
+int nq_of(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : kNqTiles; }
 
 struct Plan {
     int nq, row_tiles, splits, shares;  // shares > 0: equal shares instead of splits
@@ -713,7 +713,7 @@ Plan plan_of(const KvCache& c, long long batch, int max_q, int heads, long long 
         p.pieces = 2LL * p.shares;
         return p;
     }
-    if (p.nq == 16) {
+    if (p.nq == kNqTiles) {
         // one CTA per SM: the number of splits that fills whole waves best, with few waves
         const long long blocks = (max_keys + 127) / 128;
         long long most = blocks / kTileMinBlocks;
@@ -781,7 +781,7 @@ template <int D, int NQ> cudaError_t go(const AtArgs& a, const Plan& pl, int dev
 template <int D> cudaError_t go_tiles(const AtArgs& a, const Plan& pl, int dev, cudaStream_t st) {
     if (pl.tiles * a.splits > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     const cudaError_t e = launch_kv_attention_tiles(a, pl.tiles, dev, st);
-    return e != cudaSuccess || pl.pieces == 0 ? e : join<D, kTileRows128>(a, st);
+    return e != cudaSuccess || pl.pieces == 0 ? e : join<D, kTileRows>(a, st);
 }
 
 int sm_count(int dev) {

@@ -147,8 +147,8 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
     return v;
 }
 
-// many rows of a sequence and key head: 128 at a time, keys in blocks of 128 (mxq_attention_tc.cu)
-constexpr int kTileRows128 = 128, kTileKeysShift = 7, kTileMinBlocks = 4;
+// many rows of a sequence and key head: 256 at a time, keys in blocks of 128 (mxq_attention_tc.cu)
+constexpr int kTileRows = 256, kTileKeysShift = 7, kTileMinBlocks = 4;
 cudaError_t launch_kv_attention_tiles(const AtArgs& a, long long tiles, int dev, cudaStream_t st);
 
 }  // namespace mxq

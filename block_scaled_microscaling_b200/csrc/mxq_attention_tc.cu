@@ -1,21 +1,22 @@
 // mxq_attention_tc.cu -- attention over the paged MXFP4 cache for many queries, on the 5th-generation tensor cores
 // (sm_100a).
 //
-// A CTA takes 128 rows (query x head of one key head's group) and walks blocks of 128 keys:
-//   S = Q K^T (fp32 in tensor memory),  P = 2^(S - m) (f16, tensor memory),  O += P V (fp32, tensor memory),
-// with the formulas, the relative block scales and the masks of mxq_attention.cu. Decoding 128 keys then serves 128
+// A CTA takes two tiles of 128 rows (query x head of one key head's group) and walks blocks of 128 keys:
+//   S = Q K^T (fp32 in tensor memory),  P = 2^(S - m) (f16, over S),  O += P V (fp32, tensor memory),
+// with the formulas, the relative block scales and the masks of mxq_attention.cu. Decoding 128 keys then serves 256
 // rows, not 32 as in a warp's registers there. Roles:
 // - four decoding warps bring a block's codes to shared memory (16-byte asynchronous copies, two blocks ahead), turn
 //   them into f16 operands in the 128-byte swizzle and hand them to the tensor core: K as [key][dimension], V
 //   transposed, [dimension][key], by interleaving the nibbles of two keys before the conversion, so that both
 //   products have the summed index contiguous. The places of the raw codes are permuted so that these reads, like the
 //   16-byte writes, touch every bank once.
-// - four softmax warps own a row per thread: its 128 scores at a time come from tensor memory, the weights go back as
-//   the A operand of the second product. The maximum is raised (and O rescaled, in tensor memory) only when a score
-//   exceeds it by 2^8, or when a value block exceeds 2^13 of the reference scale.
-// - one warp issues the MMAs, S of the next block before O of this one, so that the tensor core works while the
-//   softmax does. S, P and the operands have two buffers each.
-// Per block and SM: 1024 cycles of 2^x (16 a cycle), 1024 of tensor work, about 900 issue slots of each scheduler.
+// - four softmax warps per tile, a row per thread: its 128 scores come from tensor memory, the weights go back as the A
+//   operand of the second product. The maximum is raised (and O rescaled, in tensor memory) only when a score exceeds
+//   it by 2^8, or when a value block exceeds 2^13 of the reference scale.
+// - one warp issues the MMAs: O of a tile's block, then S of its next block, while the other tile is in its softmax.
+// One tile per CTA, with S in two buffers, took 163 us for 128 queries over 32768 keys (5500 cycles a block: decoding
+// and one tile's softmax, each bound by the latency of a single warp per scheduler); two tiles share the decoding and
+// hide each other's latency.
 //
 // Every wait on an mbarrier is bounded; after a timeout every role runs to its end without waiting.
 #include <atomic>
@@ -28,14 +29,18 @@
 namespace mxq {
 namespace {
 
-constexpr int kTcThreads = 288;  // softmax warps 0 .. 3, decoding warps 4 .. 7, MMA warp 8
+// warpgroups: softmax of the two tiles, decoding, MMA (one warp of it). Registers are moved between them: 128 a thread
+// at launch = (184 + 184 + 104 + 40) / 4
+constexpr int kTcThreads = 512, kTcDecode = 8, kTcMma = 12;
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 constexpr int kTcRaw = 3;        // blocks in the ring of raw codes
 
 template <int D> struct TcCfg {
     static constexpr int ROW = D / 2, SROW = D / 32;
     static constexpr int Q = 128 * D * 2, K = 128 * D * 2, V = K;  // bytes of an operand
     static constexpr int RV = 128 * ROW, RKS = 2 * RV, RVS = RKS + 128 * SROW, RAW = RVS + 128 * SROW;
-    static constexpr int AT_K = Q, AT_V = AT_K + 2 * K, AT_RAW = AT_V + 2 * V, BYTES = AT_RAW + kTcRaw * RAW;
+    static constexpr int AT_K = 2 * Q, AT_V = AT_K + 2 * K, AT_RAW = AT_V + V, BYTES = AT_RAW + kTcRaw * RAW;
     static constexpr int SMEM = BYTES + 1024;  // + alignment slack
     static_assert(SMEM <= 224 * 1024, "shared memory");
     // place of 16-byte piece c of row r of the raw codes of K and of V
@@ -49,7 +54,7 @@ template <int D> struct TcCfg {
     }
 };
 // tensor memory columns
-constexpr int kColS = 0, kColP = 256, kColO = 384;
+constexpr int kColS = 0, kColO = 256;  // + 128 for the second tile
 
 // what the decoding warps tell the softmax warps about a block
 struct BlockInfo {
@@ -90,41 +95,35 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
     extern __shared__ uint8_t dsm8[];
     uint8_t* const base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm8) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(base);
-    __shared__ __align__(8) unsigned long long bars[18];
+    __shared__ __align__(8) unsigned long long bars[13];
     __shared__ uint32_t tmem_addr;
     __shared__ int abort_flag;
     __shared__ BlockInfo infos[4];
+    __shared__ uint32_t there[4][2];      // groups of 16 keys of a block that are in pages: even and odd ones
     __shared__ uint8_t nan_keys[4][128];  // of a block with NaN values: bit b of key's byte: its block b is NaN
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
-    const uint32_t q_full = bar(0), drained = bar(17);
-    auto k_full = [&](int i) { return bar(1 + (i & 1)); };
-    auto k_empty = [&](int i) { return bar(3 + (i & 1)); };
-    auto v_full = [&](int i) { return bar(5 + (i & 1)); };
-    auto v_empty = [&](int i) { return bar(7 + (i & 1)); };
-    auto s_full = [&](int i) { return bar(9 + (i & 1)); };
-    auto s_empty = [&](int i) { return bar(11 + (i & 1)); };
-    auto p_full = [&](int i) { return bar(13 + (i & 1)); };
-    // the product of block i that adds to O is complete, and with it P's buffer free (two barriers: a wait may come
-    // after the next block's)
-    auto pv_done = [&](int i) { return bar(15 + (i & 1)); };
+    auto k_full = [&](int i) { return bar(i & 1); };
+    auto k_empty = [&](int i) { return bar(2 + (i & 1)); };
+    const uint32_t v_full = bar(4), v_empty = bar(5), drained = bar(6);
+    auto q_full = [&](int x) { return bar(7 + x); };   // of tile x
+    auto s_full = [&](int x) { return bar(9 + x); };   // S of a block, and everything issued before it; at the end, O
+    auto p_full = [&](int x) { return bar(11 + x); };  // P of a block
     if (t == 0) {
-        mbar_init(q_full, 128);
-        mbar_init(drained, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(k_full(i), 128);
             mbar_init(k_empty(i), 1);
-            mbar_init(v_full(i), 128);
-            mbar_init(v_empty(i), 1);
+            mbar_init(q_full(i), 128);
             mbar_init(s_full(i), 1);
-            mbar_init(s_empty(i), 128);
             mbar_init(p_full(i), 128);
-            mbar_init(pv_done(i), 1);
         }
+        mbar_init(v_full, 128);
+        mbar_init(v_empty, 1);
+        mbar_init(drained, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 8) {
+    if (warp == kTcMma) {
         tmem_alloc<512>(smem_u32(&tmem_addr));
         tc_fence_before();
     }
@@ -138,243 +137,249 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
     const int bh = p.by_tiles(tile), rt = tile - bh * p.row_tiles;
     const int b = p.by_heads(bh), head = bh - b * p.c.heads;
     const Span s = span_of(p, b);
-    const int rows = s.nq * p.group, r0 = rt * 128;
+    const int rows = s.nq * p.group, r0 = rt * kTileRows;
     if (p.fill && rt == 0 && sp == 0) fill_rows<D>(p, s, b, head * p.group, p.group);
     Groups gr{0, 0, 1};
-    if (r0 < rows) gr = groups_of<kTileKeysShift, kTileMinBlocks>(p, s, p.by_group(r0), p.by_group(min(r0 + 128, rows) - 1));
+    if (r0 < rows) gr = groups_of<kTileKeysShift, kTileMinBlocks>(p, s, p.by_group(r0), p.by_group(min(r0 + kTileRows, rows) - 1));
     const int first = gr.lo + sp * gr.per, n = max(min(first + gr.per, gr.hi) - first, 0);  // blocks of this CTA
     const bool alone = gr.hi - gr.lo <= gr.per;  // one split holds all keys
-    const bool work = r0 < rows && (n > 0 || sp == 0);
+    const bool work = r0 < rows && (n > 0 || sp == 0), two = r0 + 128 < rows;  // two: the second tile has rows
 
-    if (work && warp < 4) {
-        // ---- softmax: thread t owns row r0 + t ----
-        const int r = r0 + t, i = p.by_group(min(r, rows - 1)), h = head * p.group + (min(r, rows - 1) - i * p.group);
-        const int pos = r < rows ? s.len - s.n + i : -1;
-        const int see_hi = min(pos + 1, s.len), see_lo = p.window > 0 ? pos - p.window + 1 : 0;  // keys see_lo .. see_hi - 1
-        const uint32_t lanes = tm + ((uint32_t)(warp * 32) << 16);
-        float mul;
-        {
-            // Q's row over a power of two, in f16
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + (s.q0 + i) * p.q_row_stride + h * p.q_head_stride);
-            uint32_t x[D / 2], top = 0;
+    if (warp < kTcDecode) {
+        regs_up<184>();
+        const int x = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+        if (work && (x == 0 || two)) {
+            // ---- softmax: thread's row r0 + 128 x + row ----
+            const int r = r0 + 128 * x + row, i = p.by_group(min(r, rows - 1)), h = head * p.group + (min(r, rows - 1) - i * p.group);
+            const int pos = r < rows ? s.len - s.n + i : -1;
+            const int see_hi = min(pos + 1, s.len), see_lo = p.window > 0 ? pos - p.window + 1 : 0;  // keys see_lo .. see_hi - 1
+            const uint32_t ts = tm + ((uint32_t)(quad * 32) << 16) + kColS + 128 * x, to = ts + kColO - kColS;
+            float mul;
+            {
+                // Q's row over a power of two, in f16
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + (s.q0 + i) * p.q_row_stride + h * p.q_head_stride);
+                uint32_t q[D / 2], top = 0;
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-                const uint4 v = __ldg(src + j);
-                x[4 * j] = v.x;
-                x[4 * j + 1] = v.y;
-                x[4 * j + 2] = v.z;
-                x[4 * j + 3] = v.w;
-            }
-#pragma unroll
-            for (int j = 0; j < D / 2; ++j) top = max(top, max((x[j] & 0x7FFFu) << 16, x[j] & 0x7FFF0000u));
-            const int e = min(max((int)(top >> 23), 1), 253) - 127;
-            const float down = pow2i(-e);
-            mul = p.scale * pow2i(e);
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-                uint32_t f[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    f[k] = pack_h2(__uint_as_float(x[4 * j + k] << 16) * down, __uint_as_float(x[4 * j + k] & 0xFFFF0000u) * down);
-                sts128(sb + (j >> 3) * 16384 + t * 128 + (((j & 7) ^ (t & 7)) << 4), f[0], f[1], f[2], f[3]);
-            }
-            fence_proxy_async();
-            mbar_arrive(q_full);
-        }
-        float m = 0.f, thr = -INFINITY, l = 0.f;
-        int vref = 0;
-        uint32_t vnan = 0;  // bit j: dimensions 32 j .. of the row are NaN
-        bool ok = true;
-        for (int it = 0; it < n; ++it) {
-            const uint32_t ph = (uint32_t)(it >> 1) & 1u;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full(it), ph, ab, err));
-            if (!ok) break;
-            tc_fence_after();
-            const BlockInfo bi = infos[it & 3];
-            const int key0 = (first + it) * 128;
-            uint32_t sv[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(lanes + kColS + 128 * (it & 1) + 32 * c, sv + 32 * c);
-            tmem_wait_ld();
-            if (bi.nan) {
-                for (int j = 0; j < 128; ++j) {
-                    const int key = key0 + j;
-                    if (nan_keys[it & 3][j] && key < see_hi && key >= see_lo) vnan |= nan_keys[it & 3][j];
-                }
-            }
-            tc_fence_before();
-            mbar_arrive(s_empty(it));
-            const float mk = mul * pow2i(bi.kref - 127);
-            unsigned long long* const e2 = reinterpret_cast<unsigned long long*>(sv);
-            const unsigned long long mk2 = dup2(mk);
-#pragma unroll
-            for (int j = 0; j < 64; ++j) e2[j] = f2fma(e2[j], mk2, dup2(-m));
-            float* const e = reinterpret_cast<float*>(sv);
-            // keys that the row does not see (no row of the warp sees all: the mask is worked out)
-            if (!__all_sync(0xFFFFFFFFu, bi.pages == 0xFFu && key0 >= see_lo && key0 + 128 <= see_hi)) {
-#pragma unroll
-                for (int j = 0; j < 128; ++j) {
-                    const int key = key0 + j;
-                    if (key >= see_hi || key < see_lo || !((bi.pages >> (j >> 4)) & 1u)) e[j] = -INFINITY;
-                }
-            }
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int j = 0; j < 128; j += 8)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) top[k] = max3(top[k], e[j + 2 * k], e[j + 2 * k + 1]);
-            const float x = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-            // raise the maximum, or follow the reference scale of V
-            const bool raise = x > thr, follow = it > 0 && bi.vref != vref;
-            if (__any_sync(0xFFFFFFFFu, raise || follow)) {
-                float f = 1.f, dx = 0.f;
-                if (raise) {
-                    const bool begun = thr > 0.f;
-                    f = begun ? ex2(-x) : 0.f;
-                    dx = x;
-                    m += x;
-                    thr = 8.f;
+                for (int j = 0; j < D / 8; ++j) {
+                    const uint4 v = __ldg(src + j);
+                    q[4 * j] = v.x;
+                    q[4 * j + 1] = v.y;
+                    q[4 * j + 2] = v.z;
+                    q[4 * j + 3] = v.w;
                 }
 #pragma unroll
-                for (int j = 0; j < 128; ++j)
-                    if (raise && e[j] != -INFINITY) e[j] -= dx;
-                l *= f;
-                if (it > 0) {
-                    if (follow) f *= pow2i(vref - bi.vref);
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(pv_done(it - 1), (uint32_t)((it - 1) >> 1) & 1u, ab, err));
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(lanes + kColO + c, o);
-                        tmem_wait_ld();
+                for (int j = 0; j < D / 2; ++j) top = max(top, max((q[j] & 0x7FFFu) << 16, q[j] & 0x7FFF0000u));
+                const int e = min(max((int)(top >> 23), 1), 253) - 127;
+                const float down = pow2i(-e);
+                mul = p.scale * pow2i(e);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tmem_st32(lanes + kColO + c, o);
-                    }
-                    tmem_wait_st();
+                for (int j = 0; j < D / 8; ++j) {
+                    uint32_t f[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        f[k] = pack_h2(__uint_as_float(q[4 * j + k] << 16) * down, __uint_as_float(q[4 * j + k] & 0xFFFF0000u) * down);
+                    sts128(sb + x * C::Q + (j >> 3) * 16384 + row * 128 + (((j & 7) ^ (row & 7)) << 4), f[0], f[1], f[2], f[3]);
                 }
+                fence_proxy_async();
+                mbar_arrive(q_full(x));
             }
-            vref = bi.vref;
-            // weights, and P's buffer when the product of block it - 2 has read it
-            unsigned long long sum2 = dup2(0.f);
-            uint32_t pk16[64];
-#pragma unroll
-            for (int j = 0; j < 64; ++j) {
-                const float a = ex2(e[2 * j]), c = ex2(e[2 * j + 1]);
-                sum2 = f2add(sum2, pk(a, c));
-                pk16[j] = pack_h2(a, c);
-            }
-            float sa, sc;
-            upk(sum2, sa, sc);
-            l += sa + sc;
-            if (it > 1) {
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(pv_done(it), (uint32_t)((it >> 1) - 1) & 1u, ab, err));
+            float m = 0.f, thr = -INFINITY, l = 0.f;
+            int vref = 0;
+            uint32_t vnan = 0;  // bit j: dimensions 32 j .. of the row are NaN
+            bool ok = true;
+            for (int it = 0; it < n; ++it) {
+                // S of this block, and with it the products before: O of block it - 1 is complete
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full(x), (uint32_t)it & 1u, ab, err));
                 if (!ok) break;
                 tc_fence_after();
-            }
-            tmem_st32(lanes + kColP + 64 * (it & 1), pk16);
-            tmem_st32(lanes + kColP + 64 * (it & 1) + 32, pk16 + 32);
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(p_full(it));
-        }
-        if (n > 0 && ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(pv_done(n - 1), (uint32_t)((n - 1) >> 1) & 1u, ab, err));
-        tc_fence_after();
-        if (!(thr > 0.f)) m = -INFINITY;
-        if (ok) {
-            const long long at = (long long)(s.q0 + i) * p.heads + h, slot = (long long)blockIdx.x * 128 + t;
-            const float vtrue = pow2i(vref - 127), f = alone ? (l == 0.f ? 0.f : vtrue / l) : vtrue;
-            const float nan = __uint_as_float(0x7FC00000u);
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                if (n > 0) {
-                    tmem_ld32(lanes + kColO + c, o);
-                    tmem_wait_ld();
-                } else {
+                const BlockInfo bi = infos[it & 3];
+                const int key0 = (first + it) * 128;
+                union {
+                    uint32_t u[128];
+                    float f[128];
+                    unsigned long long d[64];
+                } e;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = 0;
-                }
-                const float g = (vnan >> (c >> 5)) & 1u ? nan : f;
-                if (r < rows) {
-                    if (alone) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) w[j] = bf16x2(__uint_as_float(o[2 * j]) * g, __uint_as_float(o[2 * j + 1]) * g);
-                        uint4* const dst = reinterpret_cast<uint4*>(p.out + at * D + c);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-                    } else {
-                        float4* const dst = reinterpret_cast<float4*>(p.part + slot * D + c);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            dst[j] = make_float4(__uint_as_float(o[4 * j]) * g, __uint_as_float(o[4 * j + 1]) * g,
-                                                 __uint_as_float(o[4 * j + 2]) * g, __uint_as_float(o[4 * j + 3]) * g);
+                for (int c = 0; c < 128; c += 32) tmem_ld32(ts + c, e.u + c);
+                tmem_wait_ld();
+                if (bi.nan) {
+                    for (int j = 0; j < 128; ++j) {
+                        const uint32_t bits = nan_keys[it & 3][j];
+                        if (key0 + j < see_hi && key0 + j >= see_lo) vnan |= bits;
                     }
                 }
-            }
-            if (r < rows) {
-                if (!alone) *reinterpret_cast<float2*>(p.part + p.part_ml + slot * 2) = make_float2(m, l);
-                else if (p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-            }
-        }
-    } else if (work && warp < 8) {
-        // ---- decoding ----
-        const int d = t - 128, w = warp - 4;
-        bool live = true;
-        int pg = -1, off = 0;   // lane j < 8: page and row of keys 16 j of the block to be copied next
-        uint32_t valid[3] = {0, 0, 0};  // groups in pages, of the blocks in the raw ring (the oldest first)
-        auto lookup = [&](int blk) {
-            pg = -1;
-            const int key = (first + blk) * 128 + 16 * lane;
-            if (lane < 8 && blk < n && key < s.len) {
-                const int at = p.by_page(key), x = __ldg(p.table + b * p.table_stride + at);
-                off = key - at * p.c.page;
-                pg = x >= 0 && x < p.c.pages ? x : -1;
-            }
-        };
-        auto copy = [&](int blk) -> uint32_t {  // copies of block blk; returns its groups in pages
-            const uint32_t raw = sb + C::AT_RAW + (uint32_t)(blk % kTcRaw) * C::RAW;
-            constexpr int PIECES = C::ROW / 16;
+                const unsigned long long mk2 = dup2(mul * pow2i(bi.kref - 127)), m2 = dup2(-m);
 #pragma unroll
-            for (int j = 0; j < PIECES; ++j) {
-                const int c = j * 128 + d, r = c / PIECES, src = r >> 4;
-                const int x = __shfl_sync(0xFFFFFFFFu, pg, src), o = __shfl_sync(0xFFFFFFFFu, off, src);
-                if (x >= 0) {
-                    const long long at = (((long long)x * p.c.heads + head) * p.c.page + o + (r & 15)) * C::ROW + 16 * (c % PIECES);
-                    copy16(raw + C::k_at(r, c % PIECES), p.c.kc + at);
-                    copy16(raw + C::RV + C::v_at(r, c % PIECES), p.c.vc + at);
+                for (int j = 0; j < 64; ++j) e.d[j] = f2fma(e.d[j], mk2, m2);
+                // keys that the row does not see
+                if (!__all_sync(0xFFFFFFFFu, bi.pages == 0xFFu && key0 >= see_lo && key0 + 128 <= see_hi)) {
+                    const int lo = see_lo - key0, hi = see_hi - key0;
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (j >= hi || j < lo || !((bi.pages >> (j >> 4)) & 1u)) e.f[j] = -INFINITY;
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < 128; j += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top[k] = max3(top[k], e.f[j + 2 * k], e.f[j + 2 * k + 1]);
+                const float y = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                // raise the maximum, or follow the reference scale of V
+                const bool raise = y > thr, follow = it > 0 && bi.vref != vref;
+                if (__any_sync(0xFFFFFFFFu, raise || follow)) {
+                    float f = 1.f, dx = 0.f;
+                    if (raise) {
+                        f = thr > 0.f ? ex2(-y) : 0.f;
+                        dx = y;
+                        m += y;
+                        thr = 8.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (raise && e.f[j] != -INFINITY) e.f[j] -= dx;
+                    l *= f;
+                    if (it > 0) {
+                        if (follow) f *= pow2i(vref - bi.vref);
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(to + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st16(to + c, o);
+                        }
+                    }
+                }
+                vref = bi.vref;
+                // weights over S: two keys per column
+                unsigned long long sum2 = dup2(0.f);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float a = ex2(e.f[32 * c + 2 * j]), b2 = ex2(e.f[32 * c + 2 * j + 1]);
+                        sum2 = f2add(sum2, pk(a, b2));
+                        w[j] = pack_h2(a, b2);
+                    }
+                    tmem_st16(ts + 16 * c, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_full(x));
+                float sa, sc;
+                upk(sum2, sa, sc);
+                l += sa + sc;
+            }
+            if (n > 0 && ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full(x), (uint32_t)n & 1u, ab, err));
+            tc_fence_after();
+            if (!(thr > 0.f)) m = -INFINITY;
+            if (ok) {
+                const long long at = (long long)(s.q0 + i) * p.heads + h, slot = (long long)blockIdx.x * kTileRows + 128 * x + row;
+                const float vtrue = pow2i(vref - 127), f = alone ? (l == 0.f ? 0.f : vtrue / l) : vtrue;
+                const float nan = __uint_as_float(0x7FC00000u);
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    if (n > 0) {
+                        tmem_ld16(to + c, o);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = 0;
+                    }
+                    const float g = (vnan >> (c >> 5)) & 1u ? nan : f;
+                    if (r < rows) {
+                        if (alone) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) w[j] = bf16x2(__uint_as_float(o[2 * j]) * g, __uint_as_float(o[2 * j + 1]) * g);
+                            uint4* const dst = reinterpret_cast<uint4*>(p.out + at * D + c);
+                            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        } else {
+                            float4* const dst = reinterpret_cast<float4*>(p.part + slot * D + c);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                dst[j] = make_float4(__uint_as_float(o[4 * j]) * g, __uint_as_float(o[4 * j + 1]) * g,
+                                                     __uint_as_float(o[4 * j + 2]) * g, __uint_as_float(o[4 * j + 3]) * g);
+                        }
+                    }
+                }
+                if (r < rows) {
+                    if (!alone) *reinterpret_cast<float2*>(p.part + p.part_ml + slot * 2) = make_float2(m, l);
+                    else if (p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
                 }
             }
-            // scales: 16 bytes are 16 / SROW keys; warp 0 K's, warp 1 V's
-            constexpr int PER = 16 / C::SROW;
-            const int src = min(lane, 128 / PER - 1) * PER >> 4;
-            const int x = __shfl_sync(0xFFFFFFFFu, pg, src), o = __shfl_sync(0xFFFFFFFFu, off, src);
-            if (w < 2 && lane < 128 / PER && x >= 0) {
-                const long long at = (((long long)x * p.c.heads + head) * p.c.page + o + (lane * PER & 15)) * C::SROW;
-                copy16(raw + (w ? C::RVS : C::RKS) + 16 * lane, (w ? p.c.vs : p.c.ks) + at);
+        }
+    } else if (warp < kTcMma) {
+        regs_down<104>();
+        // ---- decoding ----
+        const int blocks = work ? n : 0, w = warp - kTcDecode, d = 32 * w + lane;
+        bool live = true;
+        // The warp copies rows 32 j + 8 w .. + 7 (j < 4), of the four groups of 16 keys 2 j + w / 2, and of these groups the
+        // scales of K (even warps) or V. Their pages are loaded a block ahead and looked at when they are used.
+        int pg[4];
+        const bool vs = w & 1;
+        auto lookup = [&](int blk) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = (first + blk) * 128 + 16 * (2 * j + (w >> 1));
+                pg[j] = -1;
+                if (blk < blocks && key < s.len) pg[j] = __ldg(p.table + b * p.table_stride + p.by_page(key));
             }
-            return __ballot_sync(0xFFFFFFFFu, pg >= 0) & 0xFFu;
         };
-        lookup(0);
-        valid[0] = copy(0);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        lookup(1);
-        valid[1] = copy(1);
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        auto copy = [&](int blk, uint32_t raw) {
+            constexpr int PIECES = C::ROW / 16;            // 16-byte pieces of a row of codes
+            constexpr int SP = C::SROW;                     // and of a group's scales
+            const int lr = lane / PIECES, c = lane % PIECES;  // D = 64: 16 rows a time, in two of the four steps
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int g = 2 * j + (w >> 1), key = (first + blk) * 128 + 16 * g;
+                if (pg[j] < 0 || pg[j] >= p.c.pages) continue;
+                const long long at = ((long long)pg[j] * p.c.heads + head) * p.c.page + (key - p.by_page(key) * p.c.page);
+                if (D == 128) {
+                    const int rr = 8 * (w & 1) + lr, r = 16 * g + rr;
+                    const long long o = (at + rr) * C::ROW + 16 * c;
+                    copy16(raw + C::k_at(r, c), p.c.kc + o);
+                    copy16(raw + C::RV + C::v_at(r, c), p.c.vc + o);
+                } else {
+                    const int r = 16 * g + lr;
+                    const long long o = (at + lr) * C::ROW + 16 * c;
+                    if (vs) copy16(raw + C::RV + C::v_at(r, c), p.c.vc + o);
+                    else copy16(raw + C::k_at(r, c), p.c.kc + o);
+                }
+                if (lane < SP) copy16(raw + (vs ? C::RVS : C::RKS) + 16 * (SP * g + lane), (vs ? p.c.vs : p.c.ks) + at * C::SROW + 16 * lane);
+            }
+            // which of the eight groups are in pages: each pair of warps tells the others
+            if (lane == 0 && !vs) {
+                uint32_t bits = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (pg[j] >= 0 && pg[j] < p.c.pages) bits |= 1u << (2 * j + (w >> 1));
+                there[blk & 3][w >> 1] = bits;
+            }
+        };
+        uint32_t raw = sb + C::AT_RAW, put = raw;
+        auto next_raw = [&](uint32_t a) { return a + C::RAW == sb + C::AT_RAW + kTcRaw * C::RAW ? sb + C::AT_RAW : a + C::RAW; };
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            lookup(i);
+            copy(i, put);
+            put = next_raw(put);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
         lookup(2);
         int vref = -1000;
-        for (int it = 0; it < n; ++it) {
+        for (int it = 0; it < blocks; ++it, raw = next_raw(raw), put = next_raw(put)) {
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             group_barrier();  // block it has landed for all, and nobody reads block it - 1 any more
-            valid[2] = copy(it + 2);
+            const uint32_t pages = there[it & 3][0] | there[it & 3][1];
+            copy(it + 2, put);
             asm volatile("cp.async.commit_group;" ::: "memory");
             lookup(it + 3);
-            const uint32_t raw = sb + C::AT_RAW + (uint32_t)(it % kTcRaw) * C::RAW;
             const int key0 = (first + it) * 128;
-            const uint32_t pages = valid[0];
             const bool edge = pages != 0xFFu || key0 + 128 > s.len;
             // the block's largest scales, by every warp for itself
             bool nan = false;
@@ -446,13 +451,13 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                 fence_proxy_async();
                 if (live) mbar_arrive(k_full(it));
             }
-            if (live && it > 1) live = mbar_wait(v_empty(it), (uint32_t)((it >> 1) - 1) & 1u, ab, err);
+            if (live && it > 0) live = mbar_wait(v_empty, (uint32_t)(it - 1) & 1u, ab, err);
             {
                 // V: keys 64 u + 8 kg .. + 7, eight dimensions of one 32-value block
                 const int c0 = vref - 15;
                 const uint32_t floor2 = (uint32_t)(c0 & 0xFFFF) * 0x10001u, minus2 = (uint32_t)(-c0 * 0x10001);
                 const int kg = lane & 7, dg = lane >> 3, blk = D == 128 ? w : w & 1;
-                const uint32_t vb = sb + C::AT_V + (uint32_t)(it & 1) * C::V;
+                const uint32_t vb = sb + C::AT_V;
 #pragma unroll
                 for (int uu = 0; uu < (D == 128 ? 2 : 1); ++uu) {
                     const int u = D == 128 ? uu : w >> 1, k0 = u * 64 + kg * 8;
@@ -497,60 +502,68 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                     }
                 }
                 fence_proxy_async();
-                if (live) mbar_arrive(v_full(it));
+                if (live) mbar_arrive(v_full);
             }
-            valid[0] = valid[1];
-            valid[1] = valid[2];
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-    } else if (work && n > 0) {
-        // ---- MMAs ----
-        const bool one = elect_one();
-        constexpr uint32_t id_s = idesc_f16(128, 128), id_o = idesc_f16(128, D);
-        const SmemDesc dq = desc_sw128(sb);
-        bool ok = mbar_wait(q_full, 0, ab, err);
-        tc_fence_after();
-        for (int it = 0; ok && it <= n; ++it) {
-            if (it < n) {
-                ok = mbar_wait(k_full(it), (uint32_t)(it >> 1) & 1u, ab, err);
-                if (ok && it > 1) ok = mbar_wait(s_empty(it), (uint32_t)((it >> 1) - 1) & 1u, ab, err);
-                if (!ok) break;
-                tc_fence_after();
+    } else {
+        regs_down<40>();
+        if (warp == kTcMma && work && n > 0) {
+            // ---- MMAs ----
+            const bool one = elect_one();
+            constexpr uint32_t id_s = idesc_f16(128, 128), id_o = idesc_f16(128, D);
+            const SmemDesc dq = desc_sw128(sb);
+            bool ok = true;
+            auto scores = [&](int x, int it) {  // S of tile x
                 if (one) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
-                        tc_mma_f16(tm + kColS + 128 * (it & 1), dq + at, dq + (C::AT_K + (it & 1) * C::K + at), id_s, k > 0);
+                        tc_mma_f16(tm + kColS + 128 * x, dq + (x * C::Q + at), dq + (C::AT_K + (it & 1) * C::K + at), id_s, k > 0);
                     }
-                    tc_commit(k_empty(it));
-                    tc_commit(s_full(it));
+                    if (x == two) tc_commit(k_empty(it));
+                    tc_commit(s_full(x));
                 }
-            }
-            if (it > 0) {
-                const int j = it - 1;
-                ok = mbar_wait(v_full(j), (uint32_t)(j >> 1) & 1u, ab, err) && mbar_wait(p_full(j), (uint32_t)(j >> 1) & 1u, ab, err);
-                if (!ok) break;
+            };
+            ok = mbar_wait(k_full(0), 0, ab, err);
+            for (int x = 0; ok && x <= two; ++x) {
+                ok = mbar_wait(q_full(x), 0, ab, err);
                 tc_fence_after();
-                if (one) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        tc_mma_f16_ts(tm + kColO, tm + kColP + 64 * (j & 1) + 8 * k,
-                                      dq + (C::AT_V + (j & 1) * C::V + (k >> 2) * (D * 128) + (k & 3) * 32), id_o, j > 0 || k > 0);
-                    tc_commit(v_empty(j));
-                    tc_commit(pv_done(j));
-                }
+                if (ok) scores(x, 0);
             }
-        }
-        if (one && *ab) {  // MMAs in flight end before their shared and tensor memory goes away
-            tc_commit(drained);
-            const unsigned long long t0 = global_ns();
-            while (!mbar_test(drained, 0) && global_ns() - t0 < kWaitLimitNs) {
+            for (int it = 0; ok && it < n; ++it)
+                for (int x = 0; ok && x <= two; ++x) {
+                    if (x == 0) ok = mbar_wait(v_full, (uint32_t)it & 1u, ab, err);
+                    ok = ok && mbar_wait(p_full(x), (uint32_t)it & 1u, ab, err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (one) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            tc_mma_f16_ts(tm + kColO + 128 * x, tm + kColS + 128 * x + 8 * k, dq + (C::AT_V + (k >> 2) * (D * 128) + (k & 3) * 32),
+                                          id_o, it > 0 || k > 0);
+                        if (x == two) tc_commit(v_empty);
+                    }
+                    if (it + 1 < n) {
+                        // S of the next block over P, which the product before has read (they execute in order)
+                        if (x == 0) ok = mbar_wait(k_full(it + 1), (uint32_t)((it + 1) >> 1) & 1u, ab, err);
+                        tc_fence_after();
+                        if (ok) scores(x, it + 1);
+                    } else if (one) {
+                        tc_commit(s_full(x));
+                    }
+                }
+            if (one && *ab) {  // MMAs in flight end before their shared and tensor memory goes away
+                tc_commit(drained);
+                const unsigned long long t0 = global_ns();
+                while (!mbar_test(drained, 0) && global_ns() - t0 < kWaitLimitNs) {
+                }
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kTcMma) {
         tc_fence_after();
         tmem_free<512>(tm);
     }
