@@ -5,7 +5,7 @@
 //   S = Q K^T (fp32 in tensor memory),  P = 2^(S - m) (f16, over S),  O += P V (fp32, tensor memory),
 // with the formulas, the relative block scales and the masks of mxq_attention.cu. Decoding 128 keys then serves 256
 // rows, not 32 as in a warp's registers there. Roles:
-// - four decoding warps bring a block's codes to shared memory (16-byte asynchronous copies, two blocks ahead), turn
+// - four decoding warps bring a block's codes to shared memory (16-byte asynchronous copies, a block ahead), turn
 //   them into f16 operands in the 128-byte swizzle and hand them to the tensor core: K as [key][dimension], V
 //   transposed, [dimension][key], by interleaving the nibbles of two keys before the conversion, so that both
 //   products have the summed index contiguous. The places of the raw codes are permuted so that these reads, like the
@@ -317,132 +317,133 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
         regs_down<104>();
         // ---- decoding ----
         const int blocks = work ? n : 0, w = warp - kTcDecode, d = 32 * w + lane;
-        bool live = true;
-        // The warp copies rows 32 j + 8 w .. + 7 (j < 4), of the four groups of 16 keys 2 j + w / 2, and of these groups the
-        // scales of K (even warps) or V. Their pages are loaded a block ahead and looked at when they are used.
-        int pg[4];
-        const bool vs = w & 1;
+        // The warp copies rows 32 j + 8 (w & 1) + 16 (w / 2) .. + 7 (j < 4), of the four groups of 16 keys 2 j + w / 2, and
+        // of these groups the scales of K (even warps) or V. Their pages are loaded a block ahead and looked at when
+        // they are used.
+        constexpr int PIECES = C::ROW / 16;  // 16-byte pieces of a row of codes
+        const bool odd = w & 1;
+        const int lr = lane / PIECES + (D == 128 ? 8 * (w & 1) : 0), lc = lane % PIECES;  // the lane's row of a group, and piece
+        const long long page_rows = (long long)p.c.heads * p.c.page, head_row = (long long)head * p.c.page;
+        const char* const k_lane = p.c.kc + (head_row + lr) * C::ROW + 16 * lc;
+        const char* const v_lane = p.c.vc + (head_row + lr) * C::ROW + 16 * lc;
+        const uint8_t* const s_lane = (odd ? p.c.vs : p.c.ks) + head_row * C::SROW + 16 * lane;
+        int pg[4], off[4];
         auto lookup = [&](int blk) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int key = (first + blk) * 128 + 16 * (2 * j + (w >> 1));
                 pg[j] = -1;
-                if (blk < blocks && key < s.len) pg[j] = __ldg(p.table + b * p.table_stride + p.by_page(key));
+                if (blk < blocks && key < s.len) {
+                    const int at = p.by_page(key);
+                    off[j] = key - at * p.c.page;
+                    pg[j] = __ldg(p.table + b * p.table_stride + at);
+                }
             }
         };
         auto copy = [&](int blk, uint32_t raw) {
-            constexpr int PIECES = C::ROW / 16;            // 16-byte pieces of a row of codes
-            constexpr int SP = C::SROW;                     // and of a group's scales
-            const int lr = lane / PIECES, c = lane % PIECES;  // D = 64: 16 rows a time, in two of the four steps
+            uint32_t bits = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int g = 2 * j + (w >> 1), key = (first + blk) * 128 + 16 * g;
+                const int g = 2 * j + (w >> 1), r = 16 * g + lr;
                 if (pg[j] < 0 || pg[j] >= p.c.pages) continue;
-                const long long at = ((long long)pg[j] * p.c.heads + head) * p.c.page + (key - p.by_page(key) * p.c.page);
-                if (D == 128) {
-                    const int rr = 8 * (w & 1) + lr, r = 16 * g + rr;
-                    const long long o = (at + rr) * C::ROW + 16 * c;
-                    copy16(raw + C::k_at(r, c), p.c.kc + o);
-                    copy16(raw + C::RV + C::v_at(r, c), p.c.vc + o);
-                } else {
-                    const int r = 16 * g + lr;
-                    const long long o = (at + lr) * C::ROW + 16 * c;
-                    if (vs) copy16(raw + C::RV + C::v_at(r, c), p.c.vc + o);
-                    else copy16(raw + C::k_at(r, c), p.c.kc + o);
-                }
-                if (lane < SP) copy16(raw + (vs ? C::RVS : C::RKS) + 16 * (SP * g + lane), (vs ? p.c.vs : p.c.ks) + at * C::SROW + 16 * lane);
+                bits |= 1u << g;
+                const long long at = pg[j] * page_rows + off[j], o = at * C::ROW;
+                if (D == 128 || !odd) copy16(raw + C::k_at(r, lc), k_lane + o);
+                if (D == 128 || odd) copy16(raw + C::RV + C::v_at(r, lc), v_lane + o);
+                if (lane < C::SROW) copy16(raw + (odd ? C::RVS : C::RKS) + 16 * (C::SROW * g + lane), s_lane + at * C::SROW);
             }
-            // which of the eight groups are in pages: each pair of warps tells the others
-            if (lane == 0 && !vs) {
-                uint32_t bits = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (pg[j] >= 0 && pg[j] < p.c.pages) bits |= 1u << (2 * j + (w >> 1));
-                there[blk & 3][w >> 1] = bits;
-            }
+            if (lane == 0 && !odd) there[blk & 3][w >> 1] = bits;  // two warps have the same groups: one tells the others
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        uint32_t raw = sb + C::AT_RAW, put = raw;
         auto next_raw = [&](uint32_t a) { return a + C::RAW == sb + C::AT_RAW + kTcRaw * C::RAW ? sb + C::AT_RAW : a + C::RAW; };
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            lookup(i);
-            copy(i, put);
-            put = next_raw(put);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        }
-        lookup(2);
-        int vref = -1000;
-        for (int it = 0; it < blocks; ++it, raw = next_raw(raw), put = next_raw(put)) {
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            group_barrier();  // block it has landed for all, and nobody reads block it - 1 any more
-            const uint32_t pages = there[it & 3][0] | there[it & 3][1];
-            copy(it + 2, put);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            lookup(it + 3);
+        uint32_t raw = sb + C::AT_RAW, raw_v = raw;
+        lookup(0);
+        copy(0, raw);
+        lookup(1);
+        bool live = true;
+        int vref = -1000, vref_v = 0;
+        uint32_t pages_v = 0;
+        bool nan_v = false;
+        // step it: K of block it, then V of block it - 1 (K's two buffers let it run ahead of the products that still read V)
+        for (int it = 0; it <= blocks; ++it) {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            group_barrier();  // block it has landed for all, and nobody reads block it - 2 any more
+            copy(it + 1, next_raw(raw));
+            lookup(it + 2);
             const int key0 = (first + it) * 128;
-            const bool edge = pages != 0xFFu || key0 + 128 > s.len;
-            // the block's largest scales, by every warp for itself
+            uint32_t pages = 0;
             bool nan = false;
-            int top[2];
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                uint32_t x[4] = {0, 0, 0, 0};
+            if (it < blocks) {
+                pages = there[it & 3][0] | there[it & 3][1];
+                const bool edge = pages != 0xFFu || key0 + 128 > s.len;
+                // the block's largest scales, by every warp for itself
+                int top[2];
+                uint32_t x[2][4];
                 constexpr int PER = 16 / C::SROW;
-                if (lane < 128 / PER) {
-                    const uint4 y = lds128u(raw + (v ? C::RVS : C::RKS) + 16 * lane);
-                    x[0] = y.x;
-                    x[1] = y.y;
-                    x[2] = y.z;
-                    x[3] = y.w;
+                const uint32_t at = raw + 16 * min(lane, 128 / PER - 1);
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const uint4 y = lds128u(at + (v ? C::RVS : C::RKS));
+                    x[v][0] = y.x;
+                    x[v][1] = y.y;
+                    x[v][2] = y.z;
+                    x[v][3] = y.w;
+                }
+                // K: thread d decodes key d
+                uint32_t sw, kx[C::SROW][4];
+                if constexpr (D == 128) sw = lds32(raw + C::RKS + 4 * d);
+                else sw = (lds32(raw + C::RKS + 4 * (d >> 1)) >> (16 * (d & 1))) & 0xFFFFu;
+#pragma unroll
+                for (int j = 0; j < C::SROW; ++j) {
+                    const uint4 y = lds128u(raw + C::k_at(d, j));
+                    kx[j][0] = y.x;
+                    kx[j][1] = y.y;
+                    kx[j][2] = y.z;
+                    kx[j][3] = y.w;
+                }
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
                     if (edge) {
-                        const int key = lane * PER;
-                        const bool there = (pages >> (key >> 4)) & 1u;
+                        const int key = min(lane, 128 / PER - 1) * PER;
+                        const bool in = (pages >> (key >> 4)) & 1u;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             if constexpr (D == 128) {
-                                if (!there || key0 + key + i >= s.len) x[i] = 0;
+                                if (!in || key0 + key + i >= s.len) x[v][i] = 0;
                             } else {
-                                if (!there || key0 + key + 2 * i >= s.len) x[i] = 0;
-                                else if (key0 + key + 2 * i + 1 >= s.len) x[i] &= 0xFFFFu;
+                                if (!in || key0 + key + 2 * i >= s.len) x[v][i] = 0;
+                                else if (key0 + key + 2 * i + 1 >= s.len) x[v][i] &= 0xFFFFu;
                             }
                         }
                     }
+                    top[v] = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)max_byte(x[v], nan));
                 }
-                top[v] = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)max_byte(x, nan));
-            }
-            nan = __any_sync(0xFFFFFFFFu, nan);
-            const int kref = top[0] - 13;
-            if (top[1] > vref + 13) vref = top[1] - 6;
-            if (live && it > 1) live = mbar_wait(k_empty(it), (uint32_t)((it >> 1) - 1) & 1u, ab, err);
-            if (d == 0) infos[it & 3] = {kref, vref, pages, nan ? 1u : 0u};
-            if (nan) {
-                // value blocks that are NaN, of key d
-                uint32_t bits = 0;
+                nan = __any_sync(0xFFFFFFFFu, nan);
+                const int kref = top[0] - 13;
+                if (top[1] > vref + 13) vref = top[1] - 6;
+                if (live && it > 1) live = mbar_wait(k_empty(it), (uint32_t)((it >> 1) - 1) & 1u, ab, err);
+                if (d == 0) infos[it & 3] = {kref, vref, pages, nan ? 1u : 0u};
+                if (nan) {
+                    // value blocks that are NaN, of key d
+                    uint32_t bits = 0;
 #pragma unroll
-                for (int j = 0; j < C::SROW; ++j)
-                    if (lds8(raw + C::RVS + d * C::SROW + j) == 0xFFu) bits |= 1u << j;
-                if (key0 + d >= s.len || !((pages >> (d >> 4)) & 1u)) bits = 0;
-                nan_keys[it & 3][d] = (uint8_t)bits;
-            }
-            {
-                // K: thread d decodes key d
+                    for (int j = 0; j < C::SROW; ++j)
+                        if (lds8(raw + C::RVS + d * C::SROW + j) == 0xFFu) bits |= 1u << j;
+                    if (key0 + d >= s.len || !((pages >> (d >> 4)) & 1u)) bits = 0;
+                    nan_keys[it & 3][d] = (uint8_t)bits;
+                }
                 const int c0 = kref - 15;
                 const uint32_t floor2 = (uint32_t)(c0 & 0xFFFF) * 0x10001u, minus2 = (uint32_t)(-c0 * 0x10001);
-                uint32_t sw;
-                if constexpr (D == 128) sw = lds32(raw + C::RKS + 4 * d);
-                else sw = (lds32(raw + C::RKS + 4 * (d >> 1)) >> (16 * (d & 1))) & 0xFFFFu;
                 const uint32_t kb = sb + C::AT_K + (uint32_t)(it & 1) * C::K + d * 128;
 #pragma unroll
                 for (int j = 0; j < C::SROW; ++j) {
                     const uint32_t byte = (sw >> (8 * j)) & 0xFFu;
                     uint32_t f = scale_pair(byte * 0x10001u, floor2, minus2);
                     if (byte == 0xFFu) f = 0x7E007E00u;
-                    const uint4 x = lds128u(raw + C::k_at(d, j));
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t o[4];
-                        e2m1_to_h2(xs[k], o);
+                        e2m1_to_h2(kx[j][k], o);
                         const int ch = (j & 1) * 4 + k;
                         sts128(kb + (j >> 1) * 16384 + ((ch ^ (d & 7)) << 4), mul_h2(o[0], f), mul_h2(o[1], f), mul_h2(o[2], f),
                                mul_h2(o[3], f));
@@ -451,59 +452,68 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                 fence_proxy_async();
                 if (live) mbar_arrive(k_full(it));
             }
-            if (live && it > 0) live = mbar_wait(v_empty, (uint32_t)(it - 1) & 1u, ab, err);
-            {
+            if (it > 0) {
                 // V: keys 64 u + 8 kg .. + 7, eight dimensions of one 32-value block
-                const int c0 = vref - 15;
+                const int key0v = key0 - 128;
+                const bool some = pages_v != 0xFFu || key0v + 128 > s.len || nan_v;
+                const int c0 = vref_v - 15;
                 const uint32_t floor2 = (uint32_t)(c0 & 0xFFFF) * 0x10001u, minus2 = (uint32_t)(-c0 * 0x10001);
                 const int kg = lane & 7, dg = lane >> 3, blk = D == 128 ? w : w & 1;
-                const uint32_t vb = sb + C::AT_V;
+                constexpr int UNITS = D == 128 ? 2 : 1;
+                uint32_t x[UNITS][8], sc[UNITS][4];
 #pragma unroll
-                for (int uu = 0; uu < (D == 128 ? 2 : 1); ++uu) {
-                    const int u = D == 128 ? uu : w >> 1, k0 = u * 64 + kg * 8;
-                    uint32_t x[8], sc[4];
+                for (int uu = 0; uu < UNITS; ++uu) {
+                    const int k0 = (D == 128 ? uu : w >> 1) * 64 + kg * 8;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = lds32(raw + C::RV + C::v_at(k0 + j, blk) + 4 * dg);
-                    {
-                        uint32_t sw[8];  // low halves: the keys' scale of the block
-                        if constexpr (D == 128) {
-                            const uint4 a = lds128u(raw + C::RVS + 4 * k0), c = lds128u(raw + C::RVS + 4 * k0 + 16);
-                            const uint32_t y[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+                    for (int j = 0; j < 8; ++j) x[uu][j] = lds32(raw_v + C::RV + C::v_at(k0 + j, blk) + 4 * dg);
+                    uint32_t sw[8];  // the keys' scale of the block
+                    if constexpr (D == 128) {
+                        const uint4 a = lds128u(raw_v + C::RVS + 4 * k0), c = lds128u(raw_v + C::RVS + 4 * k0 + 16);
+                        const uint32_t y[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) sw[j] = (y[j] >> (8 * blk)) & 0xFFu;
-                        } else {
-                            const uint4 a = lds128u(raw + C::RVS + 2 * k0);
-                            const uint32_t y[4] = {a.x, a.y, a.z, a.w};
+                        for (int j = 0; j < 8; ++j) sw[j] = (y[j] >> (8 * blk)) & 0xFFu;
+                    } else {
+                        const uint4 a = lds128u(raw_v + C::RVS + 2 * k0);
+                        const uint32_t y[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) sw[j] = (y[j >> 1] >> (16 * (j & 1) + 8 * blk)) & 0xFFu;
-                        }
-                        if (edge || nan) {
-                            const bool there = (pages >> (k0 >> 4)) & 1u;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (!there || key0 + k0 + j >= s.len || sw[j] == 0xFFu) sw[j] = 0;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) sc[j] = scale_pair(sw[2 * j] | (sw[2 * j + 1] << 16), floor2, minus2);
+                        for (int j = 0; j < 8; ++j) sw[j] = (y[j >> 1] >> (16 * (j & 1) + 8 * blk)) & 0xFFu;
                     }
+                    if (some) {
+                        const bool in = (pages_v >> (k0 >> 4)) & 1u;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (!in || key0v + k0 + j >= s.len || sw[j] == 0xFFu) sw[j] = 0;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sc[uu][j] = scale_pair(sw[2 * j] | (sw[2 * j + 1] << 16), floor2, minus2);
+                }
+                if (live && it > 1) live = mbar_wait(v_empty, (uint32_t)(it - 2) & 1u, ab, err);
+#pragma unroll
+                for (int uu = 0; uu < UNITS; ++uu) {
+                    const int u = D == 128 ? uu : w >> 1;
                     uint32_t ev[4][4], od[4][4];  // [pair of keys][dimension / 2]
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        e2m1_to_h2((x[2 * j] & 0x0F0F0F0Fu) | ((x[2 * j + 1] << 4) & 0xF0F0F0F0u), ev[j]);
-                        e2m1_to_h2(((x[2 * j] >> 4) & 0x0F0F0F0Fu) | (x[2 * j + 1] & 0xF0F0F0F0u), od[j]);
+                        e2m1_to_h2((x[uu][2 * j] & 0x0F0F0F0Fu) | ((x[uu][2 * j + 1] << 4) & 0xF0F0F0F0u), ev[j]);
+                        e2m1_to_h2(((x[uu][2 * j] >> 4) & 0x0F0F0F0Fu) | (x[uu][2 * j + 1] & 0xF0F0F0F0u), od[j]);
                     }
-                    const uint32_t row = vb + (uint32_t)u * (D * 128) + (uint32_t)(blk * 32 + dg * 8) * 128;
+                    const uint32_t row = sb + C::AT_V + (uint32_t)u * (D * 128) + (uint32_t)(blk * 32 + dg * 8) * 128;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        sts128(row + (2 * k) * 128 + ((kg ^ (2 * k)) << 4), mul_h2(ev[0][k], sc[0]), mul_h2(ev[1][k], sc[1]),
-                               mul_h2(ev[2][k], sc[2]), mul_h2(ev[3][k], sc[3]));
-                        sts128(row + (2 * k + 1) * 128 + ((kg ^ (2 * k + 1)) << 4), mul_h2(od[0][k], sc[0]), mul_h2(od[1][k], sc[1]),
-                               mul_h2(od[2][k], sc[2]), mul_h2(od[3][k], sc[3]));
+                        sts128(row + (2 * k) * 128 + ((kg ^ (2 * k)) << 4), mul_h2(ev[0][k], sc[uu][0]), mul_h2(ev[1][k], sc[uu][1]),
+                               mul_h2(ev[2][k], sc[uu][2]), mul_h2(ev[3][k], sc[uu][3]));
+                        sts128(row + (2 * k + 1) * 128 + ((kg ^ (2 * k + 1)) << 4), mul_h2(od[0][k], sc[uu][0]),
+                               mul_h2(od[1][k], sc[uu][1]), mul_h2(od[2][k], sc[uu][2]), mul_h2(od[3][k], sc[uu][3]));
                     }
                 }
                 fence_proxy_async();
                 if (live) mbar_arrive(v_full);
             }
+            raw_v = raw;
+            raw = next_raw(raw);
+            pages_v = pages;
+            vref_v = vref;
+            nan_v = nan;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else {
