@@ -5,11 +5,12 @@
 //   S = Q K^T (fp32 in tensor memory),  P = 2^(S - m) (f16, over S),  O += P V (fp32, tensor memory),
 // with the formulas, the relative block scales and the masks of mxq_attention.cu. Decoding 128 keys then serves 256
 // rows, not 32 as in a warp's registers there. Roles:
-// - four decoding warps bring a block's codes to shared memory (16-byte asynchronous copies, a block ahead), turn
-//   them into f16 operands in the 128-byte swizzle and hand them to the tensor core: K as [key][dimension], V
-//   transposed, [dimension][key], by interleaving the nibbles of two keys before the conversion, so that both
-//   products have the summed index contiguous. The places of the raw codes are permuted so that these reads, like the
-//   16-byte writes, touch every bank once.
+// - two warps bring the blocks' codes to a ring in shared memory (16-byte asynchronous copies), one finds their largest
+//   scales.
+// - four decoding warps turn the codes into f16 operands in the 128-byte swizzle: K as [key][dimension], V transposed,
+//   [dimension][key], by interleaving the nibbles of two keys before the conversion, so that both products have the
+//   summed index contiguous. The places of the raw codes are permuted so that these reads, like the 16-byte writes,
+//   touch every bank once. K is a block ahead of V.
 // - four softmax warps per tile, a row per thread: its 128 scores come from tensor memory, the weights go back as the A
 //   operand of the second product. The maximum is raised (and O rescaled, in tensor memory) only when a score exceeds
 //   it by 2^8, or when a value block exceeds 2^13 of the reference scale.
@@ -29,9 +30,9 @@
 namespace mxq {
 namespace {
 
-// warpgroups: softmax of the two tiles, decoding, MMA (one warp of it). Registers are moved between them: 128 a thread
+// warpgroups: softmax of the two tiles, decoding, and one of single warps: MMA, two of copies, scales. Registers are moved between them: 128 a thread
 // at launch = (184 + 184 + 104 + 40) / 4
-constexpr int kTcThreads = 512, kTcDecode = 8, kTcMma = 12;
+constexpr int kTcThreads = 512, kTcDecode = 8, kTcMma = 12, kTcCopy = 13, kTcScales = 15;
 template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 constexpr int kTcRaw = 3;        // blocks in the ring of raw codes
@@ -56,19 +57,29 @@ template <int D> struct TcCfg {
 // tensor memory columns
 constexpr int kColS = 0, kColO = 256;  // + 128 for the second tile
 
-// what the decoding warps tell the softmax warps about a block
+// what the scales' warp tells the others about a block
 struct BlockInfo {
     int kref, vref;      // reference scale bytes
     uint32_t pages;      // bit j: keys 16 j .. are in a page of the cache
     uint32_t nan;        // a value block of the block of keys is NaN: nan_keys holds which
 };
 
+// position in a ring of n places: place and the parity of its current use
+struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++s == n) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
+};
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-__device__ __forceinline__ void group_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // f16 factors 2^(byte - ref) of two scale bytes (in the halves of x), 0 below 2^-14: the exponent fields byte - ref + 15,
 // with floor2 = ref - 15 in both halves and minus2 the number that takes it off both
 __device__ __forceinline__ uint32_t scale_pair(uint32_t x, uint32_t floor2, uint32_t minus2) {
@@ -95,12 +106,12 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
     extern __shared__ uint8_t dsm8[];
     uint8_t* const base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm8) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(base);
-    __shared__ __align__(8) unsigned long long bars[13];
+    __shared__ __align__(8) unsigned long long bars[22];
     __shared__ uint32_t tmem_addr;
     __shared__ int abort_flag;
-    __shared__ BlockInfo infos[4];
-    __shared__ uint32_t there[4][2];      // groups of 16 keys of a block that are in pages: even and odd ones
-    __shared__ uint8_t nan_keys[4][128];  // of a block with NaN values: bit b of key's byte: its block b is NaN
+    __shared__ BlockInfo infos[8];  // eight blocks: more than the roles can be apart
+    __shared__ uint32_t there[8][2];      // groups of 16 keys of a block that are in pages: even and odd ones
+    __shared__ uint8_t nan_keys[8][128];  // of a block with NaN values: bit b of key's byte: its block b is NaN
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     auto k_full = [&](int i) { return bar(i & 1); };
@@ -109,7 +120,15 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
     auto q_full = [&](int x) { return bar(7 + x); };   // of tile x
     auto s_full = [&](int x) { return bar(9 + x); };   // S of a block, and everything issued before it; at the end, O
     auto p_full = [&](int x) { return bar(11 + x); };  // P of a block
+    auto raw_full = [&](int i) { return bar(13 + i); };   // of a place in the ring of raw codes
+    auto raw_empty = [&](int i) { return bar(16 + i); };
+    auto info_full = [&](int i) { return bar(19 + i); };
     if (t == 0) {
+        for (int i = 0; i < kTcRaw; ++i) {
+            mbar_init(raw_full(i), 66);  // the copies of 64 threads, and two that tell of the pages
+            mbar_init(raw_empty(i), 128);
+            mbar_init(info_full(i), 1);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(k_full(i), 128);
             mbar_init(k_empty(i), 1);
@@ -192,7 +211,7 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full(x), (uint32_t)it & 1u, ab, err));
                 if (!ok) break;
                 tc_fence_after();
-                const BlockInfo bi = infos[it & 3];
+                const BlockInfo bi = infos[it & 7];
                 const int key0 = (first + it) * 128;
                 union {
                     uint32_t u[128];
@@ -204,7 +223,7 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                 tmem_wait_ld();
                 if (bi.nan) {
                     for (int j = 0; j < 128; ++j) {
-                        const uint32_t bits = nan_keys[it & 3][j];
+                        const uint32_t bits = nan_keys[it & 7][j];
                         if (key0 + j < see_hi && key0 + j >= see_lo) vnan |= bits;
                     }
                 }
@@ -315,80 +334,21 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
         }
     } else if (warp < kTcMma) {
         regs_down<104>();
-        // ---- decoding ----
-        const int blocks = work ? n : 0, w = warp - kTcDecode, d = 32 * w + lane;
-        // The warp copies rows 32 j + 8 (w & 1) + 16 (w / 2) .. + 7 (j < 4), of the four groups of 16 keys 2 j + w / 2, and
-        // of these groups the scales of K (even warps) or V. Their pages are loaded a block ahead and looked at when
-        // they are used.
-        constexpr int PIECES = C::ROW / 16;  // 16-byte pieces of a row of codes
-        const bool odd = w & 1;
-        const int lr = lane / PIECES + (D == 128 ? 8 * (w & 1) : 0), lc = lane % PIECES;  // the lane's row of a group, and piece
-        const long long page_rows = (long long)p.c.heads * p.c.page, head_row = (long long)head * p.c.page;
-        const char* const k_lane = p.c.kc + (head_row + lr) * C::ROW + 16 * lc;
-        const char* const v_lane = p.c.vc + (head_row + lr) * C::ROW + 16 * lc;
-        const uint8_t* const s_lane = (odd ? p.c.vs : p.c.ks) + head_row * C::SROW + 16 * lane;
-        int pg[4], off[4];
-        auto lookup = [&](int blk) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int key = (first + blk) * 128 + 16 * (2 * j + (w >> 1));
-                pg[j] = -1;
-                if (blk < blocks && key < s.len) {
-                    const int at = p.by_page(key);
-                    off[j] = key - at * p.c.page;
-                    pg[j] = __ldg(p.table + b * p.table_stride + at);
-                }
-            }
-        };
-        auto copy = [&](int blk, uint32_t raw) {
-            uint32_t bits = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int g = 2 * j + (w >> 1), r = 16 * g + lr;
-                if (pg[j] < 0 || pg[j] >= p.c.pages) continue;
-                bits |= 1u << g;
-                const long long at = pg[j] * page_rows + off[j], o = at * C::ROW;
-                if (D == 128 || !odd) copy16(raw + C::k_at(r, lc), k_lane + o);
-                if (D == 128 || odd) copy16(raw + C::RV + C::v_at(r, lc), v_lane + o);
-                if (lane < C::SROW) copy16(raw + (odd ? C::RVS : C::RKS) + 16 * (C::SROW * g + lane), s_lane + at * C::SROW);
-            }
-            if (lane == 0 && !odd) there[blk & 3][w >> 1] = bits;  // two warps have the same groups: one tells the others
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        auto next_raw = [&](uint32_t a) { return a + C::RAW == sb + C::AT_RAW + kTcRaw * C::RAW ? sb + C::AT_RAW : a + C::RAW; };
-        uint32_t raw = sb + C::AT_RAW, raw_v = raw;
-        lookup(0);
-        copy(0, raw);
-        lookup(1);
-        bool live = true;
-        int vref = -1000, vref_v = 0;
+        // ---- decoding: K of block it, then V of block it - 1 (K's two buffers let it run ahead of the products that
+        // still read V) ----
+        const int w = warp - kTcDecode, d = 32 * w + lane;
+        Ring at, at_v;
         uint32_t pages_v = 0;
-        bool nan_v = false;
-        // step it: K of block it, then V of block it - 1 (K's two buffers let it run ahead of the products that still read V)
-        for (int it = 0; it <= blocks; ++it) {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            group_barrier();  // block it has landed for all, and nobody reads block it - 2 any more
-            copy(it + 1, next_raw(raw));
-            lookup(it + 2);
+        int vref_v = 0;
+        bool nan_v = false, live = work && n > 0;
+        for (int it = 0; live && it <= n; ++it) {
             const int key0 = (first + it) * 128;
-            uint32_t pages = 0;
-            bool nan = false;
-            if (it < blocks) {
-                pages = there[it & 3][0] | there[it & 3][1];
-                const bool edge = pages != 0xFFu || key0 + 128 > s.len;
-                // the block's largest scales, by every warp for itself
-                int top[2];
-                uint32_t x[2][4];
-                constexpr int PER = 16 / C::SROW;
-                const uint32_t at = raw + 16 * min(lane, 128 / PER - 1);
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const uint4 y = lds128u(at + (v ? C::RVS : C::RKS));
-                    x[v][0] = y.x;
-                    x[v][1] = y.y;
-                    x[v][2] = y.z;
-                    x[v][3] = y.w;
-                }
+            BlockInfo bi{0, 0, 0, 0};
+            if (it < n) {
+                live = mbar_wait(raw_full(at.s), at.phase, ab, err) && mbar_wait(info_full(at.s), at.phase, ab, err);
+                if (!live) break;
+                const uint32_t raw = sb + C::AT_RAW + (uint32_t)at.s * C::RAW;
+                bi = infos[it & 7];
                 // K: thread d decodes key d
                 uint32_t sw, kx[C::SROW][4];
                 if constexpr (D == 128) sw = lds32(raw + C::RKS + 4 * d);
@@ -401,40 +361,20 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                     kx[j][2] = y.z;
                     kx[j][3] = y.w;
                 }
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    if (edge) {
-                        const int key = min(lane, 128 / PER - 1) * PER;
-                        const bool in = (pages >> (key >> 4)) & 1u;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if constexpr (D == 128) {
-                                if (!in || key0 + key + i >= s.len) x[v][i] = 0;
-                            } else {
-                                if (!in || key0 + key + 2 * i >= s.len) x[v][i] = 0;
-                                else if (key0 + key + 2 * i + 1 >= s.len) x[v][i] &= 0xFFFFu;
-                            }
-                        }
-                    }
-                    top[v] = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)max_byte(x[v], nan));
-                }
-                nan = __any_sync(0xFFFFFFFFu, nan);
-                const int kref = top[0] - 13;
-                if (top[1] > vref + 13) vref = top[1] - 6;
-                if (live && it > 1) live = mbar_wait(k_empty(it), (uint32_t)((it >> 1) - 1) & 1u, ab, err);
-                if (d == 0) infos[it & 3] = {kref, vref, pages, nan ? 1u : 0u};
-                if (nan) {
+                if (bi.nan) {
                     // value blocks that are NaN, of key d
                     uint32_t bits = 0;
 #pragma unroll
                     for (int j = 0; j < C::SROW; ++j)
                         if (lds8(raw + C::RVS + d * C::SROW + j) == 0xFFu) bits |= 1u << j;
-                    if (key0 + d >= s.len || !((pages >> (d >> 4)) & 1u)) bits = 0;
-                    nan_keys[it & 3][d] = (uint8_t)bits;
+                    if (key0 + d >= s.len || !((bi.pages >> (d >> 4)) & 1u)) bits = 0;
+                    nan_keys[it & 7][d] = (uint8_t)bits;
                 }
-                const int c0 = kref - 15;
+                const int c0 = bi.kref - 15;
                 const uint32_t floor2 = (uint32_t)(c0 & 0xFFFF) * 0x10001u, minus2 = (uint32_t)(-c0 * 0x10001);
                 const uint32_t kb = sb + C::AT_K + (uint32_t)(it & 1) * C::K + d * 128;
+                if (it > 1) live = mbar_wait(k_empty(it), (uint32_t)((it >> 1) - 1) & 1u, ab, err);
+                if (!live) break;
 #pragma unroll
                 for (int j = 0; j < C::SROW; ++j) {
                     const uint32_t byte = (sw >> (8 * j)) & 0xFFu;
@@ -450,10 +390,11 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                     }
                 }
                 fence_proxy_async();
-                if (live) mbar_arrive(k_full(it));
+                mbar_arrive(k_full(it));
             }
             if (it > 0) {
                 // V: keys 64 u + 8 kg .. + 7, eight dimensions of one 32-value block
+                const uint32_t raw = sb + C::AT_RAW + (uint32_t)at_v.s * C::RAW;
                 const int key0v = key0 - 128;
                 const bool some = pages_v != 0xFFu || key0v + 128 > s.len || nan_v;
                 const int c0 = vref_v - 15;
@@ -465,15 +406,15 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                 for (int uu = 0; uu < UNITS; ++uu) {
                     const int k0 = (D == 128 ? uu : w >> 1) * 64 + kg * 8;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[uu][j] = lds32(raw_v + C::RV + C::v_at(k0 + j, blk) + 4 * dg);
+                    for (int j = 0; j < 8; ++j) x[uu][j] = lds32(raw + C::RV + C::v_at(k0 + j, blk) + 4 * dg);
                     uint32_t sw[8];  // the keys' scale of the block
                     if constexpr (D == 128) {
-                        const uint4 a = lds128u(raw_v + C::RVS + 4 * k0), c = lds128u(raw_v + C::RVS + 4 * k0 + 16);
+                        const uint4 a = lds128u(raw + C::RVS + 4 * k0), c = lds128u(raw + C::RVS + 4 * k0 + 16);
                         const uint32_t y[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
 #pragma unroll
                         for (int j = 0; j < 8; ++j) sw[j] = (y[j] >> (8 * blk)) & 0xFFu;
                     } else {
-                        const uint4 a = lds128u(raw_v + C::RVS + 2 * k0);
+                        const uint4 a = lds128u(raw + C::RVS + 2 * k0);
                         const uint32_t y[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
                         for (int j = 0; j < 8; ++j) sw[j] = (y[j >> 1] >> (16 * (j & 1) + 8 * blk)) & 0xFFu;
@@ -487,7 +428,9 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
 #pragma unroll
                     for (int j = 0; j < 4; ++j) sc[uu][j] = scale_pair(sw[2 * j] | (sw[2 * j + 1] << 16), floor2, minus2);
                 }
-                if (live && it > 1) live = mbar_wait(v_empty, (uint32_t)(it - 2) & 1u, ab, err);
+                mbar_arrive(raw_empty(at_v.s));
+                if (it > 1) live = mbar_wait(v_empty, (uint32_t)(it - 2) & 1u, ab, err);
+                if (!live) break;
 #pragma unroll
                 for (int uu = 0; uu < UNITS; ++uu) {
                     const int u = D == 128 ? uu : w >> 1;
@@ -507,18 +450,106 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                     }
                 }
                 fence_proxy_async();
-                if (live) mbar_arrive(v_full);
+                mbar_arrive(v_full);
             }
-            raw_v = raw;
-            raw = next_raw(raw);
-            pages_v = pages;
-            vref_v = vref;
-            nan_v = nan;
+            at_v = at;
+            at.next(kTcRaw);
+            pages_v = bi.pages;
+            vref_v = bi.vref;
+            nan_v = bi.nan != 0;
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else {
         regs_down<40>();
-        if (warp == kTcMma && work && n > 0) {
+        if (work && (warp == kTcCopy || warp == kTcCopy + 1)) {
+            // ---- copies: this warp takes four of a block's eight groups of 16 keys ----
+            const int c0 = 4 * (warp - kTcCopy);
+            constexpr int PIECES = C::ROW / 16, STEPS = 16 * PIECES / 32;  // 16-byte pieces of a row; of a group per lane
+            const long long page_rows = (long long)p.c.heads * p.c.page, head_row = (long long)head * p.c.page;
+            int pg = -1, off = 0;  // lane j < 4: page and first row of group c0 + j of the next block, as loaded
+            auto lookup = [&](int blk) {
+                const int key = (first + blk) * 128 + 16 * (c0 + lane);
+                pg = -1;
+                if (lane < 4 && blk < n && key < s.len) {
+                    const int at = p.by_page(key);
+                    off = key - at * p.c.page;
+                    pg = __ldg(p.table + b * p.table_stride + at);
+                }
+            };
+            Ring at;
+            lookup(0);
+            for (int it = 0; it < n; ++it, at.next(kTcRaw)) {
+                if (it >= kTcRaw && !mbar_wait(raw_empty(at.s), at.phase ^ 1u, ab, err)) break;
+                __syncwarp();
+                const uint32_t raw = sb + C::AT_RAW + (uint32_t)at.s * C::RAW;
+                if (pg >= p.c.pages) pg = -1;
+                uint32_t bits = 0;
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
+                    const int x = __shfl_sync(0xFFFFFFFFu, pg, j), o = __shfl_sync(0xFFFFFFFFu, off, j), g = c0 + j;
+                    if (x < 0) continue;
+                    bits |= 1u << g;
+                    const long long row = x * page_rows + head_row + o;
+#pragma unroll
+                    for (int i = 0; i < STEPS; ++i) {
+                        const int e = 32 * i + lane, r = 16 * g + e / PIECES;
+                        copy16(raw + C::k_at(r, e % PIECES), p.c.kc + row * C::ROW + 16 * e);
+                        copy16(raw + C::RV + C::v_at(r, e % PIECES), p.c.vc + row * C::ROW + 16 * e);
+                    }
+                    if (lane < 2 * C::SROW) {  // scales: SROW pieces each of K and V
+                        const bool v = lane >= C::SROW;
+                        const int e = lane - (v ? C::SROW : 0);
+                        copy16(raw + (v ? C::RVS : C::RKS) + 16 * (C::SROW * g + e), (v ? p.c.vs : p.c.ks) + row * C::SROW + 16 * e);
+                    }
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(raw_full(at.s)) : "memory");
+                if (lane == 0) {
+                    there[it & 7][warp - kTcCopy] = bits;
+                    mbar_arrive(raw_full(at.s));
+                }
+                lookup(it + 1);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        } else if (work && warp == kTcScales) {
+            // ---- reference scales ----
+            int vref = -1000;
+            Ring at;
+            for (int it = 0; it < n; ++it, at.next(kTcRaw)) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(raw_full(at.s), at.phase, ab, err))) break;
+                const uint32_t raw = sb + C::AT_RAW + (uint32_t)at.s * C::RAW;
+                const int key0 = (first + it) * 128;
+                const uint32_t pages = there[it & 7][0] | there[it & 7][1];
+                const bool edge = pages != 0xFFu || key0 + 128 > s.len;
+                constexpr int PER = 16 / C::SROW;  // keys of the lane's 16 bytes
+                const int mine = min(lane, 128 / PER - 1);
+                bool nan = false;
+                int top[2];
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const uint4 y = lds128u(raw + (v ? C::RVS : C::RKS) + 16 * mine);
+                    uint32_t x[4] = {y.x, y.y, y.z, y.w};
+                    if (edge) {
+                        const int key = mine * PER;
+                        const bool in = (pages >> (key >> 4)) & 1u;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if constexpr (D == 128) {
+                                if (!in || key0 + key + i >= s.len) x[i] = 0;
+                            } else {
+                                if (!in || key0 + key + 2 * i >= s.len) x[i] = 0;
+                                else if (key0 + key + 2 * i + 1 >= s.len) x[i] &= 0xFFFFu;
+                            }
+                        }
+                    }
+                    top[v] = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)max_byte(x, nan));
+                }
+                nan = __any_sync(0xFFFFFFFFu, nan);
+                if (top[1] > vref + 13) vref = top[1] - 6;
+                if (lane == 0) {
+                    infos[it & 7] = {top[0] - 13, vref, pages, nan ? 1u : 0u};
+                    mbar_arrive(info_full(at.s));
+                }
+            }
+        } else if (warp == kTcMma && work && n > 0) {
             // ---- MMAs ----
             const bool one = elect_one();
             constexpr uint32_t id_s = idesc_f16(128, 128), id_o = idesc_f16(128, D);
