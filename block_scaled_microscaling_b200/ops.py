@@ -12,11 +12,13 @@
 
 As in mxq.py, the mxq_* functions take raw integers and return the status; the helpers allocate outputs with
 torch, refuse tensors that the C calls could not read or write safely, launch on the current stream (or `stream`)
-and raise MXQError on a non-zero status. The product's kernel bounds its waits: check=True synchronizes and raises
+and raise MXQError on a non-zero status. Plain calls go through the C++ module _ops (csrc/ops_torch.cpp), which does the
+same in a few microseconds and leaves every other case to the code here. The product's kernel bounds its waits: check=True synchronizes and raises
 if one ran out (else call check_device() before trusting the outputs).
 """
 import ctypes
 import math
+import os
 
 from . import mxq
 from .mxq import MXQError, _as2d, _check, _dt, _finish, _fits, _fmt, _on_gpu, _torch
@@ -60,6 +62,34 @@ def lib():
             fn.restype = res
         _ready = L
     return _ready
+
+
+_native_module = None
+
+
+def _native():
+    """The C++ module for plain calls."""
+    global _native_module
+    if _native_module is None:
+        if not os.path.exists(os.path.join(mxq.HERE, "_ops.so")):
+            raise RuntimeError("_ops.so is missing: build it with `python -m block_scaled_microscaling_b200.build`")
+        _torch()
+        from . import _ops
+        _native_module = _ops
+    return _native_module
+
+
+def _plain(call, *args):
+    """What the C++ module makes of a call: None where the case is not a plain one (other types among them) or a C entry
+    point refused it, so that the code here says why."""
+    try:
+        return call(*args)
+    except TypeError:
+        return None
+    except RuntimeError as e:
+        if not str(e).startswith("mxq_"):
+            raise
+        return None
 
 
 # ---- the C entry points, same names and arguments --------------------------------
@@ -254,6 +284,10 @@ def quantize_both(x, row_fmt=None, col_fmt=None, stream=None):
 def linear(x, w_codes, w_scales, fmt, out=None, stream=None, check=False):
     """x [..., k] (bf16/fp32, contiguous) rounded to `fmt`, times the weight w [n, k] held in `fmt` (codes
     [n, k/32*P] and tile-layout scales, as quantize_mma(w, fmt) returns them): [..., n] of x's dtype."""
+    if out is None and stream is None and not check:
+        y = _plain(_native().linear, x, w_codes, w_scales, mxq.FORMATS.get(fmt, -1))
+        if y is not None:
+            return y
     if not x.is_contiguous() or x.dim() == 0:
         raise ValueError("x must be contiguous, of at least one dimension")
     _on_gpu(x, "x")
@@ -452,6 +486,9 @@ def linear_ste(x, weight, fmt="mxfp8"):
     with Q8 rounding to MXFP8 (gradients pass straight through the rounding of the operands). Of x only its MXFP8
     codes along the tokens are kept for the backward pass: the operand of the weight's gradient as it stands, 33/64 of
     x's bf16 bytes. Any number of tokens."""
+    y = _plain(_native().linear_ste, x, weight, mxq.FORMATS.get(fmt, -1))
+    if y is not None:
+        return y
     _functions()
     _product_fmt(fmt)
     _on_gpu(x, "x")
@@ -468,6 +505,9 @@ def swiglu(gate, up=None):
     """silu(gate) * up, differentiable; gate and up are kept for the backward pass as MXFP8 (33/64 of their bf16
     bytes) and the gradients are those of the rounded values. With up=None, `gate` is [..., 2 cols]: gate, then up
     (the output of one projection), and so is its gradient. cols % 32 == 0; bf16 or fp32."""
+    y = _plain(_native().swiglu, gate, up)
+    if y is not None:
+        return y
     _functions()
     _on_gpu(gate, "gate")
     _dt(gate)
@@ -494,7 +534,13 @@ class KVCache:
     page_size, head_dim/32], both contiguous. Token slot s is row s % page_size of page s // page_size."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales):
+        self._native = _plain(_native().cache, k_codes, k_scales, v_codes, v_scales)
         shape = k_codes.shape
+        if self._native is not None:
+            self.pages, self.kv_heads, self.page_size, half = shape
+            self.head_dim = 2 * half
+            self._tensors = (k_codes, k_scales, v_codes, v_scales)
+            return
         if len(shape) != 4:
             raise ValueError("codes must be [pages, kv_heads, page_size, head_dim / 2]")
         self.pages, self.kv_heads, self.page_size, self.head_dim = *shape[:3], shape[3] * 2
@@ -505,7 +551,9 @@ class KVCache:
             if tuple(t.shape) != want[what[2:]]:
                 raise ValueError(f"{what} must be {want[what[2:]]}, got {tuple(t.shape)}")
             _fits(t, 0, what)
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self._tensors = (k_codes, k_scales, v_codes, v_scales)
+
+    k_codes, k_scales, v_codes, v_scales = (property(lambda self, i=i: self._tensors[i]) for i in range(4))
 
     @classmethod
     def empty(cls, pages, kv_heads, page_size, head_dim, device="cuda"):
@@ -545,6 +593,8 @@ def _tokens(t, cache, what):
 def kv_append(k, v, cache, slots, stream=None):
     """Round keys and values [tokens, kv_heads, head_dim] (bf16/fp32; the token stride is free) to MXFP4 and write
     token t to slot slots[t] (int64). Slots outside the cache are skipped; the others must differ."""
+    if stream is None and cache._native is not None and _plain(_native().kv_append, cache._native, k, v, slots):
+        return
     ks, vs = _tokens(k, cache, "k"), _tokens(v, cache, "v")
     if k.shape[0] != v.shape[0] or k.dtype != v.dtype:
         raise ValueError("k and v must have one shape and dtype")
@@ -556,6 +606,10 @@ def kv_append(k, v, cache, slots, stream=None):
 def kv_read(cache, slots, dtype=None, stream=None):
     """(k, v) [tokens, kv_heads, head_dim] held at slots (int64), exact in bf16 (default) or fp32; zeros for a slot
     outside the cache."""
+    if dtype is None and stream is None and cache._native is not None:
+        kv = _plain(_native().kv_read, cache._native, slots)
+        if kv is not None:
+            return kv
     torch = _torch()
     _ints(slots, torch.int64, "slots")
 
@@ -582,6 +636,10 @@ def kv_attention(q, cache, block_table, seq_lens, q_starts=None, max_q=None, sca
     max_keys     an upper bound of seq_lens, if known, for a better split of the work (longer sequences are cut)
     Returns out [rows, heads, head_dim]; with lse=True (out, log-sum-exp fp32 [rows, heads]). A query that sees no key
     gives 0 (and -inf), and so do rows of no sequence and queries beyond max_q, which a given `out` keeps."""
+    if out is None and not lse and stream is None and cache._native is not None:
+        o = _plain(_native().kv_attention, cache._native, q, block_table, seq_lens, q_starts, max_q, scale, window, max_keys)
+        if o is not None:
+            return o
     torch = _torch()
     _on_gpu(q, "q")
     if q.dim() != 3 or q.shape[2] != cache.head_dim or q.dtype != torch.bfloat16:
