@@ -3,8 +3,9 @@
 // ops.py documents the helpers, checks their arguments and calls the C entry points of libmxq through ctypes. For the
 // plain case (the library's types, matching shapes, contiguous where that is asked for, default options) the same
 // calls are made here, where allocating the outputs, the checks and the autograd node take a few microseconds
-// together; a kernel of a small batch takes no more. Anything else returns None (or a null handle), and ops.py goes
-// its own way, which raises the errors: no rule is relaxed here. Linked against libmxq.so beside it.
+// together; a kernel of a small batch takes no more. Anything else returns None (or False), and ops.py goes its own way,
+// which raises the errors: no rule is relaxed here. The two training functions exist here alone. Linked against
+// libmxq.so beside it.
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAStream.h>
 #include <pybind11/pybind11.h>
@@ -96,20 +97,19 @@ variable_list once(variable_list grads) {
 struct LinearSTE : torch::autograd::Function<LinearSTE> {
     static Tensor forward(AutogradContext* ctx, const Tensor& x, const Tensor& weight, int64_t fmt, bool need_dx, bool need_dw) {
         const int64_t k = weight.size(1), n = weight.size(0), m = x.numel() / k, m32 = (m + 31) / 32 * 32;
-        const Tensor x2 = x.reshape({m, k}).contiguous(), w = weight.contiguous();
         auto shape = x.sizes().vec();
         shape.back() = n;
-        Tensor y = at::empty(shape, x.options());
-        Tensor buf = scratch(operand_bytes((int)fmt, m, k) + operand_bytes((int)fmt, n, k), x), kept;
-        const Operand a = operand(buf, 0, (int)fmt, m, k), b = operand(buf, a.end, (int)fmt, n, k);
-        Operand col;
-        if (need_dw) {  // the checkpoint is the operand of the weight's gradient: x rounded along the tokens
-            kept = scratch(operand_bytes(MXQ_MXFP8_E4M3, k, m32), x);
-            col = operand(kept, 0, MXQ_MXFP8_E4M3, k, m32);
+        Tensor y = at::empty(shape, x.options()), kept;
+        // the checkpoint is the operand of the weight's gradient: x rounded along the tokens
+        if (need_dw) kept = scratch(operand_bytes(MXQ_MXFP8_E4M3, k, m32), x);
+        if (m > 0) {
+            const Tensor x2 = x.reshape({m, k}).contiguous(), w = weight.contiguous();
+            Tensor buf = scratch(operand_bytes((int)fmt, m, k) + operand_bytes((int)fmt, n, k), x);
+            const Operand a = operand(buf, 0, (int)fmt, m, k), b = operand(buf, a.end, (int)fmt, n, k);
+            quantize(x2, a, (int)fmt, need_dw ? operand(kept, 0, MXQ_MXFP8_E4M3, k, m32) : Operand(), MXQ_MXFP8_E4M3);
+            quantize(w, b, (int)fmt, Operand(), MXQ_MXFP8_E4M3);
+            product(a, b, (int)fmt, m, n, k, y);
         }
-        quantize(x2, a, (int)fmt, col, MXQ_MXFP8_E4M3);
-        quantize(w, b, (int)fmt, Operand(), MXQ_MXFP8_E4M3);
-        product(a, b, (int)fmt, m, n, k, y);
         ctx->save_for_backward({need_dx ? weight : Tensor(), kept});
         ctx->saved_data["x"] = x.sizes().vec();
         ctx->saved_data["n"] = n;
@@ -124,9 +124,14 @@ struct LinearSTE : torch::autograd::Function<LinearSTE> {
         Tensor dx, dw;
         {
             at::NoGradGuard no_grad;
-            const Tensor g = grads[0].reshape({-1, n}).contiguous();
-            const int64_t m = g.size(0), m32 = (m + 31) / 32 * 32;
+            const int64_t m = grads[0].numel() / n, m32 = (m + 31) / 32 * 32;
+            const Tensor g = grads[0].reshape({m, n}).contiguous();
             constexpr int f = MXQ_MXFP8_E4M3;
+            if (m == 0) {  // no tokens
+                if (weight.defined()) dx = at::empty(shape, g.options().dtype((at::ScalarType)types[0]));
+                if (kept.defined()) dw = at::zeros({n, k}, g.options().dtype((at::ScalarType)types[1]));
+                return {dx, dw, Tensor(), Tensor(), Tensor()};
+            }
             int64_t need = weight.defined() ? operand_bytes(f, m, n) + operand_bytes(f, k, n) : 0;
             if (kept.defined()) need += operand_bytes(f, n, m32);
             Tensor buf = scratch(need, g);
@@ -153,8 +158,9 @@ struct LinearSTE : torch::autograd::Function<LinearSTE> {
 };
 
 std::optional<Tensor> linear_ste(const Tensor& x, const Tensor& weight, int fmt) {
-    if (!product_format(fmt) || !values(x) || !values(weight) || x.dim() == 0 || weight.dim() != 2 || x.numel() == 0 ||
-        x.size(-1) != weight.size(1) || weight.size(0) <= 0 || weight.size(0) % 32 != 0 || weight.size(1) % 32 != 0 ||
+    if (!product_format(fmt) || !values(x) || !values(weight) || x.dim() == 0 || weight.dim() != 2 ||
+        x.size(-1) != weight.size(1) || weight.size(0) <= 0 || weight.size(0) % 32 != 0 || weight.size(1) <= 0 ||
+        weight.size(1) % 32 != 0 ||
         x.device() != weight.device())
         return std::nullopt;
     const bool grad = at::GradMode::is_enabled();
@@ -175,22 +181,45 @@ struct Checkpoint {
     }
 };
 
+// values between rows if the leading dimensions of t are one dimension of rows, whose values are contiguous and whose
+// start and stride are 16-byte aligned; else 0
+int64_t row_stride(const Tensor& t) {
+    if (t.stride(-1) != 1) return 0;
+    int64_t ld = 0, n = 1;
+    for (int64_t i = t.dim() - 2; i >= 0; --i) {
+        if (t.size(i) == 1) continue;
+        if (ld == 0) ld = t.stride(i);
+        else if (t.stride(i) != ld * n) return 0;
+        n *= t.size(i);
+    }
+    if (ld == 0) ld = t.size(-1);
+    const bool aligned = ld * t.element_size() % 16 == 0 && reinterpret_cast<uintptr_t>(t.const_data_ptr()) % 16 == 0;
+    return ld >= t.size(-1) && aligned ? ld : 0;
+}
+
 struct SwiGLU : torch::autograd::Function<SwiGLU> {
-    // gate and up, contiguous, of one shape; or gate alone with up's columns behind its own
-    static Tensor forward(AutogradContext* ctx, const Tensor& gate, const std::optional<Tensor>& up, bool keep) {
-        const bool packed = !up.has_value();
+    // gate and up, of one shape; or gate alone with up's columns behind its own
+    static Tensor forward(AutogradContext* ctx, const Tensor& gate_in, const std::optional<Tensor>& up_in, bool keep) {
+        const bool packed = !up_in.has_value();
+        Tensor gate = gate_in, up = packed ? Tensor() : *up_in;
+        int64_t ld = packed ? 0 : row_stride(gate);
+        if (ld == 0 || row_stride(up) != ld) {
+            gate = gate.contiguous();
+            if (!packed) up = up.contiguous();
+            ld = gate.size(-1);
+        }
         const int64_t cols = gate.size(-1) / (packed ? 2 : 1), rows = gate.numel() / gate.size(-1), n = rows * cols;
         auto shape = gate.sizes().vec();
         shape.back() = cols;
-        Tensor out = at::empty(shape, gate.options()), kept;
+        Tensor out = at::empty(shape, gate.options().memory_format(at::MemoryFormat::Contiguous)), kept;
         Checkpoint c;
         if (keep) {
             kept = scratch(n / 32 * 66, gate);
             c = Checkpoint(kept, n);
         }
         const char* const pg = static_cast<const char*>(gate.const_data_ptr());
-        ok(mxq_swiglu_forward(pg, packed ? pg + cols * gate.element_size() : up->const_data_ptr(), dtype_of(gate), rows, cols,
-                              gate.size(-1), out.mutable_data_ptr(), c.gc, c.gs, c.uc, c.us, stream_of(gate)),
+        ok(mxq_swiglu_forward(pg, packed ? pg + cols * gate.element_size() : up.const_data_ptr(), dtype_of(gate), rows, cols, ld,
+                              out.mutable_data_ptr(), c.gc, c.gs, c.uc, c.us, stream_of(gate)),
            "mxq_swiglu_forward");
         ctx->save_for_backward({kept});
         ctx->saved_data["packed"] = packed;
@@ -228,9 +257,8 @@ struct SwiGLU : torch::autograd::Function<SwiGLU> {
 };
 
 std::optional<Tensor> swiglu(const Tensor& gate, const std::optional<Tensor>& up) {
-    if (!values(gate) || gate.dim() == 0 || gate.numel() == 0 || !gate.is_contiguous() || gate.size(-1) % (up ? 32 : 64) != 0)
-        return std::nullopt;
-    if (up && (!up->is_contiguous() || up->sizes() != gate.sizes() || up->scalar_type() != gate.scalar_type() ||
+    if (!values(gate) || gate.dim() == 0 || gate.size(-1) <= 0 || gate.size(-1) % (up ? 32 : 64) != 0) return std::nullopt;
+    if (up && (up->sizes() != gate.sizes() || up->scalar_type() != gate.scalar_type() ||
                up->device() != gate.device()))
         return std::nullopt;
     const bool keep = at::GradMode::is_enabled() && (gate.requires_grad() || (up && up->requires_grad()));

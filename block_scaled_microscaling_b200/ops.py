@@ -12,8 +12,9 @@
 
 As in mxq.py, the mxq_* functions take raw integers and return the status; the helpers allocate outputs with
 torch, refuse tensors that the C calls could not read or write safely, launch on the current stream (or `stream`)
-and raise MXQError on a non-zero status. Plain calls go through the C++ module _ops (csrc/ops_torch.cpp), which does the
-same in a few microseconds and leaves every other case to the code here. The product's kernel bounds its waits: check=True synchronizes and raises
+and raise MXQError on a non-zero status. linear_ste and swiglu with their gradients, and plain calls of the others, go
+through the C++ module _ops (csrc/ops_torch.cpp), which does the same in a few microseconds and leaves every other case
+and the errors to the code here. The product's kernel bounds its waits: check=True synchronizes and raises
 if one ran out (else call check_device() before trusting the outputs).
 """
 import ctypes
@@ -173,38 +174,6 @@ def _bytes(n, like):
     return torch.empty(n, dtype=torch.uint8, device=like.device)
 
 
-class _Operand:
-    """Pointers of the codes and tile-layout scales of a [rows, cols] operand that lie one after the other from `at` on
-    (payloads are multiples of 16 bytes and scale tiles of 512, so all are aligned as the product wants them)."""
-    __slots__ = ("codes", "scales", "end")
-
-    def __init__(self, at, fmt, rows, cols):
-        self.codes = at
-        self.scales = at + rows * (cols // 32) * 4 * mxq.ELEM_BITS[fmt]
-        self.end = self.scales + _scale_bytes(rows, cols)
-
-
-def _scale_bytes(rows, cols):
-    return -(-rows // 128) * 128 * (-(-cols // 128) * 4)
-
-
-def _operand_bytes(fmt, rows, cols):
-    return rows * (cols // 32) * 4 * mxq.ELEM_BITS[fmt] + _scale_bytes(rows, cols)
-
-
-def _both(x, row, row_fmt, col, col_fmt):
-    """Quantize the contiguous 2-D x into the operands `row` and / or `col` (None: left out)."""
-    _check(mxq_quantize_both(mxq.FORMATS[row_fmt], mxq.FORMATS[col_fmt], x.data_ptr(), _dt(x), x.shape[0], x.shape[1],
-                             row and row.codes, row and row.scales, col and col.codes, col and col.scales, _raw_stream(x)),
-           "mxq_quantize_both")
-
-
-def _product(a, b, fmt, m, n, k, out):
-    _check(mxq_matmul(mxq.FORMATS[fmt], a.codes, a.scales, b.codes, b.scales, m, n, k, out.data_ptr(), _dt(out),
-                      _raw_stream(out)), "mxq_matmul")
-    return out
-
-
 def matmul(a_codes, a_scales, b_codes, b_scales, fmt, out=None, dtype=None, stream=None, check=False):
     """out[m, n] = a b^T of the microscaled operands a [m, k], b [n, k]: codes [rows, k/32*P] and scales in the tile
     layout, as quantize_mma or quantize_both return them; `dtype` bf16 (default) or fp32."""
@@ -323,162 +292,6 @@ def linear(x, w_codes, w_scales, fmt, out=None, stream=None, check=False):
 
 # ---- training: straight-through gradients from 8-bit checkpoints ----------------------
 
-def _flat(t):
-    t = t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
-    return t if t.is_contiguous() else t.contiguous()
-
-
-def _checkpoint(buf, rows, cols):
-    """Pointers of gate's codes and scales and up's in one allocation of 66 bytes per block (codes first: aligned)."""
-    p, n = buf.data_ptr(), rows * cols
-    return p, p + 2 * n, p + n, p + 2 * n + n // 32
-
-
-def _functions():
-    """The autograd functions (built on first use: torch is imported late, as in mxq.py)."""
-    global LinearSTE, SwiGLU
-    if LinearSTE is not None:
-        return
-    torch = _torch()
-    from torch.autograd.function import once_differentiable
-
-    def first_order(backward, ctx, grad):
-        """The gradients are not differentiable: under create_graph a second derivative raises."""
-        if torch.is_grad_enabled():
-            return once_differentiable(backward)(ctx, grad)
-        return backward(ctx, grad)
-
-    def linear_backward(ctx, grad):
-        weight, kept = ctx.saved_tensors
-        (m, n, k), (xt, wt) = ctx.sizes, ctx.types
-        dx = dw = None
-        if m == 0:  # no tokens
-            dx = None if weight is None else torch.empty(ctx.shape, dtype=xt, device=grad.device)
-            dw = None if kept is None else torch.zeros((n, k), dtype=wt, device=grad.device)
-            return dx, dw, None
-        g, m32 = _flat(grad), -(-m // 32) * 32
-        need = 0 if weight is None else _operand_bytes("mxfp8", m, n) + _operand_bytes("mxfp8", k, n)
-        need += 0 if kept is None else _operand_bytes("mxfp8", n, m32)
-        scratch = _bytes(need, g)
-        at, row, col = scratch.data_ptr(), None, None
-        if weight is not None:
-            row = _Operand(at, "mxfp8", m, n)
-            w = _Operand(row.end, "mxfp8", k, n)
-            at = w.end
-        if kept is not None:
-            col = _Operand(at, "mxfp8", n, m32)
-        if row or col:
-            _both(g, row, "mxfp8", col, "mxfp8")
-        if row:
-            _both(weight if weight.is_contiguous() else weight.contiguous(), None, "mxfp8", w, "mxfp8")
-            dx = _product(row, w, "mxfp8", m, k, n, torch.empty(ctx.shape, dtype=xt, device=g.device))
-        if col:
-            x = _Operand(kept.data_ptr(), "mxfp8", k, m32)
-            dw = _product(col, x, "mxfp8", n, k, m32, torch.empty((n, k), dtype=wt, device=g.device))
-        return dx, dw, None
-
-    class Linear(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, x, weight, fmt):
-            x2 = _flat(x)
-            (m, k), n = x2.shape, weight.shape[0]
-            need_dx, need_dw = ctx.needs_input_grad[:2]
-            y = torch.empty((*x.shape[:-1], n), dtype=x.dtype, device=x.device)
-            kept = None
-            if m:
-                m32 = -(-m // 32) * 32
-                scratch = _bytes(_operand_bytes(fmt, m, k) + _operand_bytes(fmt, n, k), x2)
-                a = _Operand(scratch.data_ptr(), fmt, m, k)
-                b, col = _Operand(a.end, fmt, n, k), None
-                if need_dw:  # the checkpoint is the operand of the weight's gradient: x rounded along the tokens
-                    kept = _bytes(_operand_bytes("mxfp8", k, m32), x2)
-                    col = _Operand(kept.data_ptr(), "mxfp8", k, m32)
-                _both(x2, a, fmt, col, "mxfp8")
-                _both(weight if weight.is_contiguous() else weight.contiguous(), b, fmt, None, "mxfp8")
-                _product(a, b, fmt, m, n, k, y)
-            elif need_dw:
-                kept = _bytes(0, x2)
-            ctx.save_for_backward(weight if need_dx else None, kept)
-            ctx.shape, ctx.sizes, ctx.types = x.shape, (m, n, k), (x.dtype, weight.dtype)
-            return y
-
-        @staticmethod
-        def backward(ctx, grad):
-            return first_order(linear_backward, ctx, grad)
-
-    def swiglu_backward(ctx, grad):
-        kept, = ctx.saved_tensors
-        g, rows, cols, size = grad.contiguous(), ctx.rows, ctx.cols, grad.element_size()
-        if ctx.packed:
-            dgate, dup, ld = torch.empty((*g.shape[:-1], 2 * cols), dtype=g.dtype, device=g.device), None, 2 * cols
-            pg, pu = dgate.data_ptr(), dgate.data_ptr() + cols * size
-        else:
-            dgate, dup, ld = torch.empty_like(g), torch.empty_like(g), cols
-            pg, pu = dgate.data_ptr(), dup.data_ptr()
-        gc, gs, uc, us = _checkpoint(kept, rows, cols)
-        _check(mxq_swiglu_backward(g.data_ptr(), _dt(g), gc, gs, uc, us, rows, cols, pg, pu, ld, _raw_stream(g)),
-               "mxq_swiglu_backward")
-        return dgate, dup
-
-    class Swiglu(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, gate, up):
-            packed = up is None
-            if packed:
-                cols = gate.shape[-1] // 2
-                x, ld = gate.contiguous(), 2 * cols
-                pg, pu = x.data_ptr(), x.data_ptr() + cols * x.element_size()
-                rows = x.numel() // (2 * cols)
-                out = torch.empty((*gate.shape[:-1], cols), dtype=gate.dtype, device=gate.device)
-            else:
-                cols = gate.shape[-1]
-                ld = _row_stride(gate)
-                if ld is None or _row_stride(up) != ld:
-                    gate, up, ld = gate.contiguous(), up.contiguous(), cols
-                pg, pu = gate.data_ptr(), up.data_ptr()
-                rows = gate.numel() // cols
-                out = torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
-            kept, parts = None, (None,) * 4
-            if ctx.needs_input_grad[0] or ctx.needs_input_grad[1]:
-                kept = _bytes(rows * cols // 32 * 66, gate)
-                parts = _checkpoint(kept, rows, cols)
-            _check(mxq_swiglu_forward(pg, pu, _dt(gate), rows, cols, ld, out.data_ptr(), *parts, _raw_stream(gate)),
-                   "mxq_swiglu_forward")
-            ctx.save_for_backward(kept)
-            ctx.packed, ctx.rows, ctx.cols = packed, rows, cols
-            return out
-
-        @staticmethod
-        def backward(ctx, grad):
-            return first_order(swiglu_backward, ctx, grad)
-
-    LinearSTE, SwiGLU = Linear, Swiglu
-
-
-LinearSTE = SwiGLU = None
-
-
-def _row_stride(t):
-    """Values between rows if the leading dimensions of t are one dimension of rows, whose values are contiguous and
-    whose start and stride are 16-byte aligned; else None."""
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        return None
-    ld = None
-    for i in range(t.dim() - 2, -1, -1):
-        if t.shape[i] == 1:
-            continue
-        if ld is None:
-            ld, n = t.stride(i), t.shape[i]
-        elif t.stride(i) != ld * n:
-            return None
-        else:
-            n *= t.shape[i]
-    ld = t.shape[-1] if ld is None else ld
-    if ld < t.shape[-1] or ld * t.element_size() % 16 or t.data_ptr() % 16:
-        return None
-    return ld
-
-
 def linear_ste(x, weight, fmt="mxfp8"):
     """Differentiable linear layer in microscaled products: x [..., k], weight [n, k], k and n multiples of 32.
       forward   y = Q(x) Q(weight)^T, Q rounding to `fmt` along k
@@ -489,7 +302,6 @@ def linear_ste(x, weight, fmt="mxfp8"):
     y = _plain(_native().linear_ste, x, weight, mxq.FORMATS.get(fmt, -1))
     if y is not None:
         return y
-    _functions()
     _product_fmt(fmt)
     _on_gpu(x, "x")
     _on_gpu(weight, "weight")
@@ -498,7 +310,7 @@ def linear_ste(x, weight, fmt="mxfp8"):
         raise ValueError(f"x {tuple(x.shape)} and weight {tuple(weight.shape)} do not fit")
     if weight.shape[1] == 0 or weight.shape[1] % 32 or weight.shape[0] == 0 or weight.shape[0] % 32:
         raise MXQError(2, f"weight {tuple(weight.shape)}: both sizes must be multiples of 32")
-    return LinearSTE.apply(x, weight, fmt)
+    raise MXQError(1, f"linear_ste of tensors on {x.device} and {weight.device}")
 
 
 def swiglu(gate, up=None):
@@ -508,7 +320,6 @@ def swiglu(gate, up=None):
     y = _plain(_native().swiglu, gate, up)
     if y is not None:
         return y
-    _functions()
     _on_gpu(gate, "gate")
     _dt(gate)
     if gate.dim() == 0:
@@ -524,7 +335,7 @@ def swiglu(gate, up=None):
             raise ValueError("gate and up must have one shape, dtype and device")
     if cols == 0 or cols % 32:
         raise MXQError(2, f"cols={cols}")
-    return SwiGLU.apply(gate, up)
+    raise MXQError(1, f"swiglu of tensors on {gate.device}")
 
 
 # ---- the paged MXFP4 key/value cache ---------------------------------------------------

@@ -172,11 +172,11 @@ def test_quantize_both_errors():
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("shape,n", [((64,), 40), ((1, 1, 96), 33), ((3, 5, 256), 128), ((140, 320), 70)])
 def test_linear(shape, n, fmt, dtype):
-    x, w = values(3, shape[0] if len(shape) > 1 else 1, 32 * 9)[0, :1], None
     k = shape[-1]
     x = values(sum(shape), max(1, torch.Size(shape[:-1]).numel()), k, dtype).view(shape)
     w = values(n, n, k)
     y = ops.linear(x, *mxq.quantize_mma(w, fmt), fmt, check=True)
+    assert torch.equal(ops.linear(x, *mxq.quantize_mma(w, fmt), fmt), y)  # the plain call's way
     assert y.shape == (*shape[:-1], n) and y.dtype == dtype
     a, b = decoded(x.view(-1, k), fmt), decoded(w, fmt)
     close(y.view(-1, n), a @ b.T, a.abs() @ b.abs().T, k)

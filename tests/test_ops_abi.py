@@ -83,8 +83,6 @@ def test_product_statuses_before_any_cuda_call():
     assert ops.mxq_linear_workspace_bytes(FP4, 5, 64) == 5 * 32 + mxq.mxq_mma_scales_bytes(5, 64)
     assert ops.mxq_linear_workspace_bytes(FP8, 130, 96) == 130 * 96 + mxq.mxq_mma_scales_bytes(130, 96)
     assert [ops.mxq_linear_workspace_bytes(f, 5, k) for f, k in ((1, 64), (9, 64), (FP4, 40))] == [0, 0, 0]
-    for rows, cols in ((1, 32), (5, 64), (128, 128), (130, 96), (257, 4128)):
-        assert ops._operand_bytes("mxfp4", rows, cols) == ops.mxq_linear_workspace_bytes(FP4, rows, cols)
     qb = ops.mxq_quantize_both
     assert qb(FP4, FP8, None, BF16, 5, 48, None, None, None, None, None) == 2
     assert qb(FP4, FP8, None, BF16, 5, 64, None, None, None, None, None) == 1   # neither direction
