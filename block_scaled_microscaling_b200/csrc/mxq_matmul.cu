@@ -24,6 +24,7 @@
 #include <atomic>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 #include <cuda.h>  // CUtensorMap and its enums (types only: the encoder is fetched through the runtime)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -41,6 +42,8 @@ constexpr int kMmThreads = 320;  // producer warp, MMA warp, eight epilogue warp
 constexpr int kMmRows = 128;     // rows of X per tile
 constexpr int kMmSplitMax = 8;   // portable cluster size
 
+// output of rows that are not aligned: 32 rows of two 32-byte pieces for each epilogue warp, 17 words apart
+constexpr int kMmPitch = 17, kMmStaging = 8 * 32 * kMmPitch * 4;
 // per format: values of k in a staged 128-byte row, values per MMA, 512-byte scale tiles per 128 rows and stage
 template <int F> struct MmFmt;
 template <> struct MmFmt<F_E2M1> { static constexpr int VALS = 256, KI = 64, TS = 2; };
@@ -54,19 +57,23 @@ template <int F> struct MmCfg {
     static constexpr int MAX_STAGES = 8;
     __host__ __device__ static constexpr int stage_bytes(int bn) { return A_BYTES + bn * 128 + (SF_BYTES + 1023) / 1024 * 1024; }
     // as many stages as fit the SM, or half of it
-    static constexpr int stages(int bn, bool two) {
-        const int n = ((two ? 112 : 224) * 1024 - 1024) / stage_bytes(bn);
+    static constexpr int stages(int bn, bool two, bool staged) {
+        const int n = ((two ? 112 : 224) * 1024 - 1024 - (staged ? kMmStaging : 0)) / stage_bytes(bn);
         return n < MAX_STAGES ? n : MAX_STAGES;
     }
-    static int smem(int bn, int stages) {
-        const int ring = stages * stage_bytes(bn), part = bn * kMmRows * 4;  // the partial tile takes the stages' place
-        return (ring > part ? ring : part) + 1024;                           // + alignment slack
+    // the ring; a partial tile takes its place
+    __host__ __device__ static constexpr int ring_bytes(int bn, int stages) {
+        const int ring = stages * stage_bytes(bn), part = bn * kMmRows * 4;
+        return ring > part ? ring : part;
+    }
+    static int smem(int bn, int stages, bool staged) {
+        return ring_bytes(bn, stages) + (staged ? kMmStaging : 0) + 1024;  // + alignment slack
     }
     // tensor memory: 128 accumulator columns, then two buffers of scale columns (a stage's copies never write the
     // buffer that the stage before reads)
     static constexpr int SF_COLS = TS * 4 * 2;
     static constexpr int ALLOC = 256;
-    static_assert(128 + 2 * SF_COLS <= ALLOC && stages(128, true) >= 3, "tensor memory of two CTAs, a ring of three stages");
+    static_assert(128 + 2 * SF_COLS <= ALLOC && stages(128, true, false) >= 3, "tensor memory of two CTAs, a ring of three stages");
 };
 
 // position in a ring of n stages: stage and the parity of its current use (counters, since one thread's divisions
@@ -111,11 +118,15 @@ template <typename T> __device__ __forceinline__ T round_to(float v);
 template <> __device__ __forceinline__ float round_to<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// rows of out begin on 32 bytes
+template <typename T> __host__ __device__ __forceinline__ bool rows_aligned(const void* out, long long ld) {
+    return ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(ld * (long long)sizeof(T))) & 31) == 0;
+}
 // 32 bytes (as words) of one output row from column c on, `left` columns of the row remaining
 template <typename T>
-__device__ __forceinline__ void store_run(T* p, const uint32_t* w, int left, bool a32) {
+__device__ __forceinline__ void store_run(T* p, const uint32_t* w, int left) {
     constexpr int N = 32 / (int)sizeof(T);
-    if (a32 && left >= N) {
+    if (left >= N) {
         st_v8(p, w);
     } else {
 #pragma unroll
@@ -136,10 +147,58 @@ __device__ __forceinline__ void pack_run(const float* v, uint32_t* w) {
     }
 }
 
-// N accumulator columns of the warp's 32 rows (tensor-memory address `mine`) to row x of out, columns y0 ..; calls
+// Rows that do not start on 32 bytes (row lengths that are not a multiple of 16 bf16 or 8 fp32 values): the warp's 32 rows
+// go through shared memory, 32 bytes at a time, and two lanes write a row from one whole 32-byte sector of the output to
+// the next, wherever in the row it starts; the ring of two pieces holds what such a sector can reach. With one lane per
+// row, value by value, 16384 x 9725 x 2560 (MXFP4) took 1615 us, with words of pieces that straddle sectors 510, with
+// whole sectors word by word 354, and so 227 (n = 9720 180, n = 9728, stored from registers, 164).
+template <typename T, int N>
+__device__ __forceinline__ void store_staged(const uint32_t* w, uint32_t* stage, T* out, long long ld, int x0, int rx, int y0, int ry) {
+    const int lane = threadIdx.x & 31;
+    constexpr int P = 32 / (int)sizeof(T), H = P / 2;  // values in a piece, in a lane's half of a sector
+    const int lim = ry - y0 < N ? ry - y0 : N;
+    using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+#pragma unroll
+    for (int j = 0; j <= N / P; ++j) {
+        if ((j - 1) * P >= lim) break;  // the same for the warp: no row's window j holds a value
+        if (j < N / P)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) stage[lane * kMmPitch + (j & 1) * 8 + i] = w[j * 8 + i];
+        __syncwarp();
+#pragma unroll
+        for (int r = lane >> 1; r < 32; r += 16) {
+            if (x0 + r >= rx) continue;
+            Bits* const row = reinterpret_cast<Bits*>(out + (long long)(x0 + r) * ld + y0);
+            const int skew = (int)(reinterpret_cast<uintptr_t>(row) / sizeof(T)) & (P - 1);
+            const int c = j * P - skew + H * (lane & 1);  // the lane's first value; all lie in pieces j - 1 and j
+            const uint32_t* const from = stage + r * kMmPitch;
+            uint32_t v[5];
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = from[(c + i) & 15];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 5; ++i) v[i] = from[((c >> 1) + i) & 15];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(v[i], v[i + 1], 16 * (c & 1));
+            }
+            if (c >= 0 && c + H <= lim) {
+                *reinterpret_cast<uint4*>(row + c) = make_uint4(v[0], v[1], v[2], v[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+                    if (c + i >= 0 && c + i < lim) row[c + i] = (Bits)(sizeof(T) == 4 ? v[i & 3] : v[i >> 1] >> (16 * (i & 1)));
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// N accumulator columns of the warp's 32 rows (tensor-memory address `mine`) to rows x0 .. of out, columns y0 ..; calls
 // `release` once all of them are in registers (bf16: rounded), before the first store
 template <typename T, int N, typename R>
-__device__ __forceinline__ void store_rows(uint32_t mine, T* out, long long ld, int x, int rx, int y0, int ry, bool a32, R release) {
+__device__ __forceinline__ void store_rows(uint32_t mine, uint32_t* stage, T* out, long long ld, int x0, int rx, int y0, int ry,
+                                           bool a32, R release) {
     constexpr int PER = 32 / (int)sizeof(T);  // columns in 32 bytes
     uint32_t w[N * (int)sizeof(T) / 4];
 #pragma unroll
@@ -156,17 +215,23 @@ __device__ __forceinline__ void store_rows(uint32_t mine, T* out, long long ld, 
     }
     if constexpr (sizeof(T) == 4) tmem_wait_ld();
     release();
+    if (!a32) {
+        store_staged<T, N>(w, stage, out, ld, x0, rx, y0, ry);
+        return;
+    }
+    const int x = x0 + (threadIdx.x & 31);
     T* const row = out + (long long)x * ld + y0;
     if (x < rx)
 #pragma unroll
         for (int c = 0; c < N; c += PER)
-            if (y0 + c < ry) store_run<T>(row + c, w + c / PER * 8, ry - y0 - c, a32);
+            if (y0 + c < ry) store_run<T>(row + c, w + c / PER * 8, ry - y0 - c);
 }
 
 // the partial tiles [bn][128] of S CTAs, at `part` in each, added in rank order: this CTA's share of the columns to
 // out (256 threads: row e % 128, columns in two halves)
 template <int S, bool SWAP, typename T>
-__device__ __forceinline__ void add_parts(uint32_t part, int e, int rank, int bn, int x, int y0, const MmArgs& p, T* out, bool a32) {
+__device__ __forceinline__ void add_parts(uint32_t part, int e, int rank, int bn, int x, int y0, const MmArgs& p, T* out, uint32_t* stage,
+                                          bool a32) {
     constexpr int RUN = SWAP ? 2 : 32 / (int)sizeof(T);  // columns at a time
     const int r = e & 127, per = bn / S;                 // bn is a multiple of 16, S at most 8
     for (int c = rank * per + (e >> 7) * RUN; c < (rank + 1) * per && y0 + c < p.ry; c += 2 * RUN) {
@@ -181,15 +246,16 @@ __device__ __forceinline__ void add_parts(uint32_t part, int e, int rank, int bn
 #pragma unroll
             for (int q = 1; q < S; ++q) sum[i] += v[i][q];
         }
-        if (x + r >= p.rx) continue;
         if constexpr (SWAP) {
+            if (x + r >= p.rx) continue;
 #pragma unroll
             for (int i = 0; i < RUN; ++i)
                 if (y0 + c + i < p.ry) out[(long long)(y0 + c + i) * p.ld + x + r] = round_to<T>(sum[i]);
         } else {
             uint32_t w[8];
             pack_run<T>(sum, w);
-            store_run<T>(out + (long long)(x + r) * p.ld + y0 + c, w, p.ry - y0 - c, a32);
+            if (!a32) store_staged<T, RUN>(w, stage, out, p.ld, x + (r & ~31), p.rx, y0 + c, p.ry);
+            else if (x + r < p.rx) store_run<T>(out + (long long)(x + r) * p.ld + y0 + c, w, p.ry - y0 - c);
         }
     }
 }
@@ -209,6 +275,10 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     __shared__ int abort_flag;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const uint32_t s0 = smem_u32(stages);
+    T* const out = static_cast<T*>(p.out);
+    const bool a32 = rows_aligned<T>(out, p.ld);
+    // an epilogue warp's staging; only there if !SWAP && !a32
+    uint32_t* const stage = reinterpret_cast<uint32_t*>(stages + C::ring_bytes(bn, ST)) + (warp - 2) * 32 * kMmPitch;
     auto full = [&](int s) { return smem_u32(&bars[s]); };
     auto empty = [&](int s) { return smem_u32(&bars[MS + s]); };
     const uint32_t acc_full = smem_u32(&bars[2 * MS]), acc_empty = smem_u32(&bars[2 * MS + 1]),
@@ -316,8 +386,6 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     } else {
         const int quad = warp & 3, half = (warp - 2) >> 2;  // the warp's lanes of tensor memory, its part of the columns
         const uint32_t mine = acc + ((uint32_t)(quad * 32) << 16);
-        T* const out = static_cast<T*>(p.out);
-        const bool a32 = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.ld * (long long)sizeof(T))) & 31) == 0;
         int it = 0;
         for (int tile = tile0; tile < p.tiles; tile += tile_step, ++it) {
             // lane 0 waits for the warp (bounded); its verdict is the warp's
@@ -358,7 +426,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
                 }
                 release();
             } else {
-                store_rows<T, 64>(mine + half * 64, out, p.ld, x, p.rx, y0 + half * 64, p.ry, a32, release);
+                store_rows<T, 64>(mine + half * 64, stage, out, p.ld, x - lane, p.rx, y0 + half * 64, p.ry, a32, release);
             }
         }
     }
@@ -367,11 +435,9 @@ __global__ void __launch_bounds__(kMmThreads, 2)
         cluster_sync();
         if (t >= 64) {
             const int e = t - 64, x = tile0 % p.xtiles * kMmRows, y0 = tile0 / p.xtiles * bn;
-            T* const out = static_cast<T*>(p.out);
-            const bool a32 = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.ld * (long long)sizeof(T))) & 31) == 0;
-            if (p.split == 2) add_parts<2, SWAP, T>(s0, e, rank, bn, x, y0, p, out, a32);
-            else if (p.split == 4) add_parts<4, SWAP, T>(s0, e, rank, bn, x, y0, p, out, a32);
-            else add_parts<8, SWAP, T>(s0, e, rank, bn, x, y0, p, out, a32);
+            if (p.split == 2) add_parts<2, SWAP, T>(s0, e, rank, bn, x, y0, p, out, stage, a32);
+            else if (p.split == 4) add_parts<4, SWAP, T>(s0, e, rank, bn, x, y0, p, out, stage, a32);
+            else add_parts<8, SWAP, T>(s0, e, rank, bn, x, y0, p, out, stage, a32);
         }
         __syncwarp();
         cluster_sync();  // peers have read this CTA's partial tile
@@ -401,10 +467,11 @@ template <int F> struct PairCfg {
     static constexpr int HALF = 128 * 128;  // bytes of 128 staged rows
     static constexpr int SFA = 2 * HALF, SFB = SFA + TS * 512, BYTES = SFB + 2 * TS * 512;
     static constexpr int STAGE = (BYTES + 1023) / 1024 * 1024;
-    static constexpr int STAGES = 6;
-    static constexpr int SMEM = STAGES * STAGE + 1024;
+    static constexpr int MAX_STAGES = 6;
+    static constexpr int stages(bool staged) { return MAX_STAGES - (staged && MAX_STAGES * STAGE + kMmStaging > 226 * 1024 - 512); }
+    static constexpr int smem(bool staged) { return stages(staged) * STAGE + (staged ? kMmStaging : 0) + 1024; }
     static constexpr int SF_COLS = TS * 4 * 3;  // a's scales of the CTA's 128 rows, b's of 256
-    static_assert(SMEM <= 227 * 1024 && 256 + 2 * SF_COLS <= 512, "shared and tensor memory");
+    static_assert(smem(false) <= 227 * 1024 - 512 && smem(true) <= 227 * 1024 - 512 && 256 + 2 * SF_COLS <= 512, "shared and tensor memory");
 };
 
 // 2-D / 3-D boxes into this CTA, their bytes counted on a barrier of the pair (a cluster address)
@@ -428,20 +495,21 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                   unsigned int* err) {
     using C = PairCfg<F>;
     using FM = MmFmt<F>;
-    constexpr int ST = C::STAGES;
+    constexpr int MS = C::MAX_STAGES;
+    const int ST = p.stages;
     extern __shared__ uint8_t dsm[];
     uint8_t* const stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) unsigned long long bars[2 * ST + 3];  // full[ST], empty[ST], acc full, acc empty, drained
+    __shared__ __align__(8) unsigned long long bars[2 * MS + 3];  // full[MS], empty[MS], acc full, acc empty, drained
     __shared__ uint32_t tmem_addr;
     __shared__ int abort_flag;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const uint32_t rank = cluster_rank(), s0 = smem_u32(stages);
     auto full = [&](int s) { return smem_u32(&bars[s]); };          // the leader's counts both CTAs' bytes
-    auto empty = [&](int s) { return smem_u32(&bars[ST + s]); };
-    const uint32_t acc_full = smem_u32(&bars[2 * ST]), acc_empty = smem_u32(&bars[2 * ST + 1]),
-                   drained = smem_u32(&bars[2 * ST + 2]);
+    auto empty = [&](int s) { return smem_u32(&bars[MS + s]); };
+    const uint32_t acc_full = smem_u32(&bars[2 * MS]), acc_empty = smem_u32(&bars[2 * MS + 1]),
+                   drained = smem_u32(&bars[2 * MS + 2]);
     if (t == 0) {
-        for (int s = 0; s < 2 * ST; ++s) mbar_init(full(s), 1);
+        for (int s = 0; s < 2 * MS; ++s) mbar_init(full(s), 1);
         mbar_init(acc_full, 1);
         mbar_init(acc_empty, 16);  // the epilogue warps of both CTAs
         mbar_init(drained, 1);
@@ -548,9 +616,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         }
     } else {
         const int quad = warp & 3, half = (warp - 2) >> 2;
+        uint32_t* const stage = reinterpret_cast<uint32_t*>(stages + ST * C::STAGE) + (warp - 2) * 32 * kMmPitch;
         const uint32_t mine = acc + ((uint32_t)(quad * 32) << 16), leader_empty = peer_addr(acc_empty, 0);
         T* const out = static_cast<T*>(p.out);
-        const bool a32 = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.ld * (long long)sizeof(T))) & 31) == 0;
+        const bool a32 = rows_aligned<T>(p.out, p.ld);
         int it = 0;
         for (int tile = tile0; tile < p.tiles; tile += tile_step, ++it) {
             bool ok = lane != 0 || mbar_wait<true>(acc_full, (uint32_t)it & 1u, ab, err);
@@ -558,8 +627,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const int xt = tile % p.xtiles, yt = tile / p.xtiles;
-            const int x = xt * 256 + (int)rank * 128 + quad * 32 + lane, y0 = yt * 256 + half * 128;
-            store_rows<T, 128>(mine + half * 128, out, p.ld, x, p.rx, y0, p.ry, a32, [&] {
+            const int x0 = xt * 256 + (int)rank * 128 + quad * 32, y0 = yt * 256 + half * 128;
+            store_rows<T, 128>(mine + half * 128, stage, out, p.ld, x0, p.rx, y0, p.ry, a32, [&] {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(leader_empty);
@@ -638,7 +707,7 @@ template <int F, typename T> cudaError_t go_pair(const MmCall& c) {
     using C = PairCfg<F>;
     auto* kern = k_matmul_pair<F, T>;
     static std::atomic<unsigned long long> ready{0};
-    const cudaError_t e = allow_smem(kern, C::SMEM, c.dev, ready);
+    const cudaError_t e = allow_smem(kern, C::smem(false) > C::smem(true) ? C::smem(false) : C::smem(true), c.dev, ready);
     if (e != cudaSuccess) return e;
     const long long row_bytes = F == F_E2M1 ? c.k / 2 : c.k;
     MmArgs a{};
@@ -653,6 +722,8 @@ template <int F, typename T> cudaError_t go_pair(const MmCall& c) {
     a.tiles = (int)(xt * yt);
     a.split = 1;
     a.ld = c.ld;
+    const bool staged = !rows_aligned<T>(c.out, c.ld);
+    a.stages = C::stages(staged);
     CUtensorMap ma, mb, msa, msb;
     if (!encode_codes_map(&ma, c.xc, c.rx, row_bytes, 128) || !encode_codes_map(&mb, c.yc, c.ry, row_bytes, 128) ||
         !encode_scales_map(&msa, c.xs, c.rx, a.kt4, C::TS, 1) || !encode_scales_map(&msb, c.ys, c.ry, a.kt4, C::TS, 2))
@@ -661,7 +732,7 @@ template <int F, typename T> cudaError_t go_pair(const MmCall& c) {
     const int pairs = c.sms / 2;
     cfg.gridDim = dim3((unsigned)(2 * (a.tiles < pairs ? a.tiles : pairs)));
     cfg.blockDim = dim3(kMmThreads);
-    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.dynamicSmemBytes = C::smem(staged);
     cfg.stream = c.st;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -704,15 +775,16 @@ template <int F, bool SWAP, typename T> cudaError_t go(const MmCall& c, int bn) 
     // more tiles than SMs would take a second wave of several stages (2048 x 2048 x 2048 12.9 against 11.3; with three
     // stages, 1024 x 2560 x 352, 5.6 against 6.1).
     const int nks = (int)((c.k + MmFmt<F>::VALS - 1) / MmFmt<F>::VALS);
-    const bool two = a.tiles > c.sms && nks > 4;
+    const bool staged = !SWAP && !rows_aligned<T>(c.out, c.ld);
+    const bool two = !staged && a.tiles > c.sms && nks > 4;  // two rings and their staging would have two stages each
     a.split = 1;
     while (!two && a.split < kMmSplitMax && a.tiles * a.split * 2 <= c.sms && nks >= a.split * 4) a.split *= 2;
-    a.stages = C::stages(bn, two);
+    a.stages = C::stages(bn, two, staged);
     const int places = two ? 2 * c.sms : c.sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.split > 1 ? a.tiles * a.split : (a.tiles < places ? a.tiles : places)));
     cfg.blockDim = dim3(kMmThreads);
-    cfg.dynamicSmemBytes = C::smem(bn, a.stages);
+    cfg.dynamicSmemBytes = C::smem(bn, a.stages, staged);
     cfg.stream = c.st;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -50,18 +50,6 @@ template <bool CLUSTER = false> __device__ __forceinline__ bool mbar_test(uint32
             : "memory");
     return ok != 0;
 }
-// the phase's state now, without waiting
-__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{ .reg .pred p;\n"
-        "  mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        "  selp.u32 %0, 1, 0, p; }"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 __device__ __forceinline__ unsigned long long global_ns() {
     unsigned long long t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));

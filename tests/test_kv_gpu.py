@@ -318,6 +318,23 @@ def test_nan_blocks_reach_only_the_queries_that_see_them():
     assert torch.isnan(got[50:]).all() and not torch.isnan(got[:50]).any()
 
 
+def test_offsets_beyond_32_bits():
+    """4.9 GB of codes each: pages at both ends of the cache."""
+    pages, kv, page, d = 150_000, 8, 64, 128
+    c = ops.KVCache.empty(pages, kv, page, d)
+    assert c.k_codes.numel() > 1 << 32
+    lens = [200, 70]
+    table = torch.tensor([[pages - 1, 0, pages - 2, 131_073], [pages - 3, pages // 2, 0, 0]], dtype=torch.int32, device="cuda")
+    for b, n in enumerate(lens):
+        pos = torch.arange(n, device="cuda")
+        slots = table[b, pos // page].long() * page + pos % page
+        k, v = rand(b, n, kv, d).bfloat16(), rand(b + 5, n, kv, d).bfloat16()
+        ops.kv_append(k, v, c, slots)
+        assert torch.equal(ops.kv_read(c, slots)[1], mxq.fake_quantize(v, "mxfp4"))
+    check(rand(9, 2, 32, d).bfloat16(), c, table, lens)
+    check(rand(9, 60, 32, d).bfloat16(), c, table, lens, [0, 40, 60])
+
+
 def test_pages_outside_the_cache_are_not_seen():
     lens, page = [100, 40], 16
     c = filled(8, 12, 2, page, 64)

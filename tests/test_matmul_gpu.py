@@ -18,7 +18,7 @@ FMTS = ["mxfp4", "mxfp8"]
 SHAPES = [(1, 32, 32), (1, 128, 64), (1, 4096, 4096), (3, 130, 96), (16, 257, 160), (17, 64, 224), (33, 100, 288), (64, 129, 512),
           (65, 640, 1056), (77, 1000, 2560), (128, 300, 512), (129, 31, 544), (200, 520, 1056), (257, 385, 96),
           (300, 1000, 2048), (1000, 2300, 320), (2100, 2600, 288), (130, 1, 32), (4700, 2400, 352),
-          (5000, 4000, 2080)]
+          (5000, 4000, 2080), (4700, 2401, 352), (2300, 2552, 96), (2305, 2499, 64), (140, 77, 64), (200, 134, 96), (150, 6, 64)]
 
 
 def values(seed, rows, cols, dtype=torch.bfloat16):
@@ -104,13 +104,15 @@ def test_product_repeats_bit_for_bit(m, n, k, fmt):
         assert torch.equal(ops.matmul(*a, *b, fmt), first)
 
 
-def test_product_writes_only_its_output():
-    a, b = mxq.quantize_mma(values(1, 150, 96), "mxfp8"), mxq.quantize_mma(values(2, 75, 96), "mxfp8")
-    buf = torch.full((150 * 75 + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
-    out = buf[32:32 + 150 * 75].view(150, 75)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,n,k", [(150, 75, 96), (3, 75, 96), (130, 201, 2048), (4401, 2303, 64), (4401, 2304, 64), (4401, 2312, 64)])
+def test_product_writes_only_its_output(m, n, k, dtype):
+    a, b = mxq.quantize_mma(values(1, m, k), "mxfp8"), mxq.quantize_mma(values(2, n, k), "mxfp8")
+    buf = torch.full((m * n + 64,), 7.0, dtype=dtype, device="cuda")
+    out = buf[32:32 + m * n].view(m, n)
     ops.matmul(*a, *b, "mxfp8", out=out, check=True)
     assert (buf[:32] == 7).all() and (buf[-32:] == 7).all()
-    assert torch.equal(out, ops.matmul(*a, *b, "mxfp8"))
+    assert torch.equal(out, ops.matmul(*a, *b, "mxfp8", dtype=dtype))
 
 
 def test_product_empty_and_errors():
@@ -152,6 +154,16 @@ def test_quantize_both(rows, cols, row_fmt, col_fmt, dtype):
         assert cc.shape == want[0].shape and torch.equal(cc, want[0]) and torch.equal(cs, want[1])
     else:
         assert cc is None and cs is None
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_both_of_rows_alone_at_size(fmt, dtype):
+    x = values(5, 1152, 1024, dtype)   # whole scale tiles, over a million values: another kernel
+    x[700, 3] = float("nan")
+    rc, rs, _, _ = ops.quantize_both(x, fmt)
+    want = mxq.quantize_mma(x, fmt)
+    assert torch.equal(rc, want[0]) and torch.equal(rs, want[1])
 
 
 def test_quantize_both_errors():
