@@ -6,7 +6,7 @@
 // picosecond and the SMs have about three lane instructions for each: what bounds the kernel is turning codes into
 // operands. Hence:
 // - each warp takes groups of 16 keys (a group lies within a page) through its own ring of stages in shared memory,
-//   filled by 16-byte asynchronous copies three groups ahead: no registers hold data in flight and no warp waits for
+//   filled by 16-byte asynchronous copies two groups ahead: no registers hold data in flight and no warp waits for
 //   another. Codes leave the stage in the layout of mma.sync's fragments. The summed index may be permuted freely,
 //   so the lane that holds key g's part of an operand owns a contiguous quarter of the key (16 bytes of codes and one
 //   scale at head_dim 128), and four lanes share it; for V, whose operand pairs two keys, a lane takes the same 8
@@ -36,7 +36,7 @@ namespace mxq {
 namespace {
 
 constexpr int kAtWarps = 4, kAtThreads = 32 * kAtWarps;
-constexpr int kAtStages = 4;       // groups in a warp's ring
+constexpr int kAtStages = 3;       // groups in a warp's ring (four: as fast, six: 146 us for 141 at 16 sequences of 24..32 thousand keys)
 constexpr int kAtMaxSplits = 256;
 constexpr int kAtMaxEven = 512;    // sequences whose shares are worked out by every CTA
 
@@ -69,23 +69,37 @@ template <int D> struct AtStage {
         return (uint32_t)(V + (r ^ (r >> 2)) * ROW + 16 * c);
     }
 };
-// the lane's share of the copies of a group whose first row of the cache is `row`
-template <int D> __device__ __forceinline__ void fetch(const KvCache& c, long long row, uint32_t stage, int lane) {
+// the lane's share of the copies of a group
+template <int D> struct Fetch {
     using S = AtStage<D>;
-    constexpr int PIECES = S::ROW / 16;  // 16-byte pieces of a row
-    const long long at = row * S::ROW;
+    static constexpr int PIECES = S::ROW / 16;  // 16-byte pieces of a row
+    const char *k, *v;
+    const uint8_t* scales;
+    uint32_t at, at_v[PIECES / 2], at_s;
+    bool scaled;
+    __device__ __forceinline__ Fetch(const KvCache& c, int lane) {
+        k = c.kc + 16 * lane;
+        v = c.vc + 16 * lane;
+        at = S::K + 16 * lane;
 #pragma unroll
-    for (int i = 0; i < PIECES / 2; ++i) {
-        const int j = i * 32 + lane;
-        copy16(stage + S::K + 16 * j, c.kc + at + 16 * j);
-        copy16(stage + S::v_at(j / PIECES, j % PIECES), c.vc + at + 16 * j);
+        for (int i = 0; i < PIECES / 2; ++i) at_v[i] = S::v_at((i * 32 + lane) / PIECES, lane % PIECES);
+        const bool of_v = lane >= S::SROW;  // scales: SROW pieces of 16 bytes each of K and V
+        const int j = lane - (of_v ? S::SROW : 0);
+        scaled = lane < 2 * S::SROW;
+        scales = (of_v ? c.vs : c.ks) + 16 * j;
+        at_s = (of_v ? S::VS : S::KS) + 16 * j;
     }
-    if (lane < 2 * S::SROW) {  // scales: SROW pieces of 16 bytes each of K and V
-        const bool v = lane >= S::SROW;
-        const int j = lane - (v ? S::SROW : 0);
-        copy16(stage + (v ? S::VS : S::KS) + 16 * j, (v ? c.vs : c.ks) + row * S::SROW + 16 * j);
+    // group: its place in the cache, in groups (2^31 of them would be 2 TB at head_dim 64)
+    __device__ __forceinline__ void copy(int group, uint32_t stage) const {
+        const long long from = (long long)group * (16 * S::ROW);
+#pragma unroll
+        for (int i = 0; i < PIECES / 2; ++i) {
+            copy16(stage + at + 512 * i, k + from + 512 * i);
+            copy16(stage + at_v[i], v + from + 512 * i);
+        }
+        if (scaled) copy16(stage + at_s, scales + (long long)group * (16 * S::SROW));
     }
-}
+};
 
 // float offset of dimension d of row r in a warp's result: rows D + 4 floats apart, so that the lanes' 16-byte
 // writes (dimensions g D/8 .., rows 2t, 2t + 1) meet in a bank at most in pairs
@@ -192,24 +206,25 @@ template <int D, int NQ> __device__ __forceinline__ void attend(const AtArgs& p,
     const int pos_lo = s.len - s.n + i0, pos_hi = s.len - s.n + i1;
     const int whole_hi = min(s.len, pos_lo + 1) >> 4, whole_lo = p.window > 0 ? ((pos_hi - p.window) >> 4) + 1 : 0;
     const uint32_t ring = smem_u32(dsm) + warp * kAtStages * S::BYTES;
-    int pages = -1, offs = 0;   // lane j: page and first row of the warp's group 32 * (issued / 32) + j
+    int places = -1;            // lane j: place in the cache (in groups; -1: none) of the warp's group 32 * (issued / 32) + j
     int issued = 0;             // groups of this warp whose copies are issued
     uint32_t there = 0;         // bit j: the group issued j before the last is in a page of the cache
     uint32_t put = ring;
+    const Fetch<D> from(p.c, lane);
     auto issue = [&] {
         if ((issued & 31) == 0) {
             const int grp = first + warp + (issued + lane) * kAtWarps;
-            pages = -1;
+            places = -1;
             if (grp < last) {
                 const int key = 16 * grp, at = p.by_page(key);
-                offs = key - at * p.c.page;
                 const int pg = __ldg(p.table + b * p.table_stride + at);
-                pages = pg >= 0 && pg < p.c.pages ? pg : -1;
+                if (pg >= 0 && pg < p.c.pages)
+                    places = (int)((((long long)pg * p.c.heads + head) * p.c.page + (key - at * p.c.page)) >> 4);
             }
         }
-        const int pg = __shfl_sync(0xFFFFFFFFu, pages, issued & 31), off = __shfl_sync(0xFFFFFFFFu, offs, issued & 31);
-        if (pg >= 0) fetch<D>(p.c, ((long long)pg * p.c.heads + head) * p.c.page + off, put, lane);
-        there = (there << 1) | (pg >= 0 ? 1u : 0u);
+        const int place = __shfl_sync(0xFFFFFFFFu, places, issued & 31);
+        if (place >= 0) from.copy(place, put);
+        there = (there << 1) | (place >= 0 ? 1u : 0u);
         asm volatile("cp.async.commit_group;" ::: "memory");
         ++issued;
         put = put + S::BYTES == ring + kAtStages * S::BYTES ? ring : put + S::BYTES;
