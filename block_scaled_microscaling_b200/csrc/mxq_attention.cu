@@ -28,6 +28,7 @@
 // joins them in order. Otherwise a long sequence is split over a fixed number of CTAs, joined the same way.
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "mxq_attention.cuh"
@@ -38,6 +39,7 @@ namespace {
 constexpr int kAtWarps = 4, kAtThreads = 32 * kAtWarps;
 constexpr int kAtStages = 3;       // groups in a warp's ring (four: as fast, six: 146 us for 141 at 16 sequences of 24..32 thousand keys)
 constexpr int kAtMaxSplits = 256;
+constexpr long long kJoinRows = 2048;  // below, the warps of a CTA share the splits of a row (4096 rows of 9 splits: 92 us so, 85 with a warp each)
 constexpr int kAtMaxEven = 512;    // sequences whose shares are worked out by every CTA
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -668,13 +670,18 @@ template <int D, int NQ> __global__ void __launch_bounds__(256) k_kv_attention_j
 }
 
 // join the splits of one row: CTA (sequence, query, head), one thread per dimension
-template <int D, int ROWS> __global__ void __launch_bounds__(D) k_kv_attention_join(const AtArgs p) {
-    const int d = threadIdx.x;
+// W: warps that share a row's splits (4 where rows are few, else 1)
+template <int D, int ROWS, int W> __global__ void __launch_bounds__(kAtThreads) k_kv_attention_join(const AtArgs p) {
+    constexpr int PER = D / 32, AHEAD = 8;  // dimensions of a lane, loads in flight
+    using Vec = std::conditional_t<PER == 4, float4, float2>;
+    __shared__ float others[W][D + 1];
+    const int lane = threadIdx.x & 31, w = W == 1 ? 0 : threadIdx.x >> 5;
     pdl_wait_then_release();
-    int id = blockIdx.x;
+    int id = W == 1 ? blockIdx.x * kAtWarps + (threadIdx.x >> 5) : blockIdx.x;
     const int h = id % p.heads;
     id /= p.heads;
     const int i = id % p.max_q, b = id / p.max_q;
+    if (b >= p.batch) return;
     const Span s = span_of(p, b);
     if (i >= s.nq) return;
     const int head = h / p.group, row = i * p.group + h - head * p.group, rt = row / ROWS, r0 = rt * ROWS;
@@ -684,21 +691,63 @@ template <int D, int ROWS> __global__ void __launch_bounds__(D) k_kv_attention_j
     const int n = (gr.hi - gr.lo + gr.per - 1) / gr.per;
     if (n <= 1) return;  // written by its split
     const long long first = (((long long)b * p.c.heads + head) * p.row_tiles + rt) * p.splits * ROWS + (row - r0);
-    const float* ml = p.part + p.part_ml + first * 2;
+    const float2* const ml = reinterpret_cast<const float2*>(p.part + p.part_ml) + first;
+    const Vec* const part = reinterpret_cast<const Vec*>(p.part + first * D) + lane;
     float top = -INFINITY;
-    for (int q = 0; q < n; ++q) top = fmaxf(top, __ldcg(ml + (long long)q * ROWS * 2));
-    float total = 0.f, sum = 0.f;
-    const float* part = p.part + first * D + d;
-#pragma unroll 8
-    for (int q = 0; q < n; ++q) {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(ml + (long long)q * ROWS * 2));
-        const float f = x.x == -INFINITY ? 1.f : ex2(x.x - top);
-        total += x.y * f;
-        sum += __ldcg(part + (long long)q * ROWS * D) * f;
+    for (int q = lane; q < n; q += 32) top = fmaxf(top, __ldcg(&ml[(long long)q * ROWS]).x);
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    float total = 0.f, sum[PER] = {};
+    const int per = (n + W - 1) / W, hi = min((w + 1) * per, n);  // this warp's splits: w per .. hi - 1
+    for (int q0 = w * per; q0 < hi; q0 += 32) {
+        float f = 0.f;
+        if (q0 + lane < hi) {
+            const float2 x = __ldcg(&ml[(long long)(q0 + lane) * ROWS]);
+            f = x.x == -INFINITY ? 1.f : ex2(x.x - top);
+            total += x.y * f;
+        }
+        const int m = min(32, hi - q0);
+        for (int q1 = 0; q1 < m; q1 += AHEAD) {
+            Vec x[AHEAD];
+#pragma unroll
+            for (int q = 0; q < AHEAD; ++q)
+                if (q1 + q < m) x[q] = __ldcg(part + (long long)(q0 + q1 + q) * (ROWS * 32));
+#pragma unroll
+            for (int q = 0; q < AHEAD; ++q) {
+                const float fq = __shfl_sync(0xFFFFFFFFu, f, (q1 + q) & 31);
+                if (q1 + q >= m) continue;
+                sum[0] += x[q].x * fq;
+                sum[1] += x[q].y * fq;
+                if constexpr (PER == 4) {
+                    sum[2] += x[q].z * fq;
+                    sum[3] += x[q].w * fq;
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) others[w][PER * lane + k] = sum[k];
+        if (lane == 0) others[w][D] = total;
+        __syncthreads();
+        if (w > 0) return;
+#pragma unroll
+        for (int v = 1; v < W; ++v) {
+            total += others[v][D];
+#pragma unroll
+            for (int k = 0; k < PER; ++k) sum[k] += others[v][PER * lane + k];
+        }
     }
     const long long at = (long long)(s.q0 + i) * p.heads + h;
-    p.out[at * D + d] = __float2bfloat16_rn(total == 0.f ? 0.f : sum / total);
-    if (p.lse && d == 0) p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    uint32_t out[PER / 2];
+#pragma unroll
+    for (int k = 0; k < PER / 2; ++k) out[k] = bf16x2(sum[2 * k] * inv, sum[2 * k + 1] * inv);
+    if constexpr (PER == 4) reinterpret_cast<uint2*>(p.out + at * D)[lane] = make_uint2(out[0], out[1]);
+    else reinterpret_cast<uint32_t*>(p.out + at * D)[lane] = out[0];
+    if (p.lse && lane == 0) p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
 }
 
 // eights of rows per tile; more than 32 rows: the kernel that decodes a block of keys for 256 of them at once
@@ -759,7 +808,8 @@ Plan plan_of(const KvCache& c, long long batch, int max_q, int heads, long long 
 template <int D, int ROWS> cudaError_t join(const AtArgs& a, cudaStream_t st) {
     const long long rows = (long long)a.batch * a.max_q * a.heads;
     if (rows > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-    return launch_pdl(k_kv_attention_join<D, ROWS>, (unsigned)rows, D, st, a);
+    if (rows < kJoinRows) return launch_pdl(k_kv_attention_join<D, ROWS, kAtWarps>, (unsigned)rows, kAtThreads, st, a);
+    return launch_pdl(k_kv_attention_join<D, ROWS, 1>, (unsigned)((rows + kAtWarps - 1) / kAtWarps), kAtThreads, st, a);
 }
 
 template <int D, int NQ> cudaError_t go(const AtArgs& a, const Plan& pl, int dev, cudaStream_t st) {

@@ -173,32 +173,39 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
             const int pos = r < rows ? s.len - s.n + i : -1;
             const int see_hi = min(pos + 1, s.len), see_lo = p.window > 0 ? pos - p.window + 1 : 0;  // keys see_lo .. see_hi - 1
             const uint32_t ts = tm + ((uint32_t)(quad * 32) << 16) + kColS + 128 * x, to = ts + kColO - kColS;
+            constexpr int LANES = D / 8, RPI = 32 / LANES;  // lanes that read or write a row, rows at a time
+            const int ch = lane % LANES, sub = lane / LANES;
             float mul;
             {
-                // Q's row over a power of two, in f16
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + (s.q0 + i) * p.q_row_stride + h * p.q_head_stride);
-                uint32_t q[D / 2], top = 0;
+                // Q's rows over a power of two, in f16; D / 8 lanes read a row
+                uint4 q[LANES];
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    const uint4 v = __ldg(src + j);
-                    q[4 * j] = v.x;
-                    q[4 * j + 1] = v.y;
-                    q[4 * j + 2] = v.z;
-                    q[4 * j + 3] = v.w;
+                for (int k = 0; k < LANES; ++k) {
+                    const int rk = min(r0 + 128 * x + quad * 32 + k * RPI + sub, rows - 1), ik = p.by_group(rk);
+                    const int hk = head * p.group + (rk - ik * p.group);
+                    q[k] = __ldg(reinterpret_cast<const uint4*>(p.q + (s.q0 + ik) * p.q_row_stride + hk * p.q_head_stride) + ch);
                 }
+                int mine = 0;
 #pragma unroll
-                for (int j = 0; j < D / 2; ++j) top = max(top, max((q[j] & 0x7FFFu) << 16, q[j] & 0x7FFF0000u));
-                const int e = min(max((int)(top >> 23), 1), 253) - 127;
-                const float down = pow2i(-e);
-                mul = p.scale * pow2i(e);
+                for (int k = 0; k < LANES; ++k) {
+                    const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+                    uint32_t top = 0;
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
+                    for (int j = 0; j < 4; ++j) top = max(top, max((w[j] & 0x7FFFu) << 16, w[j] & 0x7FFF0000u));
+#pragma unroll
+                    for (int j = 1; j < LANES; j *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, j));
+                    const int e = min(max((int)(top >> 23), 1), 253) - 127;
+                    const float down = pow2i(-e);
                     uint32_t f[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        f[k] = pack_h2(__uint_as_float(q[4 * j + k] << 16) * down, __uint_as_float(q[4 * j + k] & 0xFFFF0000u) * down);
-                    sts128(sb + x * C::Q + (j >> 3) * 16384 + row * 128 + (((j & 7) ^ (row & 7)) << 4), f[0], f[1], f[2], f[3]);
+                    for (int j = 0; j < 4; ++j)
+                        f[j] = pack_h2(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xFFFF0000u) * down);
+                    const int to_row = quad * 32 + k * RPI + sub;
+                    sts128(sb + x * C::Q + (ch >> 3) * 16384 + to_row * 128 + (((ch & 7) ^ (to_row & 7)) << 4), f[0], f[1], f[2], f[3]);
+                    const int theirs = __shfl_sync(0xFFFFFFFFu, e, lane % RPI * LANES);  // of row k * RPI + lane % RPI
+                    if (lane / RPI == k) mine = theirs;
                 }
+                mul = p.scale * pow2i(mine);
                 fence_proxy_async();
                 mbar_arrive(q_full(x));
             }
@@ -295,39 +302,58 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
             tc_fence_after();
             if (!(thr > 0.f)) m = -INFINITY;
             if (ok) {
-                const long long at = (long long)(s.q0 + i) * p.heads + h, slot = (long long)blockIdx.x * kTileRows + 128 * x + row;
+                const long long at = (long long)(s.q0 + i) * p.heads + h, slot0 = (long long)blockIdx.x * kTileRows + 128 * x + quad * 32;
                 const float vtrue = pow2i(vref - 127), f = alone ? (l == 0.f ? 0.f : vtrue / l) : vtrue;
                 const float nan = __uint_as_float(0x7FC00000u);
+                // through the rows' place of Q, which nothing reads any more: whole rows, 16 bytes a lane
+                const uint32_t stage = sb + x * C::Q + quad * (C::Q / 4), mine = stage + lane * (2 * D);
+                const int cols = alone ? D : D / 2, left = rows - (r0 + 128 * x + quad * 32);  // columns at a time
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    uint32_t o[16];
-                    if (n > 0) {
-                        tmem_ld16(to + c, o);
-                        tmem_wait_ld();
-                    } else {
+                for (int c0 = 0; c0 < D; c0 += cols) {
+#pragma unroll 1
+                    for (int c = c0; c < c0 + cols; c += 16) {
+                        uint32_t o[16];
+                        if (n > 0) {
+                            tmem_ld16(to + c, o);
+                            tmem_wait_ld();
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = 0;
-                    }
-                    const float g = (vnan >> (c >> 5)) & 1u ? nan : f;
-                    if (r < rows) {
+                            for (int j = 0; j < 16; ++j) o[j] = 0;
+                        }
+                        const float g = (vnan >> (c >> 5)) & 1u ? nan : f;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * g);
                         if (alone) {
                             uint32_t w[8];
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) w[j] = bf16x2(__uint_as_float(o[2 * j]) * g, __uint_as_float(o[2 * j + 1]) * g);
-                            uint4* const dst = reinterpret_cast<uint4*>(p.out + at * D + c);
-                            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                            for (int j = 0; j < 8; ++j) w[j] = bf16x2(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                sts128(mine + ((((c >> 3) + j) ^ (lane & 7)) << 4), w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
                         } else {
-                            float4* const dst = reinterpret_cast<float4*>(p.part + slot * D + c);
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                dst[j] = make_float4(__uint_as_float(o[4 * j]) * g, __uint_as_float(o[4 * j + 1]) * g,
-                                                     __uint_as_float(o[4 * j + 2]) * g, __uint_as_float(o[4 * j + 3]) * g);
+                                sts128(mine + (((((c - c0) >> 2) + j) ^ (lane & 7)) << 4), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                         }
                     }
+                    __syncwarp();
+#pragma unroll 4
+                    for (int k = 0; k < LANES; ++k) {
+                        const int rk = k * RPI + sub;
+                        const uint4 v = lds128u(stage + rk * (2 * D) + ((ch ^ (rk & 7)) << 4));
+                        if (rk >= left) continue;
+                        if (alone) {
+                            const int row_k = r0 + 128 * x + quad * 32 + rk, ik = p.by_group(row_k);
+                            const long long at_k = (long long)(s.q0 + ik) * p.heads + head * p.group + (row_k - ik * p.group);
+                            reinterpret_cast<uint4*>(p.out + at_k * D)[ch] = v;
+                        } else {
+                            reinterpret_cast<uint4*>(p.part + (slot0 + rk) * D + c0)[ch] = v;
+                        }
+                    }
+                    __syncwarp();
                 }
                 if (r < rows) {
-                    if (!alone) *reinterpret_cast<float2*>(p.part + p.part_ml + slot * 2) = make_float2(m, l);
+                    if (!alone) *reinterpret_cast<float2*>(p.part + p.part_ml + (slot0 + lane) * 2) = make_float2(m, l);
                     else if (p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
                 }
             }
