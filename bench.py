@@ -638,7 +638,49 @@ PROFILE_CASES = ["batch_weight", "q_e2m3_weight", "q_e3m2_weight", "dq_e2m3_weig
                  "q_e2m3_layer", "fq_axs6_grad", "exp_mxfp4_scores", "expfree_mxfp4_scores", "qcols_e2m3_weight",
                  "dqcols_e2m3_weight", "qcols_e2m3_act", "dqcols_e2m3_act", "exmy_e3m3_act", "dq_exmy_e3m3_act",
                  "fq_exmy_e3m3_act", "qmma_mxfp8_act", "dq_e2m3_act", "fq_axs6_quickstart",
-                 "swizzle_scales_act", "exp_e2m3_scores", "exp_axs6_scores", "dqcols_e2m3_f32", "stack_steady"]
+                 "swizzle_scales_act", "exp_e2m3_scores", "exp_axs6_scores", "dqcols_e2m3_f32", "stack_steady",
+                 "matmul_mxfp4", "matmul_mxfp8", "matmul_mxfp8_token", "qboth_mxfp8", "swiglu_fwd", "swiglu_bwd", "kv_append",
+                 "kv_attention_decode", "kv_attention_chunk"]
+
+
+def operator_case(torch, name, gen):
+    """The call of one operator on its workload."""
+    import block_scaled_microscaling_b200 as mxb
+    dev = torch.device("cuda")
+    rand = lambda *s: torch.randn(*s, device=dev, generator=gen).to(torch.bfloat16)  # noqa: E731
+    if name.startswith("matmul"):
+        fmt = name.split("_")[1]
+        m, n, k = (1, 4096, 4096) if name.endswith("token") else (8192, 9728, 2560)
+        a, b = mxb.quantize_mma(rand(m, k), fmt), mxb.quantize_mma(rand(n, k), fmt)
+        out = torch.empty(m, n, dtype=torch.bfloat16, device=dev)
+        return lambda: mxb.matmul(*a, *b, fmt, out=out)
+    if name == "qboth_mxfp8":
+        x = rand(8192, 9728)
+        return lambda: mxb.quantize_both(x, "mxfp8", "mxfp8")
+    if name.startswith("swiglu"):
+        x = rand(16384, 2 * 9728).requires_grad_()
+        dy = rand(16384, 9728)
+        if name == "swiglu_fwd":
+            return lambda: mxb.swiglu(x)
+        y = mxb.swiglu(x)
+        return lambda: torch.autograd.grad(y, x, dy, retain_graph=True)
+    heads, d, page = 8, 128, 64
+    if name == "kv_append":
+        c = mxb.KVCache.empty(256, heads, page, d)
+        k, v = rand(16384, heads, d), rand(16384, heads, d)
+        slots = torch.randperm(256 * page, device=dev, generator=gen)
+        return lambda: mxb.kv_append(k, v, c, slots)
+    batch, queries, keys = (16, 1, 32768) if name == "kv_attention_decode" else (1, 128, 32768)
+    pages = batch * keys // page
+    c = mxb.KVCache.empty(pages, heads, page, d)
+    for i in range(0, pages * page, 16384):
+        slots = torch.arange(i, i + 16384, device=dev)
+        mxb.kv_append(rand(16384, heads, d), rand(16384, heads, d), c, slots)
+    table = torch.randperm(pages, device=dev, generator=gen).to(torch.int32).view(batch, -1)
+    lens = torch.full((batch,), keys, dtype=torch.int32, device=dev)
+    q = rand(batch * queries, 4 * heads, d)
+    starts = torch.arange(0, batch * queries + 1, queries, dtype=torch.int32, device=dev)
+    return lambda: mxb.kv_attention(q, c, table, lens, q_starts=starts, max_q=queries)
 
 
 def profile_case(name, reps):
@@ -749,6 +791,8 @@ def profile_case(name, reps):
         sc = torch.randn(4096, 32768, device=dev, generator=gen) * 3
         c, s = mxq.exp_free_quantize(sc)
         fn = lambda: mxq.exp_free_quantize(sc, codes=c, scales=s)
+    elif name.split("_")[0] in ("matmul", "qboth", "swiglu", "kv"):
+        fn = operator_case(torch, name, gen)
     else:
         raise SystemExit(f"unknown profile case {name}; one of {PROFILE_CASES}")
     for _ in range(reps):
