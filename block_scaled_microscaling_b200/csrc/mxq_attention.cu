@@ -20,12 +20,16 @@
 //   of it; codes of blocks more than 2^29 below the largest seen lose bits. Rows of Q are divided by a power of
 //   two for the same reason. Scores return to their true size in fp32.
 // - the running maximum m_r is raised only when a score exceeds it by 2^8 (one vote per 16 keys); the weights
-//   then are at most 2^8 and round to f16 (relative error 2^-12; below 2^-14 absolute, 2^-25).
+//   then are at most 2^8 and round to f16 (relative error 2^-11; below 2^-14 absolute, 2^-25).
 // The four warps of a CTA take every fourth group (page numbers are fetched 32 groups at a time); their results are
 // joined through shared memory. Where one row tile holds a sequence's queries (decoding), the groups of all sequences
 // and heads are cut into equal shares, one per resident CTA, whatever the lengths: a CTA walks the pieces of its
 // share, and the at most two of them that are part of a split sequence leave their sums to a second kernel, which
 // joins them in order. Otherwise a long sequence is split over a fixed number of CTAs, joined the same way.
+// Measured (32 heads on 8 of 128, one query each): 16 sequences of 24 .. 32 thousand keys 140 us (3.6 TB/s of cache; the
+// issue slots are 63% busy, the arithmetic pipe 52%, and the waits of dependent conversions fill the rest: with three
+// CTAs to an SM, 183 us; five, with spilled registers, 158; two groups at a time, 143), one sequence of 4000 keys 10
+// us, of 32768 keys 22.
 #include <atomic>
 #include <cstdint>
 #include <type_traits>

@@ -9,7 +9,10 @@
 // 16-byte reads along a row and 4-byte reads across columns are both free of conflicts); a thread encodes two
 // blocks of a row, then two of the columns. Rows past the end count as zeros: the column direction fills its
 // last block up with them, and the scale tiles are written whole, padding included.
-// Bound by memory: E4M3 both ways of bf16 moves 2 + 2 * 33/32 bytes per value.
+// Bound by memory: E4M3 both ways of bf16 moves 2 + 2 * 33/32 bytes per value; 8192 x 9728 63 us (5.1 TB/s; the
+// shared-memory transposition and the long-scoreboard waits of its loads are what is left, DRAM is half busy). Rows
+// alone of whole scale tiles and at least 2^20 values take the quantize kernel of the conversions, which needs no
+// transposition (16384 x 2560 MXFP4 17 us).
 #include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>

@@ -62,7 +62,8 @@ MXQ_API mxq_status mxq_quantize_both(mxq_format row_fmt, mxq_format col_fmt, con
  *   out [m, n] of type dtype.
  * workspace: mxq_linear_workspace_bytes(fmt, m, k) bytes, 16-byte aligned, for x's
  * codes and scales; used by this call alone until it has finished. Other rules
- * and errors as mxq_quantize_mma and mxq_matmul.
+ * and errors, and bounded waits (mxq_check_device), as mxq_quantize_mma and
+ * mxq_matmul.
  */
 MXQ_API size_t mxq_linear_workspace_bytes(mxq_format fmt, int64_t m, int64_t k);
 MXQ_API mxq_status mxq_linear(mxq_format fmt, const void* x, mxq_dtype dtype, int64_t m, int64_t k,
@@ -161,7 +162,10 @@ MXQ_API mxq_status mxq_kv_read(const mxq_kv_cache* cache, const int64_t* slots, 
  *   workspace  mxq_kv_attention_workspace_bytes(...) bytes (may be 0: then NULL),
  *          16-byte aligned, used by this call alone until it has finished.
  * Keys and values are decoded to half precision (f16) exactly up to a power of
- * two; scores and sums are fp32; the weights w enter the second product in f16.
+ * two (a block more than 2^20 below the largest of its sequence and head may
+ * lose bits or count as zero); scores and sums are fp32; the weights w enter the second product in f16.
+ * Where max_q * (q_heads / kv_heads) exceeds 32, the kernel's waits are bounded
+ * (mxq_check_device).
  */
 MXQ_API size_t mxq_kv_attention_workspace_bytes(const mxq_kv_cache* cache, int64_t batch, int64_t q_rows,
                                                 int32_t max_q, int32_t q_heads, int64_t max_keys);
