@@ -178,8 +178,8 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
             const uint32_t ts = tm + ((uint32_t)(quad * 32) << 16) + kColS + 128 * x, to = ts + kColO - kColS;
             constexpr int LANES = D / 8, RPI = 32 / LANES;  // lanes that read or write a row, rows at a time
             const int ch = lane % LANES, sub = lane / LANES;
-            float mul;
-            {
+            float mul = 0.f;
+            if (n > 0) {  // (without keys the rows' place of Q is used for the output alone)
                 // Q's rows over a power of two, in f16; D / 8 lanes read a row
                 uint4 q[LANES];
 #pragma unroll

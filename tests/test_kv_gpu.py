@@ -318,6 +318,21 @@ def test_nan_blocks_reach_only_the_queries_that_see_them():
     assert torch.isnan(got[50:]).all() and not torch.isnan(got[:50]).any()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_queries_of_empty_sequences_give_zeros(d):
+    batch, news = 150, 40   # more CTAs than fit at a time; 160 rows each
+    c = filled(1, 4, 2, 16, d)
+    q = rand(2, batch * news, 8, d).bfloat16()
+    for n in (0, -3):
+        lens = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+        out, lse = ops.kv_attention(q, c, torch.zeros(batch, 2, dtype=torch.int32, device="cuda"), lens, lse=True)
+        assert (out == 0).all() and (lse == -math.inf).all()
+    # the queries before the first key see nothing
+    lens = torch.full((batch,), 5, dtype=torch.int32, device="cuda")
+    out = ops.kv_attention(q, c, torch.zeros(batch, 2, dtype=torch.int32, device="cuda"), lens).view(batch, news, 8, d)
+    assert (out[:, :-5] == 0).all() and (out[:, -5:] != 0).any(-1).all()
+
+
 def test_offsets_beyond_32_bits():
     """4.9 GB of codes each: pages at both ends of the cache."""
     pages, kv, page, d = 150_000, 8, 64, 128
