@@ -228,30 +228,54 @@ __device__ __forceinline__ void store_rows(uint32_t mine, uint32_t* stage, T* ou
 }
 
 // the partial tiles [bn][128] of S CTAs, at `part` in each, added in rank order: this CTA's share of the columns to
-// out (256 threads: row e % 128, columns in two halves)
+// out. 256 threads: in the transposed form (rows of out are columns of the tile) four rows of a column each, 16 bytes
+// from every CTA; else row e % 128, a run of columns in two halves
 template <int S, bool SWAP, typename T>
 __device__ __forceinline__ void add_parts(uint32_t part, int e, int rank, int bn, int x, int y0, const MmArgs& p, T* out, uint32_t* stage,
                                           bool a32) {
-    constexpr int RUN = SWAP ? 2 : 32 / (int)sizeof(T);  // columns at a time
-    const int r = e & 127, per = bn / S;                 // bn is a multiple of 16, S at most 8
-    for (int c = rank * per + (e >> 7) * RUN; c < (rank + 1) * per && y0 + c < p.ry; c += 2 * RUN) {
-        float v[RUN][S], sum[RUN];
+    const int per = bn / S;  // bn is a multiple of 16, S at most 8
+    if constexpr (SWAP) {
+        const int r = 4 * (e & 31);
+        if (x + r >= p.rx) return;
+        const bool whole = a32 && x + r + 4 <= p.rx;
+#pragma unroll 2
+        for (int c = rank * per + (e >> 5); c < (rank + 1) * per && y0 + c < p.ry; c += 8) {
+            float4 v[S];
 #pragma unroll
-        for (int i = 0; i < RUN; ++i)
+            for (int q = 0; q < S; ++q) v[q] = ld_peer_f32x4(part + 4u * (uint32_t)(c * 128 + r), (uint32_t)q);
 #pragma unroll
-            for (int q = 0; q < S; ++q) v[i][q] = ld_peer_f32(part + 4u * (uint32_t)((c + i) * 128 + r), (uint32_t)q);
+            for (int q = 1; q < S; ++q) {
+                v[0].x += v[q].x;
+                v[0].y += v[q].y;
+                v[0].z += v[q].z;
+                v[0].w += v[q].w;
+            }
+            T* const to = out + (long long)(y0 + c) * p.ld + x + r;
+            if (whole) {
+                if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(to) = v[0];
+                else *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(v[0].x, v[0].y), bf16x2(v[0].z, v[0].w));
+            } else {
+                const float f[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
-        for (int i = 0; i < RUN; ++i) {
-            sum[i] = v[i][0];
-#pragma unroll
-            for (int q = 1; q < S; ++q) sum[i] += v[i][q];
+                for (int i = 0; i < 4; ++i)
+                    if (x + r + i < p.rx) to[i] = round_to<T>(f[i]);
+            }
         }
-        if constexpr (SWAP) {
-            if (x + r >= p.rx) continue;
+    } else {
+        constexpr int RUN = 32 / (int)sizeof(T);  // columns at a time
+        const int r = e & 127;
+        for (int c = rank * per + (e >> 7) * RUN; c < (rank + 1) * per && y0 + c < p.ry; c += 2 * RUN) {
+            float v[RUN][S], sum[RUN];
 #pragma unroll
             for (int i = 0; i < RUN; ++i)
-                if (y0 + c + i < p.ry) out[(long long)(y0 + c + i) * p.ld + x + r] = round_to<T>(sum[i]);
-        } else {
+#pragma unroll
+                for (int q = 0; q < S; ++q) v[i][q] = ld_peer_f32(part + 4u * (uint32_t)((c + i) * 128 + r), (uint32_t)q);
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {
+                sum[i] = v[i][0];
+#pragma unroll
+                for (int q = 1; q < S; ++q) sum[i] += v[i][q];
+            }
             uint32_t w[8];
             pack_run<T>(sum, w);
             if (!a32) store_staged<T, RUN>(w, stage, out, p.ld, x + (r & ~31), p.rx, y0 + c, p.ry);

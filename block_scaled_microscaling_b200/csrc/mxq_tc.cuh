@@ -188,5 +188,12 @@ __device__ __forceinline__ float ld_peer_f32(uint32_t saddr, uint32_t rank) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(p) : "memory");
     return v;
 }
+__device__ __forceinline__ float4 ld_peer_f32x4(uint32_t saddr, uint32_t rank) {  // four of them, 16-byte aligned
+    uint32_t p;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(saddr), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(p) : "memory");
+    return v;
+}
 
 }  // namespace mxq
