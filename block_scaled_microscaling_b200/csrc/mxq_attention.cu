@@ -643,43 +643,113 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
     attend<D, NQ>(p, w);
 }
 
-// the sequences that shares split: share c's first piece names one; the share where it was split first joins it.
-// 256 threads take 256 / D rows, one dimension each.
+// ---- joining ------------------------------------------------------------------------------------
+
+template <int D> struct Joined {
+    static constexpr int PER = D / 32;  // dimensions of a lane
+    float top, total, sum[PER];
+};
+// the sum of a row's pieces: its maximum, total and the lane's D / 32 dimensions. `at(q)` is piece q's row of the partial
+// sums; this warp takes the pieces lo .. hi - 1 of n (the maximum is over all)
+template <int D, typename At> __device__ __forceinline__ Joined<D> join_pieces(const AtArgs& p, int n, int lo, int hi, At at) {
+    constexpr int PER = D / 32, AHEAD = 8;  // loads in flight
+    using Vec = std::conditional_t<PER == 4, float4, float2>;
+    const int lane = threadIdx.x & 31;
+    const float2* const ml = reinterpret_cast<const float2*>(p.part + p.part_ml);
+    const Vec* const part = reinterpret_cast<const Vec*>(p.part) + lane;
+    Joined<D> r;
+    r.top = -INFINITY;
+    for (int q = lane; q < n; q += 32) r.top = fmaxf(r.top, __ldcg(&ml[at(q)]).x);
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) r.top = fmaxf(r.top, __shfl_xor_sync(0xFFFFFFFFu, r.top, d));
+    r.total = 0.f;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) r.sum[k] = 0.f;
+    for (int q0 = lo; q0 < hi; q0 += 32) {
+        float f = 0.f;
+        if (q0 + lane < hi) {
+            const float2 x = __ldcg(&ml[at(q0 + lane)]);
+            f = x.x == -INFINITY ? 1.f : ex2(x.x - r.top);
+            r.total += x.y * f;
+        }
+        const int m = min(32, hi - q0);
+        for (int q1 = 0; q1 < m; q1 += AHEAD) {
+            Vec x[AHEAD];
+#pragma unroll
+            for (int q = 0; q < AHEAD; ++q)
+                if (q1 + q < m) x[q] = __ldcg(part + at(q0 + q1 + q) * 32);
+#pragma unroll
+            for (int q = 0; q < AHEAD; ++q) {
+                const float fq = __shfl_sync(0xFFFFFFFFu, f, (q1 + q) & 31);
+                if (q1 + q >= m) continue;
+                r.sum[0] += x[q].x * fq;
+                r.sum[1] += x[q].y * fq;
+                if constexpr (PER == 4) {
+                    r.sum[2] += x[q].z * fq;
+                    r.sum[3] += x[q].w * fq;
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) r.total += __shfl_xor_sync(0xFFFFFFFFu, r.total, d);
+    return r;
+}
+template <int D> __device__ __forceinline__ void write_joined(const AtArgs& p, const Joined<D>& r, long long at) {
+    constexpr int PER = D / 32;
+    const int lane = threadIdx.x & 31;
+    const float inv = r.total == 0.f ? 0.f : 1.f / r.total;
+    uint32_t out[PER / 2];
+#pragma unroll
+    for (int k = 0; k < PER / 2; ++k) out[k] = bf16x2(r.sum[2 * k] * inv, r.sum[2 * k + 1] * inv);
+    if constexpr (PER == 4) reinterpret_cast<uint2*>(p.out + at * D)[lane] = make_uint2(out[0], out[1]);
+    else reinterpret_cast<uint32_t*>(p.out + at * D)[lane] = out[0];
+    if (p.lse && lane == 0) p.lse[at] = r.total == 0.f ? -INFINITY : (r.top + log2f(r.total)) * kLn2;
+}
+// adds what the other warps of a row summed, in their order: warp `w` of W; `others` is the row's, [W][D + 1]. All of the
+// CTA's threads call it; warp 0 has the result.
+template <int D, int W> __device__ __forceinline__ void join_warps(Joined<D>& r, int w, float* others) {
+    constexpr int PER = D / 32;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) others[w * (D + 1) + PER * lane + k] = r.sum[k];
+    if (lane == 0) others[w * (D + 1) + D] = r.total;
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int v = 1; v < W; ++v) {
+        r.total += others[v * (D + 1) + D];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) r.sum[k] += others[v * (D + 1) + PER * lane + k];
+    }
+}
+
+// the sequences that shares split: share c's first piece names one; the share where it was split first joins it. Four
+// warps take a row, two rows to a CTA.
 template <int D, int NQ> __global__ void __launch_bounds__(256) k_kv_attention_join_shares(const AtArgs p) {
-    constexpr int ROWS = 8 * NQ;
+    constexpr int ROWS = 8 * NQ, W = 4;
+    __shared__ float others[2][W][D + 1];
     pdl_wait_then_release();
     const int c = blockIdx.x + 1;
     const int4 info = __ldcg(p.info + c);
     if (info.x < 0 || !info.z) return;
-    const int d = threadIdx.x % D, row = blockIdx.y * (256 / D) + threadIdx.x / D;
+    const int warp = threadIdx.x >> 5, w = warp & 3, row = blockIdx.y * 2 + (warp >> 2);
     const Span s = span_of(p, info.x);
-    if (row >= s.nq * p.group) return;
+    const bool there = row < s.nq * p.group;
     // pieces: the last of share c - 1, the first of shares c .. info.w
-    auto slot = [&](int q) { return (q < c ? 2LL * q + 1 : 2LL * q) * ROWS + row; };
-    const float* const ml = p.part + p.part_ml;
-    float top = -INFINITY;
-    for (int q = c - 1; q <= info.w; ++q) top = fmaxf(top, __ldcg(ml + slot(q) * 2));
-    float total = 0.f, sum = 0.f;
-#pragma unroll 4
-    for (int q = c - 1; q <= info.w; ++q) {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(ml + slot(q) * 2));
-        const float f = x.x == -INFINITY ? 1.f : ex2(x.x - top);
-        total += x.y * f;
-        sum += __ldcg(p.part + slot(q) * D + d) * f;
-    }
+    const int n = there ? info.w - c + 2 : 0, per = (n + W - 1) / W;
+    Joined<D> r = join_pieces<D>(p, n, w * per, min((w + 1) * per, n),
+                                 [&](int q) { return (q == 0 ? 2LL * c - 1 : 2LL * (c - 1 + q)) * ROWS + row; });
+    join_warps<D, W>(r, w, &others[warp >> 2][0][0]);
+    if (w > 0 || !there) return;
     const int i = p.by_group(row), h = info.y * p.group + row - i * p.group;
-    const long long at = (long long)(s.q0 + i) * p.heads + h;
-    p.out[at * D + d] = __float2bfloat16_rn(total == 0.f ? 0.f : sum / total);
-    if (p.lse && d == 0) p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+    write_joined<D>(p, r, (long long)(s.q0 + i) * p.heads + h);
 }
 
-// join the splits of one row: CTA (sequence, query, head), one thread per dimension
-// W: warps that share a row's splits (4 where rows are few, else 1)
+// the splits of each row (sequence, query, head); W: warps that share a row's splits (4 where rows are few, else 1)
 template <int D, int ROWS, int W> __global__ void __launch_bounds__(kAtThreads) k_kv_attention_join(const AtArgs p) {
-    constexpr int PER = D / 32, AHEAD = 8;  // dimensions of a lane, loads in flight
-    using Vec = std::conditional_t<PER == 4, float4, float2>;
     __shared__ float others[W][D + 1];
-    const int lane = threadIdx.x & 31, w = W == 1 ? 0 : threadIdx.x >> 5;
+    const int w = W == 1 ? 0 : threadIdx.x >> 5;
     pdl_wait_then_release();
     int id = W == 1 ? blockIdx.x * kAtWarps + (threadIdx.x >> 5) : blockIdx.x;
     const int h = id % p.heads;
@@ -695,63 +765,13 @@ template <int D, int ROWS, int W> __global__ void __launch_bounds__(kAtThreads) 
     const int n = (gr.hi - gr.lo + gr.per - 1) / gr.per;
     if (n <= 1) return;  // written by its split
     const long long first = (((long long)b * p.c.heads + head) * p.row_tiles + rt) * p.splits * ROWS + (row - r0);
-    const float2* const ml = reinterpret_cast<const float2*>(p.part + p.part_ml) + first;
-    const Vec* const part = reinterpret_cast<const Vec*>(p.part + first * D) + lane;
-    float top = -INFINITY;
-    for (int q = lane; q < n; q += 32) top = fmaxf(top, __ldcg(&ml[(long long)q * ROWS]).x);
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    float total = 0.f, sum[PER] = {};
-    const int per = (n + W - 1) / W, hi = min((w + 1) * per, n);  // this warp's splits: w per .. hi - 1
-    for (int q0 = w * per; q0 < hi; q0 += 32) {
-        float f = 0.f;
-        if (q0 + lane < hi) {
-            const float2 x = __ldcg(&ml[(long long)(q0 + lane) * ROWS]);
-            f = x.x == -INFINITY ? 1.f : ex2(x.x - top);
-            total += x.y * f;
-        }
-        const int m = min(32, hi - q0);
-        for (int q1 = 0; q1 < m; q1 += AHEAD) {
-            Vec x[AHEAD];
-#pragma unroll
-            for (int q = 0; q < AHEAD; ++q)
-                if (q1 + q < m) x[q] = __ldcg(part + (long long)(q0 + q1 + q) * (ROWS * 32));
-#pragma unroll
-            for (int q = 0; q < AHEAD; ++q) {
-                const float fq = __shfl_sync(0xFFFFFFFFu, f, (q1 + q) & 31);
-                if (q1 + q >= m) continue;
-                sum[0] += x[q].x * fq;
-                sum[1] += x[q].y * fq;
-                if constexpr (PER == 4) {
-                    sum[2] += x[q].z * fq;
-                    sum[3] += x[q].w * fq;
-                }
-            }
-        }
-    }
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
+    const int per = (n + W - 1) / W;
+    Joined<D> r = join_pieces<D>(p, n, w * per, min((w + 1) * per, n), [&](int q) { return first + (long long)q * ROWS; });
     if constexpr (W > 1) {
-#pragma unroll
-        for (int k = 0; k < PER; ++k) others[w][PER * lane + k] = sum[k];
-        if (lane == 0) others[w][D] = total;
-        __syncthreads();
+        join_warps<D, W>(r, w, &others[0][0]);
         if (w > 0) return;
-#pragma unroll
-        for (int v = 1; v < W; ++v) {
-            total += others[v][D];
-#pragma unroll
-            for (int k = 0; k < PER; ++k) sum[k] += others[v][PER * lane + k];
-        }
     }
-    const long long at = (long long)(s.q0 + i) * p.heads + h;
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    uint32_t out[PER / 2];
-#pragma unroll
-    for (int k = 0; k < PER / 2; ++k) out[k] = bf16x2(sum[2 * k] * inv, sum[2 * k + 1] * inv);
-    if constexpr (PER == 4) reinterpret_cast<uint2*>(p.out + at * D)[lane] = make_uint2(out[0], out[1]);
-    else reinterpret_cast<uint32_t*>(p.out + at * D)[lane] = out[0];
-    if (p.lse && lane == 0) p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+    write_joined<D>(p, r, (long long)(s.q0 + i) * p.heads + h);
 }
 
 // eights of rows per tile; more than 32 rows: the kernel that decodes a block of keys for 256 of them at once
@@ -782,17 +802,16 @@ Plan plan_of(const KvCache& c, long long batch, int max_q, int heads, long long 
         return p;
     }
     if (p.nq == kNqTiles) {
-        // one CTA per SM: the number of splits that fills whole waves best, with few waves
+        // one CTA per SM: the number of splits whose waves are over first; a CTA's start and end take about as long as four
+        // blocks of keys
         const long long blocks = (max_keys + 127) / 128;
-        long long most = blocks / kTileMinBlocks;
+        long long most = blocks / kTileMinBlocks, best = 0;
         if (most > kAtMaxSplits) most = kAtMaxSplits;
-        double best = 0;
         for (long long n = 1; n <= most || n == 1; ++n) {
-            const long long waves = (tiles * n + sms - 1) / sms;
+            const long long waves = (tiles * n + sms - 1) / sms, time = waves * (4 + (blocks + n - 1) / n);
             if (n > 1 && waves > 4) break;
-            const double fill = (double)(tiles * n) / (double)(waves * sms) - 0.02 * (double)waves;
-            if (n == 1 || fill > best) {
-                best = fill;
+            if (n == 1 || time < best) {
+                best = time;
                 p.splits = (int)n;
             }
         }
@@ -843,7 +862,7 @@ template <int D, int NQ> cudaError_t go(const AtArgs& a, const Plan& pl, int dev
     if (e != cudaSuccess || pl.pieces == 0 || pl.shares == 1) return e;
     cfg.dynamicSmemBytes = 0;
     if (pl.shares == 0) return join<D, 8 * NQ>(a, st);
-    cfg.gridDim = dim3((unsigned)(pl.shares - 1), (unsigned)((a.max_q * a.group + 256 / D - 1) / (256 / D)));
+    cfg.gridDim = dim3((unsigned)(pl.shares - 1), (unsigned)((a.max_q * a.group + 1) / 2));
     cfg.blockDim = dim3(256);
     return cudaLaunchKernelEx(&cfg, k_kv_attention_join_shares<D, NQ>, a);
 }

@@ -148,7 +148,7 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
 }
 
 // many rows of a sequence and key head: 256 at a time, keys in blocks of 128 (mxq_attention_tc.cu)
-constexpr int kTileRows = 256, kTileKeysShift = 7, kTileMinBlocks = 4;
+constexpr int kTileRows = 256, kTileKeysShift = 7, kTileMinBlocks = 1;
 cudaError_t launch_kv_attention_tiles(const AtArgs& a, long long tiles, int dev, cudaStream_t st);
 
 }  // namespace mxq
