@@ -44,6 +44,7 @@ constexpr int kAtWarps = 4, kAtThreads = 32 * kAtWarps;
 constexpr int kAtStages = 3;       // groups in a warp's ring (four: as fast, six: 146 us for 141 at 16 sequences of 24..32 thousand keys)
 constexpr int kAtMaxSplits = 256;
 constexpr long long kJoinRows = 2048;  // below, the warps of a CTA share the splits of a row (4096 rows of 9 splits: 92 us so, 85 with a warp each)
+constexpr int kEvenGroups = 8;     // groups that an equal share has at least, if there are fewer sequences
 constexpr int kAtMaxEven = 512;    // sequences whose shares are worked out by every CTA
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -559,6 +560,7 @@ template <int D, int NQ> __device__ __forceinline__ void attend_share(const AtAr
         if (lane >= d) incl += x;
     }
     __shared__ long long warp_total[kAtWarps];
+    __shared__ int warp_filled[kAtWarps];
     if (lane == 31) warp_total[warp] = incl;
     __syncthreads();
     long long at = incl - sum;
@@ -570,7 +572,15 @@ template <int D, int NQ> __device__ __forceinline__ void attend_share(const AtAr
         at += n[i];
     }
     if (t == kAtThreads - 1 && p.batch == kAtMaxEven) pre[kAtMaxEven] = at;
+    int filled = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) filled += n[i] > 0;
+    filled = __reduce_add_sync(0xFFFFFFFFu, filled);
+    if (lane == 0) warp_filled[warp] = filled;
     __syncthreads();
+    int some = 0;  // sequences with a key
+#pragma unroll
+    for (int w = 0; w < kAtWarps; ++w) some += warp_filled[w];
     // sequences without a key, and rows that nobody computes
     for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
         const bool none = pre[b + 1] == pre[b];
@@ -581,7 +591,10 @@ template <int D, int NQ> __device__ __forceinline__ void attend_share(const AtAr
         }
     }
     const long long total = pre[p.batch] * p.c.heads;
-    const long long shares = min((long long)gridDim.x, (total + kAtMinGroups - 1) / kAtMinGroups), c = blockIdx.x;
+    // kEvenGroups groups a share, but a share for each sequence and head with a key if the grid has them (a piece takes as
+    // long as several groups); never more shares than groups: each has one
+    const long long want = max((total + kEvenGroups - 1) / kEvenGroups, (long long)some * p.c.heads);
+    const long long shares = min((long long)gridDim.x, want), c = blockIdx.x;
     int4 info = make_int4(-1, 0, 0, 0);
     if (c < shares) {
         const long long end = total * (c + 1) / shares;
@@ -796,7 +809,7 @@ Plan plan_of(const KvCache& c, long long batch, int max_q, int heads, long long 
     const long long groups = (max_keys + 15) / 16, tiles = p.tiles > 0 ? p.tiles : 1;
     const long long places = (long long)sms * (p.nq == 4 ? 2 : p.nq == 2 ? 3 : 4);  // resident CTAs
     if (p.nq < 4 && batch > 1 && batch <= kAtMaxEven && groups > kAtMinGroups) {
-        const long long most = (tiles * groups + kAtMinGroups - 1) / kAtMinGroups;
+        const long long by_groups = (tiles * groups + kEvenGroups - 1) / kEvenGroups, most = by_groups > tiles ? by_groups : tiles;
         p.shares = (int)(most < places ? most : places);
         p.pieces = 2LL * p.shares;
         return p;

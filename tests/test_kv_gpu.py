@@ -318,6 +318,17 @@ def test_nan_blocks_reach_only_the_queries_that_see_them():
     assert torch.isnan(got[50:]).all() and not torch.isnan(got[:50]).any()
 
 
+@pytest.mark.parametrize("window", [1, 4, 17, 40])
+@pytest.mark.parametrize("lens", [[3000, 700], [1500, 0, 2, 900], [400] * 70])
+def test_batches_that_see_few_keys(lens, window):
+    page, d = 16, 128
+    pages = sum(-(-n // page) for n in lens) + 1
+    c = filled(2, pages, 2, page, d)
+    table = tables(lens, page, pages)
+    spoil_tails(c, table, lens)
+    check(rand(4, len(lens), 8, d).bfloat16(), c, table, lens, window=window)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_many_queries_of_empty_sequences_give_zeros(d):
     batch, news = 150, 40   # more CTAs than fit at a time; 160 rows each
