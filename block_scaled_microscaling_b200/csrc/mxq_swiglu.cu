@@ -6,9 +6,9 @@
 // one thread decodes the two blocks and computes, with s = sigmoid(g),
 //   dgate = dy * u * s * (1 + g * (1 - s)),   dup = dy * g * s.
 // Both are bound by memory: 8.06 bytes per value pair forward and 8.06 backward in bf16 (about 40 instructions
-// per pair fit beside that): 16384 x 9728 bf16 takes 217 us forward (5.9 TB/s) and 187 backward (6.9 TB/s). One thread per
-// block needs no shuffle for the block's maximum; a few rows are bound by that thread's latency instead (37 x 2560
-// fp32 5 us a pass). bf16 divides with the
+// per pair fit beside that): 16384 x 9728 bf16 takes 190 us forward (6.8 TB/s; 218 with the checkpoint after the products,
+// for want of warps) and 187 backward (6.9 TB/s). One thread per block needs no shuffle for the block's maximum; a few
+// rows are bound by that thread's latency instead (37 x 2560 fp32 4 us a pass). bf16 divides with the
 // hardware's approximate reciprocal (2 units in the last place, before the rounding to 2^-8); the exponential is the
 // accurate one for both types, since the approximate one loses |x| / 2^24 of its result.
 #include <cstdint>
@@ -48,33 +48,40 @@ __global__ void __launch_bounds__(kSwThreads) k_swiglu_forward(const void* __res
     pdl_wait_then_release();
     if (b >= nblocks) return;
     const long long at = block_at(b, kb, ld) * (long long)sizeof(T);
-    uint32_t g[Blk<T>::NW], u[Blk<T>::NW], o[Blk<T>::NW];
+    uint32_t g[Blk<T>::NW], u[Blk<T>::NW];
     load_block<T>(static_cast<const char*>(gate) + at, 0, g, in32);
     load_block<T>(static_cast<const char*>(up) + at, 0, u, in32);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float g0, g1, u0, u1;
-        upk(pair<T>(g, i), g0, g1);
-        upk(pair<T>(u, i), u0, u1);
-        const float y0 = g0 * sigmoid<T>(g0) * u0, y1 = g1 * sigmoid<T>(g1) * u1;
-        if constexpr (sizeof(T) == 4) {
-            o[2 * i] = __float_as_uint(y0);
-            o[2 * i + 1] = __float_as_uint(y1);
-        } else {
-            o[i] = bf16x2(y0, y1);
-        }
+    if (gc != nullptr) {  // a checkpoint is asked for; stored before the products, so that few registers are live at a time
+        uint32_t code[8];
+        uint32_t byte = scale_byte<F_E4M3>(block_amax<T>(g));
+        encode_block<F_E4M3, T>(g, byte, code);
+        store_payload<F_E4M3>(gc, b, code, codes32);
+        gs[b] = (uint8_t)byte;
+        byte = scale_byte<F_E4M3>(block_amax<T>(u));
+        encode_block<F_E4M3, T>(u, byte, code);
+        store_payload<F_E4M3>(uc, b, code, codes32);
+        us[b] = (uint8_t)byte;
     }
-    store_block<T>(out, b, o, out32);
-    if (gc == nullptr) return;  // no checkpoint asked for
-    uint32_t code[8];
-    uint32_t byte = scale_byte<F_E4M3>(block_amax<T>(g));
-    encode_block<F_E4M3, T>(g, byte, code);
-    store_payload<F_E4M3>(gc, b, code, codes32);
-    gs[b] = (uint8_t)byte;
-    byte = scale_byte<F_E4M3>(block_amax<T>(u));
-    encode_block<F_E4M3, T>(u, byte, code);
-    store_payload<F_E4M3>(uc, b, code, codes32);
-    us[b] = (uint8_t)byte;
+    char* const to = static_cast<char*>(out) + b * 32 * (long long)sizeof(T);
+#pragma unroll
+    for (int q = 0; q < Blk<T>::NW / 8; ++q) {
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 32 / (int)sizeof(T) / 2; ++j) {
+            const int i = q * (32 / (int)sizeof(T) / 2) + j;  // pair of values
+            float g0, g1, u0, u1;
+            upk(pair<T>(g, i), g0, g1);
+            upk(pair<T>(u, i), u0, u1);
+            const float y0 = g0 * sigmoid<T>(g0) * u0, y1 = g1 * sigmoid<T>(g1) * u1;
+            if constexpr (sizeof(T) == 4) {
+                o[2 * j] = __float_as_uint(y0);
+                o[2 * j + 1] = __float_as_uint(y1);
+            } else {
+                o[j] = bf16x2(y0, y1);
+            }
+        }
+        st32(to + 32 * q, o, out32);
+    }
 }
 
 template <typename T>
