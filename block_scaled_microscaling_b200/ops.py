@@ -14,8 +14,9 @@ As in mxq.py, the mxq_* functions take raw integers and return the status; the h
 torch, refuse tensors that the C calls could not read or write safely, launch on the current stream (or `stream`)
 and raise MXQError on a non-zero status. linear_ste and swiglu with their gradients, and plain calls of the others, go
 through the C++ module _ops (csrc/ops_torch.cpp), which does the same in a few microseconds and leaves every other case
-and the errors to the code here. The product's kernel bounds its waits: check=True synchronizes and raises
-if one ran out (else call check_device() before trusting the outputs).
+and the errors to the code here. The kernels of the product and of attention for many queries bound their waits:
+check=True (of matmul and linear) synchronizes and raises if one ran out; else call check_device() before trusting
+the outputs.
 """
 import ctypes
 import math
