@@ -181,18 +181,19 @@ struct Checkpoint {
     }
 };
 
-// values between rows if the leading dimensions of t are one dimension of rows, whose values are contiguous and whose
-// start and stride are 16-byte aligned; else 0
+// values between rows if the leading dimensions of t are one dimension of rows, which do not overlap (a broadcast
+// dimension has the stride 0), whose values are contiguous and whose start and stride are 16-byte aligned; else 0
 int64_t row_stride(const Tensor& t) {
     if (t.stride(-1) != 1) return 0;
-    int64_t ld = 0, n = 1;
+    int64_t ld = t.size(-1), n = 1;
+    bool one = true;  // no dimension of more than one row so far
     for (int64_t i = t.dim() - 2; i >= 0; --i) {
         if (t.size(i) == 1) continue;
-        if (ld == 0) ld = t.stride(i);
+        if (one) ld = t.stride(i);
         else if (t.stride(i) != ld * n) return 0;
+        one = false;
         n *= t.size(i);
     }
-    if (ld == 0) ld = t.size(-1);
     const bool aligned = ld * t.element_size() % 16 == 0 && reinterpret_cast<uintptr_t>(t.const_data_ptr()) % 16 == 0;
     return ld >= t.size(-1) && aligned ? ld : 0;
 }

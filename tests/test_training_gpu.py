@@ -237,3 +237,32 @@ def test_mlp_step_as_it_is_used(fmt):
         t.zero_()
     graph.replay()
     assert all(torch.equal(a, b) for a, b in zip(first, out))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("which", ["gate", "up", "both"])
+@pytest.mark.parametrize("base", [(1, 64), (1, 1, 64), (4, 1, 64), (1, 8, 64)])
+def test_swiglu_of_broadcast_inputs(base, which, dtype):
+    """Rows that share memory (strides of 0 in the last row dimension, in an outer one and in both): what a copy gives, with
+    its gradients, which sum over the broadcast rows."""
+    shape = (8, 64) if len(base) == 2 else (4, 8, 64)
+    rows = torch.Size(shape[:-1]).numel()
+    small = lambda seed: values(seed, torch.Size(base[:-1]).numel(), 64, dtype).view(base)  # noqa: E731
+    gate = small(1) if which != "up" else values(1, rows, 64, dtype).view(shape)
+    up = small(2) if which != "gate" else values(2, rows, 64, dtype).view(shape)
+    dy = values(3, rows, 64, dtype).view(shape)
+    views = [t.expand(shape).requires_grad_() for t in (gate, up)]
+    copies = [t.detach().contiguous().requires_grad_() for t in views]
+    y, want = ops.swiglu(*views), ops.swiglu(*copies)
+    assert torch.equal(y, want)
+    for got, exp in zip(torch.autograd.grad(y, views, dy), torch.autograd.grad(want, copies, dy)):
+        assert torch.equal(got, exp)
+    leaves = [gate.detach().requires_grad_(), up.detach().requires_grad_()]
+    sums = torch.autograd.grad(ops.swiglu(*(t.expand(shape) for t in leaves)), leaves, dy)
+    for got, leaf, per_row in zip(sums, leaves, torch.autograd.grad(ops.swiglu(*copies), copies, dy)):
+        assert torch.equal(got, per_row.sum_to_size(leaf.shape))
+
+
+def test_swiglu_of_a_broadcast_packed_input():
+    both = values(5, 4, 128).view(4, 1, 128)
+    assert torch.equal(ops.swiglu(both.expand(4, 8, 128)), ops.swiglu(both.expand(4, 8, 128).contiguous()))
