@@ -507,8 +507,8 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
             Ring at;
             lookup(0);
             for (int it = 0; it < n; ++it, at.next(kTcRaw)) {
-                if (it >= kTcRaw && !mbar_wait(raw_empty(at.s), at.phase ^ 1u, ab, err)) break;
-                __syncwarp();
+                // one verdict for the warp: the shuffles below need every lane
+                if (it >= kTcRaw && !__all_sync(0xFFFFFFFFu, mbar_wait(raw_empty(at.s), at.phase ^ 1u, ab, err))) break;
                 const uint32_t raw = sb + C::AT_RAW + (uint32_t)at.s * C::RAW;
                 if (pg >= p.c.pages) pg = -1;
                 uint32_t bits = 0;

@@ -250,3 +250,20 @@ def test_cache_helper_refusals():
                  lambda: ops.kv_attention(fake(2, 4, 64), c, i32(2, 4), i64(2))]:
         with pytest.raises(TypeError):
             call()
+
+
+def test_roles_with_warp_collectives_share_the_verdict_of_a_wait():
+    """A bounded wait may end differently for the lanes of a warp. In a role of the many-query attention kernel whose lanes
+    meet in shuffles or warp barriers, a lane that leaves alone would hang the others: the verdict has to be the warp's."""
+    src = open(os.path.join(ROOT, "block_scaled_microscaling_b200", "csrc", "mxq_attention_tc.cu")).read()
+    body = src[src.index("void __launch_bounds__(kTcThreads"):src.index("template <int D> cudaError_t go(")]
+    roles = re.split(r"(?=// ---- )", body)[1:]
+    assert len(roles) == 5
+    together = 0
+    for role in roles:
+        waits = len(re.findall(r"\bmbar_wait\(", role))
+        assert waits > 0
+        if re.search(r"__syncwarp|__shfl|__reduce|__any_sync", role):
+            together += 1
+            assert len(re.findall(r"__all_sync\(0xFFFFFFFFu, mbar_wait\(", role)) == waits, role.splitlines()[0]
+    assert together >= 3
