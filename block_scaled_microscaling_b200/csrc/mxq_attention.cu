@@ -212,6 +212,7 @@ template <int D, int NQ> __device__ __forceinline__ void attend(const AtArgs& p,
     // groups of which every row sees every key (in a page of the cache)
     const int pos_lo = s.len - s.n + i0, pos_hi = s.len - s.n + i1;
     const int whole_hi = min(s.len, pos_lo + 1) >> 4, whole_lo = p.window > 0 ? ((pos_hi - p.window) >> 4) + 1 : 0;
+    const KeyRange seen_by_some = keys_seen(p, s, i0, i1);
     const uint32_t ring = smem_u32(dsm) + warp * kAtStages * S::BYTES;
     int places = -1;            // lane j: place in the cache (in groups; -1: none) of the warp's group 32 * (issued / 32) + j
     int issued = 0;             // groups of this warp whose copies are issued
@@ -265,14 +266,14 @@ template <int D, int NQ> __device__ __forceinline__ void attend(const AtArgs& p,
             vs[3] = prmt(w.y, v_sel + 2);
         }
         const bool whole = in_page && grp < whole_hi && grp >= whole_lo;
-        if (!whole) {  // bytes of keys that nobody sees count as zeros
-            const int end = in_page ? s.len - key0 : 0;
+        if (!whole) {  // bytes of keys that no row of the tile sees count as zeros
+            const int end = in_page ? seen_by_some.hi - key0 : 0, begin = seen_by_some.lo - key0;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (kr + 2 * i >= end) ks[i] = 0;
+                if (kr + 2 * i >= end || kr + 2 * i < begin) ks[i] = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (4 * t + i >= end) vs[i] = 0;
+                if (4 * t + i >= end || 4 * t + i < begin) vs[i] = 0;
         }
         if (__any_sync(0xFFFFFFFFu, (int)max(ks[0], ks[1]) > klim || (int)max(max(vs[0], vs[1]), max(vs[2], vs[3])) > vlim)) {
             // raise the references where a block (NaN blocks aside) exceeds 2^13 of them
@@ -386,7 +387,7 @@ template <int D, int NQ> __device__ __forceinline__ void attend(const AtArgs& p,
                 e[n][k] = weight_exponent(sc[n][k], mk[n][k & 1], m[n][k & 1]);
                 if (!whole) {
                     const int key = key0 + kr + (k & 2);
-                    const bool seen = in_page && key < s.len && key <= pos[n][k & 1] && (p.window <= 0 || key > pos[n][k & 1] - p.window);
+                    const bool seen = in_page && key <= pos[n][k & 1] && (p.window <= 0 || key > pos[n][k & 1] - p.window);
                     if (!seen) e[n][k] = -INFINITY;
                 }
             }

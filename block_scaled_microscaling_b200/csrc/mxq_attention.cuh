@@ -70,16 +70,25 @@ __device__ __forceinline__ Span span_of(const AtArgs& p, int b) {
     s.len = (int)min((long long)max(__ldg(p.lens + b), 0), p.max_keys);
     return s;
 }
-// groups of 2^SHIFT keys that the queries i0 .. i1 see together, and groups per split (MIN at least)
+// the keys lo .. hi - 1 are those that at least one of the queries i0 .. i1 sees
+struct KeyRange {
+    int lo, hi;
+};
+__device__ __forceinline__ KeyRange keys_seen(const AtArgs& p, const Span& s, int i0, int i1) {
+    KeyRange k;
+    k.hi = min(s.len, max(s.len - s.n + i1 + 1, 0));
+    k.lo = p.window > 0 ? min(max(s.len - s.n + i0 - p.window + 1, 0), k.hi) : 0;
+    return k;
+}
+// their groups of 2^SHIFT keys, and groups per split (MIN at least)
 struct Groups {
     int lo, hi, per;
 };
 template <int SHIFT = 4, int MIN = kAtMinGroups> __device__ __forceinline__ Groups groups_of(const AtArgs& p, const Span& s, int i0, int i1) {
-    const int hi = min(s.len, max(s.len - s.n + i1 + 1, 0));
-    const int lo = p.window > 0 ? min(max(s.len - s.n + i0 - p.window + 1, 0), hi) : 0;
+    const KeyRange k = keys_seen(p, s, i0, i1);
     Groups g;
-    g.lo = lo >> SHIFT;
-    g.hi = (hi + (1 << SHIFT) - 1) >> SHIFT;
+    g.lo = k.lo >> SHIFT;
+    g.hi = (k.hi + (1 << SHIFT) - 1) >> SHIFT;
     const int n = g.hi - g.lo;
     g.per = max((n + p.splits - 1) / p.splits, MIN);
     return g;

@@ -162,7 +162,12 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
     const int rows = s.nq * p.group, r0 = rt * kTileRows;
     if (p.fill && rt == 0 && sp == 0) fill_rows<D>(p, s, b, head * p.group, p.group);
     Groups gr{0, 0, 1};
-    if (r0 < rows) gr = groups_of<kTileKeysShift, kTileMinBlocks>(p, s, p.by_group(r0), p.by_group(min(r0 + kTileRows, rows) - 1));
+    KeyRange some{0, 0};  // the keys that a row of the CTA sees: the bytes of others count as zeros
+    if (r0 < rows) {
+        const int i0 = p.by_group(r0), i1 = p.by_group(min(r0 + kTileRows, rows) - 1);
+        gr = groups_of<kTileKeysShift, kTileMinBlocks>(p, s, i0, i1);
+        some = keys_seen(p, s, i0, i1);
+    }
     const int first = gr.lo + sp * gr.per, n = max(min(first + gr.per, gr.hi) - first, 0);  // blocks of this CTA
     const bool alone = gr.hi - gr.lo <= gr.per;  // one split holds all keys
     const bool work = r0 < rows && (n > 0 || sp == 0), two = r0 + 128 < rows;  // two: the second tile has rows
@@ -396,7 +401,7 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
 #pragma unroll
                     for (int j = 0; j < C::SROW; ++j)
                         if (lds8(raw + C::RVS + d * C::SROW + j) == 0xFFu) bits |= 1u << j;
-                    if (key0 + d >= s.len || !((bi.pages >> (d >> 4)) & 1u)) bits = 0;
+                    if (key0 + d >= some.hi || !((bi.pages >> (d >> 4)) & 1u)) bits = 0;
                     nan_keys[it & 7][d] = (uint8_t)bits;
                 }
                 const int c0 = bi.kref - 15;
@@ -425,7 +430,7 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                 // V: keys 64 u + 8 kg .. + 7, eight dimensions of one 32-value block
                 const uint32_t raw = sb + C::AT_RAW + (uint32_t)at_v.s * C::RAW;
                 const int key0v = key0 - 128;
-                const bool some = pages_v != 0xFFu || key0v + 128 > s.len || nan_v;
+                const bool edge = pages_v != 0xFFu || key0v + 128 > some.hi || key0v < some.lo || nan_v;
                 const int c0 = vref_v - 15;
                 const uint32_t floor2 = (uint32_t)(c0 & 0xFFFF) * 0x10001u, minus2 = (uint32_t)(-c0 * 0x10001);
                 const int kg = lane & 7, dg = lane >> 3, blk = D == 128 ? w : w & 1;
@@ -448,11 +453,11 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
 #pragma unroll
                         for (int j = 0; j < 8; ++j) sw[j] = (y[j >> 1] >> (16 * (j & 1) + 8 * blk)) & 0xFFu;
                     }
-                    if (some) {
+                    if (edge) {
                         const bool in = (pages_v >> (k0 >> 4)) & 1u;
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            if (!in || key0v + k0 + j >= s.len || sw[j] == 0xFFu) sw[j] = 0;
+                            if (!in || key0v + k0 + j >= some.hi || key0v + k0 + j < some.lo || sw[j] == 0xFFu) sw[j] = 0;
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) sc[uu][j] = scale_pair(sw[2 * j] | (sw[2 * j + 1] << 16), floor2, minus2);
@@ -498,7 +503,7 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
             auto lookup = [&](int blk) {
                 const int key = (first + blk) * 128 + 16 * (c0 + lane);
                 pg = -1;
-                if (lane < 4 && blk < n && key < s.len) {
+                if (lane < 4 && blk < n && key < some.hi) {
                     const int at = p.by_page(key);
                     off = key - at * p.c.page;
                     pg = __ldg(p.table + b * p.table_stride + at);
@@ -547,7 +552,7 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                 const uint32_t raw = sb + C::AT_RAW + (uint32_t)at.s * C::RAW;
                 const int key0 = (first + it) * 128;
                 const uint32_t pages = there[it & 7][0] | there[it & 7][1];
-                const bool edge = pages != 0xFFu || key0 + 128 > s.len;
+                const bool edge = pages != 0xFFu || key0 + 128 > some.hi || key0 < some.lo;
                 constexpr int PER = 16 / C::SROW;  // keys of the lane's 16 bytes
                 const int mine = min(lane, 128 / PER - 1);
                 bool nan = false;
@@ -557,15 +562,15 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                     const uint4 y = lds128u(raw + (v ? C::RVS : C::RKS) + 16 * mine);
                     uint32_t x[4] = {y.x, y.y, y.z, y.w};
                     if (edge) {
-                        const int key = mine * PER;
-                        const bool in = (pages >> (key >> 4)) & 1u;
+                        const int key = key0 + mine * PER;
+                        const bool in = (pages >> (mine * PER >> 4)) & 1u;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             if constexpr (D == 128) {
-                                if (!in || key0 + key + i >= s.len) x[i] = 0;
-                            } else {
-                                if (!in || key0 + key + 2 * i >= s.len) x[i] = 0;
-                                else if (key0 + key + 2 * i + 1 >= s.len) x[i] &= 0xFFFFu;
+                                if (!in || key + i >= some.hi || key + i < some.lo) x[i] = 0;
+                            } else {  // two keys to a word
+                                if (!in || key + 2 * i >= some.hi || key + 2 * i < some.lo) x[i] &= 0xFFFF0000u;
+                                if (!in || key + 2 * i + 1 >= some.hi || key + 2 * i + 1 < some.lo) x[i] &= 0xFFFFu;
                             }
                         }
                     }

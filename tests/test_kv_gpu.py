@@ -318,6 +318,64 @@ def test_nan_blocks_reach_only_the_queries_that_see_them():
     assert torch.isnan(got[50:]).all() and not torch.isnan(got[:50]).any()
 
 
+def spoil(c, table, b, keys, scale):
+    """Every code of keys of sequence b, and their scales one byte (0xFE: 2^127; 0xFF: NaN)."""
+    for j in keys:
+        pg, off = int(table[b, j // c.page_size]), j % c.page_size
+        for t, x in ((c.k_codes, 0x77), (c.k_scales, scale), (c.v_codes, 0x77), (c.v_scales, scale)):
+            t[pg, :, off] = x
+
+
+@pytest.mark.parametrize("scale", [0xFE, 0xFF])
+@pytest.mark.parametrize("window", [1, 5, 37, 130, 300])
+@pytest.mark.parametrize("news,group,d", [([1, 1], 4, 128), ([3, 2], 4, 64), ([8, 5], 4, 128), ([40, 3], 4, 128), ([100, 70], 2, 64)])
+def test_bytes_in_front_of_the_window_do_not_count(news, group, d, window, scale):
+    """Keys in front of every query's window hold the largest scales, or NaN: few queries, queries in shares, row tiles."""
+    page = 32
+    for lens in ([310, 145], [700, 333]):
+        pages = sum(-(-n // page) for n in lens) + 1
+        c = filled(3, pages, 2, page, d)
+        table = tables(lens, page, pages)
+        for b, (n, new) in enumerate(zip(lens, news)):
+            spoil(c, table, b, range(max(0, n - new - window + 1)), scale)
+        spoil_tails(c, table, lens)
+        starts = [0, news[0], sum(news)]
+        check(rand(9, sum(news), 2 * group, d).bfloat16(), c, table, lens, starts, window=window)
+        one = [0, news[0]]                                      # a sequence alone
+        check(rand(9, news[0], 2 * group, d).bfloat16(), c, table[:1], lens[:1], one, window=window)
+
+
+@pytest.mark.parametrize("scale", [0xFE, 0xFF])
+@pytest.mark.parametrize("d,group,news", [(128, 4, 200), (64, 8, 70), (64, 1, 600)])
+def test_bytes_behind_the_keys_of_a_row_tile_do_not_count(d, group, news, scale):
+    """The last key, which the last query alone sees, holds the largest scales: queries of other row tiles (256 rows each) keep
+    their results."""
+    lens, page = [news + 50], 16
+    c = filled(3, -(-lens[0] // page), 2, page, d)
+    table = tables(lens, page, c.pages)
+    spoil(c, table, 0, [lens[0] - 1], scale)
+    q = rand(9, news, 2 * group, d).bfloat16()
+    got = ops.kv_attention(q, c, table, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    out, _, tol, _ = reference(q, c, table, lens, [0, news])
+    others = (news * group - 1) // 256 * 256 // group           # queries that share no tile with the last
+    assert others > 0
+    assert ((got.double() - out).abs() <= tol + out.abs() * 2.0 ** -8)[:others].all()
+
+
+@pytest.mark.parametrize("group", [4, 16])
+def test_bytes_behind_the_queries_that_are_computed_do_not_count(group):
+    """Queries beyond max_q are left out, and the keys that they alone see do not count."""
+    lens, page, max_q = [90], 16, 3
+    c = filled(3, 6, 2, page, 128)
+    table = tables(lens, page, 6)
+    spoil(c, table, 0, range(83, 90), 0xFE)                       # queries stand at 80 .. 89
+    q = rand(9, 10, 2 * group, 128).bfloat16()
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    got = ops.kv_attention(q, c, table, dev(lens), q_starts=dev([0, 10]), max_q=max_q)
+    out, _, tol, _ = reference(q, c, table, lens, [0, 10])
+    assert ((got.double() - out).abs() <= tol + out.abs() * 2.0 ** -8)[:max_q].all()
+
+
 @pytest.mark.parametrize("window", [1, 4, 17, 40])
 @pytest.mark.parametrize("lens", [[3000, 700], [1500, 0, 2, 900], [400] * 70])
 def test_batches_that_see_few_keys(lens, window):
