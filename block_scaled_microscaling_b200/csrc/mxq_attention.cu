@@ -137,7 +137,7 @@ template <int D, int NQ> __device__ __forceinline__ void attend(const AtArgs& p,
     uint32_t qf[QS ? 1 : NQ][STEPS][2];
     uint2* const qsm = reinterpret_cast<uint2*>(reinterpret_cast<char*>(dsm) + kAtWarps * kAtStages * S::BYTES);
     float mul[NQ][2];  // per column of the score tiles (rows 2t, 2t + 1): scale * log2(e) * 2^e
-    int pos[NQ][2];    // last key that the row sees (-1: no row)
+    int pos[NQ][2];    // last key that the row sees (-1: no row, or none; never less, so that pos - window is an int)
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
         const int r = r0 + 8 * n + g;
@@ -183,7 +183,7 @@ template <int D, int NQ> __device__ __forceinline__ void attend(const AtArgs& p,
         for (int k = 0; k < 2; ++k) {
             const int col = 2 * t + k, rr = r0 + 8 * n + col;
             mul[n][k] = p.scale * pow2i(__shfl_sync(0xFFFFFFFFu, e, 4 * col));
-            pos[n][k] = rr < rows ? s.len - s.n + p.by_group(rr) : -1;
+            pos[n][k] = rr < rows ? max(s.len - s.n + p.by_group(rr), -1) : -1;
         }
     }
     if constexpr (QS) __syncthreads();
@@ -211,7 +211,7 @@ template <int D, int NQ> __device__ __forceinline__ void attend(const AtArgs& p,
 
     // groups of which every row sees every key (in a page of the cache)
     const int pos_lo = s.len - s.n + i0, pos_hi = s.len - s.n + i1;
-    const int whole_hi = min(s.len, pos_lo + 1) >> 4, whole_lo = p.window > 0 ? ((pos_hi - p.window) >> 4) + 1 : 0;
+    const int whole_hi = min(s.len, pos_lo + 1) >> 4, whole_lo = p.window > 0 ? ((max(pos_hi, -1) - p.window) >> 4) + 1 : 0;
     const KeyRange seen_by_some = keys_seen(p, s, i0, i1);
     const uint32_t ring = smem_u32(dsm) + warp * kAtStages * S::BYTES;
     int places = -1;            // lane j: place in the cache (in groups; -1: none) of the warp's group 32 * (issued / 32) + j

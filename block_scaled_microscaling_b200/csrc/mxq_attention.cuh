@@ -77,7 +77,8 @@ struct KeyRange {
 __device__ __forceinline__ KeyRange keys_seen(const AtArgs& p, const Span& s, int i0, int i1) {
     KeyRange k;
     k.hi = min(s.len, max(s.len - s.n + i1 + 1, 0));
-    k.lo = p.window > 0 ? min(max(s.len - s.n + i0 - p.window + 1, 0), k.hi) : 0;
+    // 64 bits: the first query may stand far before the first key, and the window may be any int
+    k.lo = p.window > 0 ? (int)min(max((long long)(s.len - s.n + i0 + 1) - p.window, 0LL), (long long)k.hi) : 0;
     return k;
 }
 // their groups of 2^SHIFT keys, and groups per split (MIN at least)

@@ -178,7 +178,7 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
         if (work && (x == 0 || two)) {
             // ---- softmax: thread's row r0 + 128 x + row ----
             const int r = r0 + 128 * x + row, i = p.by_group(min(r, rows - 1)), h = head * p.group + (min(r, rows - 1) - i * p.group);
-            const int pos = r < rows ? s.len - s.n + i : -1;
+            const int pos = r < rows ? max(s.len - s.n + i, -1) : -1;  // (-1 at least, so that pos - window is an int)
             const int see_hi = min(pos + 1, s.len), see_lo = p.window > 0 ? pos - p.window + 1 : 0;  // keys see_lo .. see_hi - 1
             const uint32_t ts = tm + ((uint32_t)(quad * 32) << 16) + kColS + 128 * x, to = ts + kColO - kColS;
             constexpr int LANES = D / 8, RPI = 32 / LANES;  // lanes that read or write a row, rows at a time

@@ -478,6 +478,7 @@ def kv_attention(q, cache, block_table, seq_lens, q_starts=None, max_q=None, sca
             raise ValueError("max_q < 0")
     if window < 0:
         raise ValueError("window < 0")
+    window = min(window, 2 ** 31 - 1)  # a sequence has fewer keys: each query sees all of them
     most = block_table.shape[1] * cache.page_size
     max_keys = most if max_keys is None else min(max_keys, most)
     if max_keys < 0:

@@ -540,3 +540,17 @@ def test_decoding_as_it_is_used():
     assert ((got - out).abs() <= tol + out.abs() * 2.0 ** -8).all()
     assert all(torch.equal(a, b) for a, b in zip(state(c), state(whole)))
     assert want.shape == q.shape
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 200, 2 ** 31, 2 ** 32 + 100])
+@pytest.mark.parametrize("lens,news,group", [([5], [8], 4), ([40], [43], 4), ([256], [260], 4), ([40], [43], 1), ([40, 3], [43, 6], 1),
+                                             ([20, 200], [23, 2], 1), ([3, 2], [6, 6], 2), ([3000, 0, 6], [5, 2, 9], 1)])
+def test_a_window_beyond_every_key_is_none(lens, news, group, window):
+    """More queries than keys: the first ones stand before the first key, by up to their number."""
+    page = 16
+    c = filled(3, 256, 2, page, 64)
+    table = tables(lens, page, 256)
+    starts = [sum(news[:i]) for i in range(len(news) + 1)]
+    q = rand(9, sum(news), 2 * group, 64).bfloat16()
+    got = check(q, c, table, lens, starts, window=window)
+    assert torch.equal(got, check(q, c, table, lens, starts))
