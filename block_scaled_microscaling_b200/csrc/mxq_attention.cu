@@ -792,6 +792,26 @@ template <int D, int ROWS, int W> __global__ void __launch_bounds__(kAtThreads) 
 constexpr int kNqTiles = kTileRows / 8;
 int nq_of(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : kNqTiles; }
 
+// Splits of many-query tiles: those whose waves are over first; a CTA's start and end take about as long as kTileEnds
+// blocks of keys.
+constexpr long long kTileWaves = 4, kTileEnds = 4;
+// No number of blocks up to `blocks` gets more splits than this. In w waves there are at most c = w sms / tiles splits,
+// which end after w (ends + b / c) or later; in v < w waves, d = v sms / tiles splits end before v (ends + 1 + b / d). So w
+// can win at b only if the first is below the second, and since v (ends + 1) <= w ends, then also at every larger b.
+long long most_splits(long long tiles, long long blocks, int sms) {
+    long long most = 1;
+    for (long long w = 1; w <= kTileWaves; ++w) {
+        const long long c = w * sms / tiles;
+        bool wins = c > most;
+        for (long long v = 1; v < w && wins; ++v) {
+            const long long d = v * sms / tiles;
+            wins = d == 0 || w * (kTileEnds * c + blocks) * d < v * ((kTileEnds + 1) * d + blocks) * c;
+        }
+        if (wins) most = c;
+    }
+    return most;
+}
+
 struct Plan {
     int nq, row_tiles, splits, shares;  // shares > 0: equal shares instead of splits
     long long tiles, pieces;            // places for partial sums
@@ -800,7 +820,8 @@ struct Plan {
 // keys: 145 us, 156 with splits). Otherwise, and for one sequence, where working out the shares only takes time (4000
 // keys: 14.4 us against 20.2), the keys in splits of at least kAtMinGroups groups of 16 keys for one wave of CTAs, or of
 // 32 groups or more for about two.
-Plan plan_of(const KvCache& c, long long batch, int max_q, int heads, long long max_keys, int sms) {
+// at_most: the workspace that any smaller max_keys needs too.
+Plan plan_of(const KvCache& c, long long batch, int max_q, int heads, long long max_keys, int sms, bool at_most = false) {
     Plan p{};
     const long long rows = (long long)max_q * (heads / c.heads);
     p.nq = nq_of(rows);
@@ -816,14 +837,19 @@ Plan plan_of(const KvCache& c, long long batch, int max_q, int heads, long long 
         return p;
     }
     if (p.nq == kNqTiles) {
-        // one CTA per SM: the number of splits whose waves are over first; a CTA's start and end take about as long as four
-        // blocks of keys
+        // one CTA per SM
         const long long blocks = (max_keys + 127) / 128;
         long long most = blocks / kTileMinBlocks, best = 0;
         if (most > kAtMaxSplits) most = kAtMaxSplits;
+        if (at_most) {
+            p.splits = (int)most_splits(tiles, blocks, sms);
+            if (p.splits > most) p.splits = most > 1 ? (int)most : 1;
+            p.pieces = p.splits > 1 ? p.tiles * p.splits : 0;
+            return p;
+        }
         for (long long n = 1; n <= most || n == 1; ++n) {
-            const long long waves = (tiles * n + sms - 1) / sms, time = waves * (4 + (blocks + n - 1) / n);
-            if (n > 1 && waves > 4) break;
+            const long long waves = (tiles * n + sms - 1) / sms, time = waves * (kTileEnds + (blocks + n - 1) / n);
+            if (n > 1 && waves > kTileWaves) break;
             if (n == 1 || time < best) {
                 best = time;
                 p.splits = (int)n;
@@ -897,10 +923,10 @@ int sm_count(int dev) {
 
 }  // namespace
 
-long long kv_attention_workspace(const KvCache& c, long long batch, int max_q, int heads, long long max_keys) {
+long long kv_attention_workspace(const KvCache& c, long long batch, int max_q, int heads, long long max_keys, bool at_most) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
-    const Plan p = plan_of(c, batch, max_q, heads, max_keys, sm_count(dev));
+    const Plan p = plan_of(c, batch, max_q, heads, max_keys, sm_count(dev), at_most);
     return p.pieces * 8 * p.nq * (c.db * 32 + 2) * 4 + p.shares * (long long)sizeof(int4);
 }
 

@@ -140,7 +140,8 @@ struct KvAttention {
     float* lse;
     void* workspace;
 };
-long long kv_attention_workspace(const KvCache& c, long long batch, int max_q, int heads, long long max_keys);
+// at_most: enough for any smaller max_keys too
+long long kv_attention_workspace(const KvCache& c, long long batch, int max_q, int heads, long long max_keys, bool at_most);
 cudaError_t launch_kv_attention(const KvAttention& x, cudaStream_t st);
 
 }  // namespace mxq

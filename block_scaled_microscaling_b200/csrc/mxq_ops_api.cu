@@ -11,6 +11,8 @@
 namespace {
 
 constexpr int64_t kMaxInt = 0x7FFFFFFF;
+// keys of a sequence: the kernels step over blocks of 128 in 32 bits, some blocks past the last
+constexpr int64_t kMaxKeys = kMaxInt - 511;
 
 bool product_format(mxq_format f) { return f == MXQ_MXFP4_E2M1 || f == MXQ_MXFP8_E4M3; }
 
@@ -251,10 +253,11 @@ mxq_status mxq_kv_read(const mxq_kv_cache* cache, const int64_t* slots, int64_t 
 size_t mxq_kv_attention_workspace_bytes(const mxq_kv_cache* cache, int64_t batch, int64_t q_rows, int32_t max_q,
                                         int32_t q_heads, int64_t max_keys) {
     if (check_cache(cache) != MXQ_OK || batch <= 0 || q_rows <= 0 || max_q <= 0 || q_heads <= 0 ||
-        q_heads % cache->kv_heads != 0 || max_keys <= 0 || batch > kMaxInt || max_keys > kMaxInt)
+        q_heads % cache->kv_heads != 0 || max_keys <= 0 || batch > kMaxInt)
         return 0;
     if (max_q > q_rows) max_q = (int32_t)q_rows;
-    return (size_t)mxq::kv_attention_workspace(cache_of(cache), batch, max_q, q_heads, max_keys);
+    if (max_keys > kMaxKeys) max_keys = kMaxKeys;
+    return (size_t)mxq::kv_attention_workspace(cache_of(cache), batch, max_q, q_heads, max_keys, true);
 }
 
 mxq_status mxq_kv_attention(const mxq_kv_cache* cache, const void* q, int64_t q_rows, int64_t q_row_stride,
@@ -280,13 +283,13 @@ mxq_status mxq_kv_attention(const mxq_kv_cache* cache, const void* q, int64_t q_
     MXQ_TRY(check_ptr(seq_lens, 4));
     const int64_t cap = table_stride > kMaxInt / cache->page_size ? kMaxInt : table_stride * cache->page_size;
     if (max_keys > cap) max_keys = cap;
-    if (max_keys > kMaxInt - 64) max_keys = kMaxInt - 64;
+    if (max_keys > kMaxKeys) max_keys = kMaxKeys;
     if (max_keys > 0) MXQ_TRY(check_ptr(block_table, 4));
     MXQ_TRY(check_cache_memory(cache));
     if (max_q > q_rows) max_q = (int32_t)q_rows;  // no sequence has more
     mxq::KvAttention x{};
     x.c = cache_of(cache);
-    const size_t need = (size_t)mxq::kv_attention_workspace(x.c, batch, max_q, q_heads, max_keys);
+    const size_t need = (size_t)mxq::kv_attention_workspace(x.c, batch, max_q, q_heads, max_keys, false);
     if (need > 0) {
         if (workspace_bytes < need) return MXQ_ERR_INVALID_ARG;
         MXQ_TRY(check_ptr(workspace, 16));

@@ -161,7 +161,9 @@ MXQ_API mxq_status mxq_kv_read(const mxq_kv_cache* cache, const int64_t* slots, 
  *          are cut to it); at most table_stride * page_size counts. It sets how
  *          the keys are split over CTAs.
  *   workspace  mxq_kv_attention_workspace_bytes(...) bytes (may be 0: then NULL),
- *          16-byte aligned, used by this call alone until it has finished.
+ *          16-byte aligned, used by this call alone until it has finished. What
+ *          a max_keys asks for is enough for every smaller one, and for tables
+ *          of any width.
  * Keys and values are decoded to half precision (f16) exactly up to a power of
  * two that up to 256 rows (query x head of a key head) share: a block more than
  * 2^20 below the largest that one of these rows sees may lose bits or count as

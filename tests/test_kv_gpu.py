@@ -554,3 +554,24 @@ def test_a_window_beyond_every_key_is_none(lens, news, group, window):
     q = rand(9, sum(news), 2 * group, 64).bfloat16()
     got = check(q, c, table, lens, starts, window=window)
     assert torch.equal(got, check(q, c, table, lens, starts))
+
+
+@pytest.mark.parametrize("kv,group,batch,queries", [(2, 4, 1, 64), (8, 4, 1, 64), (3, 4, 3, 80), (2, 4, 1, 1), (2, 4, 3, 2), (1, 16, 1, 2)])
+def test_a_workspace_serves_fewer_keys_and_narrower_tables(kv, group, batch, queries):
+    """Asked for 2432 and for 6000 keys, used with fewer, and with a table that holds fewer."""
+    page, d, width = 16, 64, 375
+    c = filled(3, 40, kv, page, d)
+    table = torch.randint(0, 40, (batch, width), generator=torch.Generator().manual_seed(1)).int().cuda()
+    rows, heads = batch * queries, kv * group
+    q = rand(1, rows, heads, d).bfloat16()
+    lens = torch.full((batch,), 1 << 20, dtype=torch.int32, device="cuda")
+    st = torch.cuda.current_stream().cuda_stream
+    for asked in (2432, 6000):
+        n = ops.mxq_kv_attention_workspace_bytes(c._raw(), batch, rows, queries, heads, asked)
+        ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+        for keys, w in [(asked, width), (asked, asked // page - 8), (asked - 128, width), (asked, 57), (1000, width), (300, width), (128, width), (7, width)]:
+            t = table[:, :w].contiguous()
+            out = torch.empty_like(q)
+            assert ops.mxq_kv_attention(c._raw(), q.data_ptr(), rows, heads * d, d, heads, batch, None, queries, lens.data_ptr(), keys,
+                                        t.data_ptr(), w, d ** -0.5, 0, 0, out.data_ptr(), None, ws.data_ptr() if n else None, n, st) == 0
+            assert torch.equal(out, ops.kv_attention(q, c, t, lens, max_keys=keys))

@@ -267,3 +267,16 @@ def test_roles_with_warp_collectives_share_the_verdict_of_a_wait():
             together += 1
             assert len(re.findall(r"__all_sync\(0xFFFFFFFFu, mbar_wait\(", role)) == waits, role.splitlines()[0]
     assert together >= 3
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_workspace_for_many_keys_is_enough_for_fewer(dim):
+    """The size never falls as max_keys grows, whatever the form that the call takes, and has no end at 2^31."""
+    ws = ops.mxq_kv_attention_workspace_bytes
+    for heads in (1, 2, 8):
+        c = cache(pages=1 << 20, heads=heads, dim=dim)
+        for group, batch, queries in [(4, 1, 128), (4, 1, 64), (4, 3, 40), (8, 9, 16), (1, 1, 300), (4, 1, 1), (4, 2, 1), (4, 600, 1), (16, 1, 2), (1, 5, 7)]:
+            sizes = [ws(c, batch, batch * queries, queries, heads * group, 16 * k)
+                     for k in (*range(1, 600, 3), 1000, 5000, 40000, 1 << 20, 1 << 26, (1 << 27) - 1, 1 << 27, 1 << 28, 1 << 50)]
+            assert sizes == sorted(sizes), (heads, group, batch, queries)
+            assert sizes[-1] == sizes[-4]
