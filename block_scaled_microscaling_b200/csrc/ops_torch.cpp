@@ -283,8 +283,8 @@ std::optional<Cache> cache(const Tensor& kc, const Tensor& ks, const Tensor& vc,
     for (const Tensor* t : {&kc, &ks, &vc, &vs})
         if (!bytes(*t) || t->dim() != 4) return std::nullopt;
     const auto s = kc.sizes(), e = ks.sizes();
-    if (vc.sizes() != s || vs.sizes() != e || e[0] != s[0] || e[1] != s[1] || e[2] != s[2] || e[3] != s[3] / 16 || s[1] > 65536 ||
-        s[2] > 65536 || s[3] > 65536)
+    if (vc.sizes() != s || vs.sizes() != e || e[0] != s[0] || e[1] != s[1] || e[2] != s[2] || e[3] != s[3] / 16 || s[1] < 1 ||
+        s[2] < 1 || s[3] < 16 || s[1] > 65536 || s[2] > 65536 || s[3] > 65536)
         return std::nullopt;
     Cache x{kc, ks, vc, vs, {}};
     x.c.pages = s[0];

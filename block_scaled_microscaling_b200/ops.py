@@ -355,6 +355,8 @@ class KVCache:
             return
         if len(shape) != 4:
             raise ValueError("codes must be [pages, kv_heads, page_size, head_dim / 2]")
+        if min(shape[1:3]) < 1 or shape[3] < 16:
+            raise ValueError(f"a cache needs heads, rows in a page and blocks of 32 dimensions, got codes {tuple(shape)}")
         self.pages, self.kv_heads, self.page_size, self.head_dim = *shape[:3], shape[3] * 2
         want = {"codes": tuple(shape), "scales": (*shape[:3], shape[3] // 16)}
         for t, what in ((k_codes, "k_codes"), (k_scales, "k_scales"), (v_codes, "v_codes"), (v_scales, "v_scales")):

@@ -575,3 +575,12 @@ def test_a_workspace_serves_fewer_keys_and_narrower_tables(kv, group, batch, que
             assert ops.mxq_kv_attention(c._raw(), q.data_ptr(), rows, heads * d, d, heads, batch, None, queries, lens.data_ptr(), keys,
                                         t.data_ptr(), w, d ** -0.5, 0, 0, out.data_ptr(), None, ws.data_ptr() if n else None, n, st) == 0
             assert torch.equal(out, ops.kv_attention(q, c, t, lens, max_keys=keys))
+
+
+@pytest.mark.parametrize("heads,page,dim", [(0, 16, 64), (2, 0, 64), (2, 16, 0)])
+def test_a_cache_without_heads_rows_or_dimensions_is_refused(heads, page, dim):
+    with pytest.raises(ValueError, match="a cache needs"):
+        ops.KVCache.empty(4, heads, page, dim)
+    c = ops.KVCache.empty(0, 2, 16, 64)      # no pages: nothing to see
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    assert (ops.kv_attention(rand(1, 3, 4, 64).bfloat16(), c, i32(3, 2), i32(3) + 5) == 0).all()

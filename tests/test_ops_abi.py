@@ -280,3 +280,10 @@ def test_a_workspace_for_many_keys_is_enough_for_fewer(dim):
                      for k in (*range(1, 600, 3), 1000, 5000, 40000, 1 << 20, 1 << 26, (1 << 27) - 1, 1 << 27, 1 << 28, 1 << 50)]
             assert sizes == sorted(sizes), (heads, group, batch, queries)
             assert sizes[-1] == sizes[-4]
+
+
+@pytest.mark.parametrize("heads,page,dim", [(0, 16, 64), (2, 0, 64), (2, 16, 0), (2, 16, 16)])
+def test_a_cache_without_heads_rows_or_dimensions_is_refused(heads, page, dim):
+    with pytest.raises(ValueError, match="a cache needs"):
+        fake_cache(heads=heads, page=page, dim=dim)
+    assert fake_cache(pages=0).pages == 0
