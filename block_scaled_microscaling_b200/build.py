@@ -43,7 +43,7 @@ def _stale():
 
 def build_ops(force=False):
     """_ops.so (ops_torch.cpp against the installed torch and libmxq.so)."""
-    if not force and not _older(OPS, [OPS_SRC] + glob.glob(os.path.join(ROOT, "include", "*.h"))):
+    if not force and not _older(OPS, [OPS_SRC, __file__] + glob.glob(os.path.join(ROOT, "include", "*.h"))):
         return OPS
     import sysconfig
 
@@ -56,7 +56,10 @@ def build_ops(force=False):
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-DTORCH_API_INCLUDE_EXTENSION_H",
            *(a for i in inc for a in ("-isystem", i)), OPS_SRC, "-o", OPS + ".tmp", "-L", HERE, "-l:libmxq.so",
-           "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda"]
+           "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda",
+           # torch's own C++ library and no other: a compiler that has only the static one would put a second copy into
+           # the process, where the first exception with a number in its message ends it
+           "-nostdlib++", "-l:libstdc++.so.6"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)

@@ -287,3 +287,13 @@ def test_a_cache_without_heads_rows_or_dimensions_is_refused(heads, page, dim):
     with pytest.raises(ValueError, match="a cache needs"):
         fake_cache(heads=heads, page=page, dim=dim)
     assert fake_cache(pages=0).pages == 0
+
+
+def test_the_torch_module_shares_the_cpp_library():
+    """A second C++ library linked into the module (a compiler with the static one alone) ended the process at the first
+    exception."""
+    path = os.path.join(os.path.dirname(mxq.LIB_PATH), "_ops.so")
+    needed = subprocess.run(["readelf", "-d", path], capture_output=True, text=True, check=True).stdout
+    assert "[libstdc++.so.6]" in needed
+    own = subprocess.run(["nm", "-D", "--defined-only", path], capture_output=True, text=True, check=True).stdout
+    assert "_ZNSo" not in own and "St6locale" not in own      # streams, locales

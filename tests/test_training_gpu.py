@@ -266,3 +266,16 @@ def test_swiglu_of_broadcast_inputs(base, which, dtype):
 def test_swiglu_of_a_broadcast_packed_input():
     both = values(5, 4, 128).view(4, 1, 128)
     assert torch.equal(ops.swiglu(both.expand(4, 8, 128)), ops.swiglu(both.expand(4, 8, 128).contiguous()))
+
+
+@pytest.mark.parametrize("layer", ["linear_ste", "swiglu"])
+def test_a_refusal_in_the_backward_pass_is_an_exception(layer):
+    """A checkpoint that comes back in host memory is refused by the C entry point."""
+    x, w = values(1, 40, 64).requires_grad_(), values(2, 96, 64)
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t, lambda t: t.cpu()):
+        y = ops.linear_ste(x, w) if layer == "linear_ste" else ops.swiglu(x)
+    with pytest.raises(RuntimeError, match="mxq_.*status 1"):
+        torch.autograd.grad(y, x, torch.ones_like(y))
+    torch.cuda.synchronize()
+    y = ops.swiglu(x)                          # and the next call works
+    assert torch.autograd.grad(y, x, torch.ones_like(y))[0].shape == x.shape
