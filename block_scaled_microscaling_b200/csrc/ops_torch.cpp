@@ -30,6 +30,12 @@ mxq_dtype dtype_of(const Tensor& t) { return t.scalar_type() == at::kFloat ? MXQ
 mxq_stream stream_of(const Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.device().index()).stream(); }
 int64_t payload(int fmt) { return fmt == MXQ_MXFP4_E2M1 ? 16 : 32; }
 bool product_format(int fmt) { return fmt == MXQ_MXFP4_E2M1 || fmt == MXQ_MXFP8_E4M3; }
+// t as the C entry points read it: contiguous, on a 16-byte boundary (a slice, such as a gradient that cat() hands back, may
+// begin anywhere)
+Tensor dense(const Tensor& t) {
+    const Tensor c = t.contiguous();
+    return reinterpret_cast<uintptr_t>(c.const_data_ptr()) % 16 == 0 ? c : c.clone();
+}
 Tensor scratch(int64_t n, const Tensor& like) { return at::empty({n}, like.options().dtype(at::kByte)); }
 
 void ok(mxq_status s, const char* what) {
@@ -103,7 +109,7 @@ struct LinearSTE : torch::autograd::Function<LinearSTE> {
         // the checkpoint is the operand of the weight's gradient: x rounded along the tokens
         if (need_dw) kept = scratch(operand_bytes(MXQ_MXFP8_E4M3, k, m32), x);
         if (m > 0) {
-            const Tensor x2 = x.reshape({m, k}).contiguous(), w = weight.contiguous();
+            const Tensor x2 = dense(x.reshape({m, k})), w = dense(weight);
             Tensor buf = scratch(operand_bytes((int)fmt, m, k) + operand_bytes((int)fmt, n, k), x);
             const Operand a = operand(buf, 0, (int)fmt, m, k), b = operand(buf, a.end, (int)fmt, n, k);
             quantize(x2, a, (int)fmt, need_dw ? operand(kept, 0, MXQ_MXFP8_E4M3, k, m32) : Operand(), MXQ_MXFP8_E4M3);
@@ -125,7 +131,7 @@ struct LinearSTE : torch::autograd::Function<LinearSTE> {
         {
             at::NoGradGuard no_grad;
             const int64_t m = grads[0].numel() / n, m32 = (m + 31) / 32 * 32;
-            const Tensor g = grads[0].reshape({m, n}).contiguous();
+            const Tensor g = dense(grads[0].reshape({m, n}));
             constexpr int f = MXQ_MXFP8_E4M3;
             if (m == 0) {  // no tokens
                 if (weight.defined()) dx = at::empty(shape, g.options().dtype((at::ScalarType)types[0]));
@@ -143,7 +149,7 @@ struct LinearSTE : torch::autograd::Function<LinearSTE> {
             if (kept.defined()) col = operand(buf, wt.end, f, n, m32);
             if (weight.defined() || kept.defined()) quantize(g, row, f, col, f);
             if (weight.defined()) {
-                quantize(weight.contiguous(), Operand(), f, wt, f);
+                quantize(dense(weight), Operand(), f, wt, f);
                 dx = at::empty(shape, g.options().dtype((at::ScalarType)types[0]));
                 product(row, wt, f, m, k, n, dx);
             }
@@ -205,8 +211,8 @@ struct SwiGLU : torch::autograd::Function<SwiGLU> {
         Tensor gate = gate_in, up = packed ? Tensor() : *up_in;
         int64_t ld = packed ? 0 : row_stride(gate);
         if (ld == 0 || row_stride(up) != ld) {
-            gate = gate.contiguous();
-            if (!packed) up = up.contiguous();
+            gate = dense(gate);
+            if (!packed) up = dense(up);
             ld = gate.size(-1);
         }
         const int64_t cols = gate.size(-1) / (packed ? 2 : 1), rows = gate.numel() / gate.size(-1), n = rows * cols;
@@ -232,7 +238,7 @@ struct SwiGLU : torch::autograd::Function<SwiGLU> {
         Tensor dgate, dup;
         {
             at::NoGradGuard no_grad;
-            const Tensor g = grads[0].contiguous();
+            const Tensor g = dense(grads[0]);
             const int64_t cols = g.size(-1), rows = g.numel() / cols;
             const Checkpoint c(kept, rows * cols);
             char *pg, *pu;

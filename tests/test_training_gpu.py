@@ -279,3 +279,46 @@ def test_a_refusal_in_the_backward_pass_is_an_exception(layer):
     torch.cuda.synchronize()
     y = ops.swiglu(x)                          # and the next call works
     assert torch.autograd.grad(y, x, torch.ones_like(y))[0].shape == x.shape
+
+
+def off(t, by=1):
+    """t's values, `by` values behind a 16-byte boundary, contiguous."""
+    buf = torch.empty(t.numel() + by, dtype=t.dtype, device="cuda")
+    buf[by:] = t.reshape(-1)
+    return buf[by:].view(t.shape)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("by", [1, 2, 3])
+def test_tensors_that_begin_off_a_16_byte_boundary(by, dtype):
+    x, w, both = values(1, 40, 64, dtype), values(2, 96, 64, dtype), values(3, 40, 128, dtype)
+    gy, gs = values(4, 40, 96, dtype), values(5, 40, 64, dtype)
+
+    def grads(f, ins, dy):
+        ins = [t.detach().requires_grad_() for t in ins]
+        y = f(*ins)
+        return [y.detach(), *torch.autograd.grad(y, ins, dy)]
+
+    for f, ins, dy in ((ops.linear_ste, (x, w), gy), (ops.swiglu, (both,), gs), (ops.swiglu, (x, gs), gy[:, :64].contiguous())):
+        want = grads(f, ins, dy)
+        for moved in ([off(t, by) for t in ins], [off(ins[0], by), *ins[1:]], [*ins[:-1], off(ins[-1], by)]):
+            assert moved[0].is_contiguous()
+            for g in (dy, off(dy, by)):
+                assert all(torch.equal(a, b) for a, b in zip(grads(f, moved, g), want))
+
+
+@pytest.mark.parametrize("odd", [1, 5])
+def test_gradients_that_are_slices(odd):
+    """The gradient that cat() hands back begins behind the values in front of the output."""
+    x, w = values(1, 40, 64).requires_grad_(), values(2, 128, 64).requires_grad_()
+    aux, dy = torch.zeros(odd, dtype=torch.bfloat16, device="cuda").requires_grad_(), values(3, 1, 64 * 40 + 32)[0]
+    y = ops.swiglu(ops.linear_ste(x, w))
+    n = y.numel()
+    got = torch.autograd.grad(torch.cat([aux, y.flatten()]), (x, w), torch.cat([dy[:odd], dy[:n]]))
+    want = torch.autograd.grad(ops.swiglu(ops.linear_ste(x, w)), (x, w), dy[:n].view(y.shape))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    z = ops.linear_ste(x, w)
+    dz = values(4, 40, 128)
+    got = torch.autograd.grad(torch.cat([aux, z.flatten()]), (x, w), torch.cat([aux.detach(), dz.flatten()]))
+    want = torch.autograd.grad(ops.linear_ste(x, w), (x, w), dz)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
