@@ -21,6 +21,7 @@ the outputs.
 import ctypes
 import math
 import os
+import re
 
 from . import mxq
 from .mxq import MXQError, _as2d, _check, _dt, _finish, _fits, _fmt, _on_gpu, _torch
@@ -82,16 +83,17 @@ def _native():
 
 
 def _plain(call, *args):
-    """What the C++ module makes of a call: None where the case is not a plain one (other types among them) or a C entry
-    point refused it, so that the code here says why."""
+    """What the C++ module makes of a call: None where the case is not a plain one (other types among them), so that the
+    code here says why. A refusal of a C entry point is raised with its status."""
     try:
         return call(*args)
     except TypeError:
         return None
     except RuntimeError as e:
-        if not str(e).startswith("mxq_"):
+        refused = re.match(r"(mxq_\w+): status (\d+)", str(e))
+        if not refused:
             raise
-        return None
+        raise MXQError(int(refused[2]), refused[1]) from None
 
 
 # ---- the C entry points, same names and arguments --------------------------------

@@ -297,3 +297,24 @@ def test_the_torch_module_shares_the_cpp_library():
     assert "[libstdc++.so.6]" in needed
     own = subprocess.run(["nm", "-D", "--defined-only", path], capture_output=True, text=True, check=True).stdout
     assert "_ZNSo" not in own and "St6locale" not in own      # streams, locales
+
+
+@pytest.mark.parametrize("status", [1, 2, 3, 4, 5])
+def test_the_status_of_a_refused_training_call_is_kept(status, monkeypatch):
+    """The module reports the entry point and its status; the exception carries both, whatever the devices are."""
+    def refuse(*args):
+        raise RuntimeError(f"mxq_quantize_both: status {status} ({mxq.mxq_status_string(status)})")
+
+    module = type("M", (), {"linear_ste": staticmethod(refuse), "swiglu": staticmethod(refuse)})
+    monkeypatch.setattr(ops, "_native", lambda: module)
+    for call in (lambda: ops.linear_ste(fake(4, 64), fake(32, 64)), lambda: ops.swiglu(fake(4, 64)), lambda: ops.swiglu(fake(4, 32), fake(4, 32))):
+        with pytest.raises(mxq.MXQError, match="mxq_quantize_both") as e:
+            call()
+        assert e.value.status == status
+
+    def other(*args):
+        raise RuntimeError("CUDA out of memory")
+
+    monkeypatch.setattr(module, "swiglu", staticmethod(other))
+    with pytest.raises(RuntimeError, match="out of memory"):
+        ops.swiglu(fake(4, 64))
