@@ -14,7 +14,8 @@ As in mxq.py, the mxq_* functions take raw integers and return the status; the h
 torch, refuse tensors that the C calls could not read or write safely, launch on the current stream (or `stream`)
 and raise MXQError on a non-zero status. linear_ste and swiglu with their gradients, and plain calls of the others, go
 through the C++ module _ops (csrc/ops_torch.cpp), which does the same in a few microseconds and leaves every other case
-and the errors to the code here. The kernels of the product and of attention for many queries bound their waits:
+and the errors to the code here. Of these functions linear_ste and swiglu alone are differentiable: the results of the
+others carry no gradient, also where an input requires one. The kernels of the product and of attention for many queries bound their waits:
 check=True (of matmul and linear) synchronizes and raises if one ran out; else call check_device() before trusting
 the outputs.
 """
@@ -255,7 +256,8 @@ def quantize_both(x, row_fmt=None, col_fmt=None, stream=None):
 
 def linear(x, w_codes, w_scales, fmt, out=None, stream=None, check=False):
     """x [..., k] (bf16/fp32, contiguous) rounded to `fmt`, times the weight w [n, k] held in `fmt` (codes
-    [n, k/32*P] and tile-layout scales, as quantize_mma(w, fmt) returns them): [..., n] of x's dtype."""
+    [n, k/32*P] and tile-layout scales, as quantize_mma(w, fmt) returns them): [..., n] of x's dtype. For serving: the
+    result carries no gradient (linear_ste is the layer to train)."""
     if out is None and stream is None and not check:
         y = _plain(_native().linear, x, w_codes, w_scales, mxq.FORMATS.get(fmt, -1))
         if y is not None:
@@ -447,11 +449,15 @@ def kv_attention(q, cache, block_table, seq_lens, q_starts=None, max_q=None, sca
     block_table  int32 [batch, pages]: page of keys page_size * i .. of a sequence
     seq_lens     int32 [batch]: keys of each sequence, the new tokens' among them
     q_starts     int32 [batch + 1]: sequence b's queries are rows q_starts[b] .. q_starts[b + 1] (starts do not
-                 decrease), at most max_q of them (default: rows); None: rows / batch queries each
+                 decrease), at most max_q of them; None: rows / batch queries each
+    max_q        with q_starts: the most queries of a sequence, which the host knows and the call cannot see. It chooses the
+                 kernel and the grid, so give it: the default, rows, computes a ragged batch of single tokens with the
+                 kernel for many queries (right, but slow)
     scale        of the scores (default head_dim ** -0.5); window: keys a query sees at most (0: all)
     max_keys     an upper bound of seq_lens, if known, for a better split of the work (longer sequences are cut)
     Returns out [rows, heads, head_dim]; with lse=True (out, log-sum-exp fp32 [rows, heads]). A query that sees no key
-    gives 0 (and -inf), and so do rows of no sequence and queries beyond max_q, which a given `out` keeps."""
+    gives 0 (and -inf), and so do rows of no sequence and queries beyond max_q, which a given `out` keeps. For serving: the
+    results carry no gradient."""
     if out is None and not lse and stream is None and cache._native is not None:
         o = _plain(_native().kv_attention, cache._native, q, block_table, seq_lens, q_starts, max_q, scale, window, max_keys)
         if o is not None:

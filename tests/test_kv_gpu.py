@@ -584,3 +584,26 @@ def test_a_cache_without_heads_rows_or_dimensions_is_refused(heads, page, dim):
     c = ops.KVCache.empty(0, 2, 16, 64)      # no pages: nothing to see
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
     assert (ops.kv_attention(rand(1, 3, 4, 64).bfloat16(), c, i32(3, 2), i32(3) + 5) == 0).all()
+
+
+def test_serving_results_carry_no_gradient():
+    c = filled(3, 4, 2, 16, 64)
+    table, lens = torch.arange(4, dtype=torch.int32, device="cuda")[None], torch.tensor([50], dtype=torch.int32, device="cuda")
+    q = rand(1, 3, 4, 64).bfloat16().requires_grad_()
+    out, lse = ops.kv_attention(q, c, table, lens, lse=True)
+    assert not out.requires_grad and not lse.requires_grad and not ops.kv_attention(q, c, table, lens).requires_grad
+    x, w = rand(1, 3, 64).bfloat16().requires_grad_(), mxq.quantize_mma(rand(2, 32, 64).bfloat16(), "mxfp8")
+    assert not ops.linear(x, *w, "mxfp8").requires_grad and not ops.linear(x, *w, "mxfp8", check=True).requires_grad
+    k = rand(3, 1, 2, 64).bfloat16().requires_grad_()
+    ops.kv_append(k, k, c, torch.zeros(1, dtype=torch.int64, device="cuda"))
+
+
+def test_ragged_single_tokens_without_max_q():
+    """max_q left out: the kernel for many queries, the same result within both errors."""
+    page, lens = 16, [130, 0, 64, 1, 700]
+    c = filled(5, 60, 2, page, 64)
+    table = tables(lens, page, 60)
+    spoil_tails(c, table, lens)
+    check(rand(7, 5, 8, 64).bfloat16(), c, table, lens, list(range(6)), max_q=None)
+    check(rand(7, 5, 8, 64).bfloat16(), c, table, lens, list(range(6)), max_q=5)
+    check(rand(7, 40, 8, 64).bfloat16(), c, table, lens, [8, 9, 9, 10, 11, 12], max_q=40)
