@@ -7,7 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "mxq_device.cuh"
-#include "mxq_internal.h"
+#include "mxq_ops_internal.h"
 #include "mxq_tma.cuh"
 
 namespace mxq {

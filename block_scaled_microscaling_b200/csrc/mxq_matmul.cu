@@ -31,7 +31,7 @@
 #include <cudaTypedefs.h>
 
 #include "mxq_device.cuh"
-#include "mxq_internal.h"
+#include "mxq_ops_internal.h"
 #include "mxq_tc.cuh"
 #include "mxq_tma.cuh"
 

@@ -6,7 +6,7 @@
 
 #include "../../include/mxq_ops.h"
 #include "mxq_check.h"
-#include "mxq_internal.h"
+#include "mxq_ops_internal.h"
 
 namespace {
 

@@ -16,7 +16,7 @@
 #include <cuda_runtime.h>
 
 #include "mxq_block.cuh"
-#include "mxq_internal.h"
+#include "mxq_ops_internal.h"
 
 namespace mxq {
 namespace {

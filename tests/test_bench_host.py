@@ -268,3 +268,9 @@ def test_timed_region_with_a_set_status_word_reports_nothing():
     ms, _ = bench.timed_replay(t, FakeGraph(t, [3.0, 4.0, 99.0]), "cpu", None, sampler_sequence([GOOD]),
                                replays=2, after=lambda: calls.append(1))
     assert ms == 7.0 and calls == [1]  # K replays in one region, one check after it
+
+
+def test_the_measured_traffic_belongs_to_the_sources():
+    """The headline kernel's sources are those of its committed DRAM capture: the roofline reports the traffic."""
+    assert bench.ncu_traffic("grouped_layer") == 282169472
+    assert bench.ncu_traffic("no such kernel") is None
