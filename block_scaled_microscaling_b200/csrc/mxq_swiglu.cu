@@ -120,8 +120,9 @@ __global__ void __launch_bounds__(kSwThreads) k_swiglu_backward(const void* __re
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float y = e ? y1 : y0, gv = g[i + e] * fg, uv = u[i + e] * fu, s = sigmoid<T>(gv);
-                    d[i + e] = y * gv * s;
-                    a[i + e] = y * uv * s * (1.0f + gv * (1.0f - s));
+                    // s first: for a gate far below zero it is 0, and the other factors' product may be infinite
+                    d[i + e] = y * (gv * s);
+                    a[i + e] = y * (s * (1.0f + gv * (1.0f - s))) * uv;
                 }
             }
             if constexpr (sizeof(T) == 4) {

@@ -322,3 +322,27 @@ def test_gradients_that_are_slices(odd):
     got = torch.autograd.grad(torch.cat([aux, z.flatten()]), (x, w), torch.cat([aux.detach(), dz.flatten()]))
     want = torch.autograd.grad(ops.linear_ste(x, w), (x, w), dz)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("low", [-3.3e38, -1e30, -200.0, -100.0])
+def test_swiglu_gradients_of_gates_far_below_zero(low, dtype):
+    """silu and its derivative vanish there, however large the other factors are. In fp32 s = e^-|g| / (1 + e^-|g|) lies below
+    the normal range: its exponential is off by at most two steps of 2^-149, its product and the factor 1 + g (1 - s) by half a
+    step each, together below (1 + |g|) 2^-147 before dy and u are multiplied in."""
+    gate = torch.full((3, 64), low, device="cuda", dtype=dtype)
+    up = torch.tensor([1.0, -3e38, 1e20, 0.0], device="cuda", dtype=dtype).repeat(3, 16)
+    dy = torch.tensor([4.0, -3e38, 1e20, 1e-3], device="cuda", dtype=dtype).repeat_interleave(48).view(3, 64)
+    gate.requires_grad_(), up.requires_grad_()
+    y = ops.swiglu(gate, up)
+    dgate, dup = torch.autograd.grad(y, (gate, up), dy)
+    for t in (y, dgate, dup):
+        assert torch.isfinite(t).all()
+    g8, u8 = decoded(gate.detach(), "mxfp8"), decoded(up.detach(), "mxfp8")
+    s, dy = 1 / (1 + torch.exp(-g8)), dy.double()
+    below = (1 + g8.abs()) * 2.0 ** -147
+    for got, want, by in ((dgate, dy * (s * (1 + g8 * (1 - s))) * u8, dy * u8), (dup, dy * (g8 * s), dy)):
+        room = by.abs() * below + half_step(dtype) * want.abs() + 2.0 ** -18 * want.abs() + torch.finfo(dtype).tiny
+        assert ((got.double() - want).abs() <= room).all()
+    if low < -200:
+        assert (dgate == 0).all() and (dup == 0).all()
