@@ -17,10 +17,13 @@
 //   columns, so one query of up to 8 heads per key head (a decoding step) wastes nothing.
 // - f16 holds a code times 2^x exactly for -23 <= x <= 13, so block scales are taken relative to a reference per
 //   warp (K and V each), 2^6 below the largest block when it was set and raised by a vote when a block exceeds 2^13
-//   of it; codes of blocks more than 2^29 below the largest seen lose bits. Rows of Q are divided by a power of
-//   two for the same reason. Scores return to their true size in fp32.
+//   of it; codes of blocks more than 2^29 below the largest that the warp's rows see lose bits (mxq_attention.cuh has what
+//   happens where rows see different keys). Rows of Q are divided by a power of two for the same reason: values 2^17
+//   below a row's largest lose bits, those 2^25 below it are 0. Scores return to their true size in fp32.
 // - the running maximum m_r is raised only when a score exceeds it by 2^8 (one vote per 16 keys); the weights
-//   then are at most 2^8 and round to f16 (relative error 2^-11; below 2^-14 absolute, 2^-25).
+//   then are at most 2^8 and round to f16 for the second product (relative error 2^-11; below 2^-14 absolute, 2^-25): the
+//   tensor cores take 16-bit operands, and f16 is the one with the most digits. Their sum is that of the fp32 values,
+//   since the rounding is even on average. 2^x is the hardware's (relative error 2^-22, far below that rounding).
 // The four warps of a CTA take every fourth group (page numbers are fetched 32 groups at a time); their results are
 // joined through shared memory. Where one row tile holds a sequence's queries (decoding), the groups of all sequences
 // and heads are cut into equal shares, one per resident CTA, whatever the lengths: a CTA walks the pieces of its
@@ -44,6 +47,9 @@ constexpr int kAtWarps = 4, kAtThreads = 32 * kAtWarps;
 constexpr int kAtStages = 3;       // groups in a warp's ring (four: as fast, six: 146 us for 141 at 16 sequences of 24..32 thousand keys)
 constexpr int kAtMaxSplits = 256;
 constexpr long long kJoinRows = 2048;  // below, the warps of a CTA share the splits of a row (4096 rows of 9 splits: 92 us so, 85 with a warp each)
+// a reference is at most 2^6 below the largest block, and blocks 2^23 below a reference are exact: so are those 2^16 below
+// what a row sees while the others of its tile see 2^13 of it
+constexpr int kAtRoom = 13;
 constexpr int kEvenGroups = 8;     // groups that an equal share has at least, if there are fewer sequences
 constexpr int kAtMaxEven = 512;    // sequences whose shares are worked out by every CTA
 
@@ -122,7 +128,8 @@ struct Piece {
 };
 
 // NQ: groups of eight rows that a warp handles together (their Q operands in shared memory when NQ is 4)
-template <int D, int NQ> __device__ __forceinline__ void attend(const AtArgs& p, const Piece& w) {
+// MIXED: the rows may see different keys (several queries)
+template <int D, int NQ, bool MIXED> __device__ __forceinline__ void attend(const AtArgs& p, const Piece& w) {
     constexpr int ROWS = 8 * NQ, STEPS = D / 16, TILES = D / 16;
     constexpr bool QS = NQ == 4;
     using S = AtStage<D>;
@@ -239,6 +246,9 @@ template <int D, int NQ> __device__ __forceinline__ void attend(const AtArgs& p,
     };
 #pragma unroll
     for (int i = 0; i < kAtStages - 1; ++i) issue();
+    __shared__ Spread spreads[MIXED ? kAtWarps : 1][2];
+    const bool mixed = MIXED && i1 > i0;
+    if (mixed) note_spread<D>(p, s, b, head, i0, i1, 16 * first, 16 * last, threadIdx.x, kAtThreads, spreads);
     uint32_t stage = ring;
     const int kr = 4 * (g >> 1) + (g & 1);  // the lane's keys of the score tiles: kr, kr + 2
     const uint32_t k_at = S::K + kr * S::ROW + t * (S::ROW / 4), ks_at = S::KS + kr * S::SROW + (D == 128 ? t : t >> 1);
@@ -482,6 +492,11 @@ template <int D, int NQ> __device__ __forceinline__ void attend(const AtArgs& p,
             }
         }
     __syncthreads();
+    if (mixed && spread_beyond<MIXED ? kAtWarps : 1>(spreads, kAtRoom, kAtRoom)) {
+        for (int r = warp; r < min(ROWS, rows - r0); r += kAtWarps)
+            exact_row<D>(p, s, b, head, r0 + r, 16 * first, 16 * last, w.alone, w.slot * ROWS + r);
+        return;
+    }
     float* const mine = dsm + warp * ROWS * (D + 4);
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
@@ -539,7 +554,7 @@ __device__ __forceinline__ Groups groups_in(const AtArgs& p, const Span& s) {
 }
 
 // the share of CTA blockIdx.x of all groups, (sequence, head, group) in order
-template <int D, int NQ> __device__ __forceinline__ void attend_share(const AtArgs& p) {
+template <int D, int NQ, bool MIXED> __device__ __forceinline__ void attend_share(const AtArgs& p) {
     __shared__ long long pre[kAtMaxEven + 1];  // groups of the sequences before, one head
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     constexpr int PER = kAtMaxEven / kAtThreads;
@@ -625,17 +640,17 @@ template <int D, int NQ> __device__ __forceinline__ void attend_share(const AtAr
                 info = make_int4(lo, w.head, total * (c - 1) / shares <= t0, (int)((t1 * shares - 1) / total));
             }
             if (!begin) __syncthreads();  // the piece before is out of shared memory
-            attend<D, NQ>(p, w);
+            attend<D, NQ, MIXED>(p, w);
             u += g1 - g0;
         }
     }
     if (t == 0) p.info[c] = info;
 }
 
-template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ? 2 : NQ == 2 ? 3 : 4) k_kv_attention(const AtArgs p) {
+template <int D, int NQ, bool MIXED> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ? 2 : NQ == 2 ? 3 : 4) k_kv_attention(const __grid_constant__ AtArgs p) {
     pdl_wait_then_release();
     if (NQ < 4 && p.even) {
-        attend_share<D, NQ>(p);
+        attend_share<D, NQ, MIXED>(p);
         return;
     }
     Piece w;
@@ -654,7 +669,7 @@ template <int D, int NQ> __global__ void __launch_bounds__(kAtThreads, NQ == 4 ?
     w.alone = gr.hi - gr.lo <= gr.per;  // one split holds all keys
     w.slot = blockIdx.x;
     if (w.first >= w.last && sp > 0) return;
-    attend<D, NQ>(p, w);
+    attend<D, NQ, MIXED>(p, w);
 }
 
 // ---- joining ------------------------------------------------------------------------------------
@@ -875,11 +890,11 @@ template <int D, int ROWS> cudaError_t join(const AtArgs& a, cudaStream_t st) {
     return launch_pdl(k_kv_attention_join<D, ROWS, 1>, (unsigned)((rows + kAtWarps - 1) / kAtWarps), kAtThreads, st, a);
 }
 
-template <int D, int NQ> cudaError_t go(const AtArgs& a, const Plan& pl, int dev, cudaStream_t st) {
+template <int D, int NQ, bool MIXED> cudaError_t go(const AtArgs& a, const Plan& pl, int dev, cudaStream_t st) {
     constexpr int RES = kAtWarps * 8 * NQ * (D + 4) * 4;
     constexpr int IN = kAtWarps * kAtStages * AtStage<D>::BYTES + (NQ == 4 ? NQ * (D / 16) * 32 * 8 : 0);
     constexpr int SMEM = RES > IN ? RES : IN;
-    auto* kern = k_kv_attention<D, NQ>;
+    auto* kern = k_kv_attention<D, NQ, MIXED>;
     static std::atomic<unsigned long long> ready{0};
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
     if (!(ready.load(std::memory_order_acquire) & bit)) {
@@ -967,14 +982,14 @@ cudaError_t launch_kv_attention(const KvAttention& x, cudaStream_t st) {
     a.by_tiles = FastDiv((uint32_t)pl.row_tiles);
     a.by_heads = FastDiv((uint32_t)x.c.heads);
     if (x.c.db == 4) {
-        if (pl.nq == 1) return go<128, 1>(a, pl, dev, st);
-        if (pl.nq == 2) return go<128, 2>(a, pl, dev, st);
-        if (pl.nq == 4) return go<128, 4>(a, pl, dev, st);
+        if (pl.nq == 1) return a.max_q > 1 ? go<128, 1, true>(a, pl, dev, st) : go<128, 1, false>(a, pl, dev, st);
+        if (pl.nq == 2) return a.max_q > 1 ? go<128, 2, true>(a, pl, dev, st) : go<128, 2, false>(a, pl, dev, st);
+        if (pl.nq == 4) return a.max_q > 1 ? go<128, 4, true>(a, pl, dev, st) : go<128, 4, false>(a, pl, dev, st);
         return go_tiles<128>(a, pl, dev, st);
     }
-    if (pl.nq == 1) return go<64, 1>(a, pl, dev, st);
-    if (pl.nq == 2) return go<64, 2>(a, pl, dev, st);
-    if (pl.nq == 4) return go<64, 4>(a, pl, dev, st);
+    if (pl.nq == 1) return a.max_q > 1 ? go<64, 1, true>(a, pl, dev, st) : go<64, 1, false>(a, pl, dev, st);
+    if (pl.nq == 2) return a.max_q > 1 ? go<64, 2, true>(a, pl, dev, st) : go<64, 2, false>(a, pl, dev, st);
+    if (pl.nq == 4) return a.max_q > 1 ? go<64, 4, true>(a, pl, dev, st) : go<64, 4, false>(a, pl, dev, st);
     return go_tiles<64>(a, pl, dev, st);
 }
 

@@ -157,6 +157,156 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
     return v;
 }
 
+// ---- keys that only some rows of a tile see -------------------------------------------------------
+//
+// The rows of a tile share the powers of two that keys and values are decoded to. A key that only some of them see (the
+// causal edge of a chunk, the lower edge of a window) may hold far larger blocks than the others see, and would cost
+// those bits. So the kernels look at the scales of these keys, which are few (two for each query at most), and of up to
+// kSpreadKeys keys that every row sees: the largest block of the former (`edge`), of the latter (`whole`), and the smallest
+// of the former keys' largest blocks (`least`, keys of zeros aside). Every row that sees a key sees a block of `whole`, or of
+// `least` where no key is seen by all: where `edge` exceeds that by more than `room`, the tile's rows are computed anew by
+// exact_row, which shares nothing. That is slow (4 queries of 32 heads
+// over 3000 keys 92 us for 18, 128 over 32768 keys 21 ms for 0.08) and does not happen with keys and values of one kind;
+// the look itself takes up to 1 us a call (prompts of 2000 tokens with a window of 512 180 us for 174).
+struct Spread {
+    int whole, edge, least;
+    __device__ __forceinline__ bool beyond(int room) const { return edge > (whole >= 0 ? whole : least) + room; }
+};
+constexpr int kSpreadKeys = 128;
+// `out` [warps][2]: of K and V, for the queries i0 .. i1 (i1 > i0) over the keys first .. last - 1; `t` of `threads` threads,
+// whole warps, call it
+template <int D> __device__ __forceinline__ void note_spread(const AtArgs& p, const Span& s, int b, int head, int i0, int i1, int first, int last, int t, int threads, Spread (*out)[2]) {
+    const KeyRange some = keys_seen(p, s, i0, i1);
+    const int pos_lo = max(s.len - s.n + i0, -1), pos_hi = max(s.len - s.n + i1, -1);
+    const int lo = max(some.lo, first), hi = max(min(some.hi, last), lo);
+    // every row sees the keys all_lo .. all_hi - 1
+    const int all_lo = min(max(p.window > 0 ? pos_hi - p.window + 1 : 0, lo), hi), all_hi = max(min(pos_lo + 1, hi), all_lo);
+    const int below = all_lo - lo, edges = below + (hi - all_hi), n = edges + min(all_hi - all_lo, kSpreadKeys);
+    int whole[2] = {-1, -1}, edge[2] = {-1, -1}, least[2] = {256, 256};
+    for (int e = t; e < n; e += threads) {
+        const int key = e < below ? lo + e : e < edges ? all_hi + (e - below) : all_hi - 1 - (e - edges);
+        const int at = p.by_page(key), pg = __ldg(p.table + b * p.table_stride + at);
+        if (pg < 0 || pg >= p.c.pages) continue;
+        const long long row = ((long long)pg * p.c.heads + head) * p.c.page + (key - at * p.c.page);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const uint8_t* const scales = (v ? p.c.vs : p.c.ks) + row * (D / 32);
+            uint32_t w = D == 128 ? *reinterpret_cast<const uint32_t*>(scales) : (uint32_t)*reinterpret_cast<const uint16_t*>(scales);
+            w &= ~__vcmpeq4(w, 0xFFFFFFFFu);  // NaN blocks aside
+            w = __vmaxu4(w, w >> 16);
+            const int most = (int)max(w & 0xFFu, (w >> 8) & 0xFFu);
+            if (e >= edges) {
+                whole[v] = max(whole[v], most);
+            } else {
+                edge[v] = max(edge[v], most);
+                if (most > 0) least[v] = min(least[v], most);
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        const Spread x{__reduce_max_sync(0xFFFFFFFFu, whole[v]), __reduce_max_sync(0xFFFFFFFFu, edge[v]), __reduce_min_sync(0xFFFFFFFFu, least[v])};
+        if ((t & 31) == 0) out[t >> 5][v] = x;
+    }
+}
+// whether the notes of W warps call for exact_row
+template <int W> __device__ __forceinline__ bool spread_beyond(const Spread (*notes)[2], int room_k, int room_v) {
+    bool beyond = false;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        Spread x = notes[0][v];
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+            x.whole = max(x.whole, notes[w][v].whole);
+            x.edge = max(x.edge, notes[w][v].edge);
+            x.least = min(x.least, notes[w][v].least);
+        }
+        beyond |= x.beyond(v ? room_v : room_k);
+    }
+    return beyond;
+}
+// by one warp: the row of rows (query x head of the group) `row` of a sequence over the keys first .. last - 1, in fp32
+// throughout, to out (alone) or to row `part_row` of the partial sums. Lane d / (D / 32) holds dimension d.
+template <int D> __device__ __forceinline__ void exact_row(const AtArgs& p, const Span s, int b, int head, int row, int first, int last, bool alone, long long part_row) {
+    constexpr int PER = D / 32, KEYS = 8;  // keys at a time
+    const int lane = threadIdx.x & 31;
+    const int i = p.by_group(row), h = head * p.group + (row - i * p.group), pos = s.len - s.n + i;
+    const int lo = p.window > 0 && pos >= p.window ? max(first, pos - p.window + 1) : first, hi = min(last, pos + 1);
+    const uint16_t* const q16 = reinterpret_cast<const uint16_t*>(p.q + (s.q0 + i) * p.q_row_stride + h * p.q_head_stride) + lane * PER;
+    float q[PER], o[PER], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int d = 0; d < PER; ++d) {
+        q[d] = __uint_as_float((uint32_t)__ldg(q16 + d) << 16);
+        o[d] = 0.f;
+    }
+    auto decode = [&](const char* codes, const uint8_t* scales, long long at, float* v) {
+        const char* const c = codes + at * (D / 2) + lane * (PER / 2);
+        const uint32_t byte = scales[at * (D / 32) + lane * PER / 32];
+        const float f = byte == 0xFFu ? __uint_as_float(0x7FC00000u) : fwd_scale(byte);
+        const uint32_t x = PER == 4 ? (uint32_t)*reinterpret_cast<const uint16_t*>(c) : (uint32_t)*reinterpret_cast<const uint8_t*>(c);
+#pragma unroll
+        for (int d = 0; d < PER; ++d) {  // twice the value of codes 0 .. 7: 0 1 2 3 4 6 8 12, a byte each
+            const uint32_t code = x >> (4 * d), twice = __byte_perm(0x03020100u, 0x0C080604u, code & 7u) & 0xFFu;
+            v[d] = (code & 8u ? -0.5f : 0.5f) * (float)twice * f;
+        }
+    };
+    for (int j = lo; j < hi;) {
+        const int at = p.by_page(j), off = j - at * p.c.page, n = min(hi - j, p.c.page - off);
+        const int pg = __ldg(p.table + b * p.table_stride + at);
+        j += n;
+        if (pg < 0 || pg >= p.c.pages) continue;
+        const long long place = ((long long)pg * p.c.heads + head) * p.c.page + off;
+        for (int r = 0; r < n; r += KEYS) {  // (beyond the last key: the last again, which does not count)
+            float v[KEYS][PER], x[KEYS];
+#pragma unroll
+            for (int u = 0; u < KEYS; ++u) {
+                float k[PER];
+                decode(p.c.kc, p.c.ks, place + min(r + u, n - 1), k);
+                decode(p.c.vc, p.c.vs, place + min(r + u, n - 1), v[u]);
+                x[u] = 0.f;
+#pragma unroll
+                for (int d = 0; d < PER; ++d) x[u] = fmaf(q[d], k[d], x[u]);
+            }
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2)
+#pragma unroll
+                for (int u = 0; u < KEYS; ++u) x[u] += __shfl_xor_sync(0xFFFFFFFFu, x[u], d);
+            float top = m;
+#pragma unroll
+            for (int u = 0; u < KEYS; ++u) {
+                x[u] = r + u < n ? x[u] * p.scale : -INFINITY;
+                top = fmaxf(top, x[u]);
+            }
+            if (top > m) {
+                const float f = ex2(m - top);
+                m = top;
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < PER; ++d) o[d] *= f;
+            }
+#pragma unroll
+            for (int u = 0; u < KEYS; ++u) {
+                if (x[u] == -INFINITY) continue;
+                const float w = ex2(x[u] - m);
+                l += w;
+#pragma unroll
+                for (int d = 0; d < PER; ++d) o[d] = fmaf(w, v[u][d], o[d]);
+            }
+        }
+    }
+    if (alone) {
+        const long long at = (long long)(s.q0 + i) * p.heads + h;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int d = 0; d < PER; ++d) p.out[at * D + lane * PER + d] = __float2bfloat16_rn(o[d] * inv);
+        if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    } else {
+#pragma unroll
+        for (int d = 0; d < PER; ++d) p.part[part_row * D + lane * PER + d] = o[d];
+        if (lane == 0) *reinterpret_cast<float2*>(p.part + p.part_ml + part_row * 2) = make_float2(m, l);
+    }
+}
+
 // many rows of a sequence and key head: 256 at a time, keys in blocks of 128 (mxq_attention_tc.cu)
 constexpr int kTileRows = 256, kTileKeysShift = 7, kTileMinBlocks = 1;
 cudaError_t launch_kv_attention_tiles(const AtArgs& a, long long tiles, int dev, cudaStream_t st);

@@ -3,7 +3,8 @@
 //
 // A CTA takes two tiles of 128 rows (query x head of one key head's group) and walks blocks of 128 keys:
 //   S = Q K^T (fp32 in tensor memory),  P = 2^(S - m) (f16, over S),  O += P V (fp32, tensor memory),
-// with the formulas, the relative block scales and the masks of mxq_attention.cu. Decoding 128 keys then serves 256
+// with the formulas, the masks and the roundings of mxq_attention.cu. Block scales are relative to the largest K of a block of
+// keys (blocks 2^28 below it are 0) and to the largest V so far (0 from 2^24 to 2^28 below it on). Decoding 128 keys then serves 256
 // rows, not 32 as in a warp's registers there. Roles:
 // - two warps bring the blocks' codes to a ring in shared memory (16-byte asynchronous copies), one finds their largest
 //   scales.
@@ -38,6 +39,9 @@ namespace {
 constexpr int kTcThreads = 512, kTcDecode = 8, kTcMma = 12, kTcCopy = 13, kTcScales = 15;
 template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// K is decoded to 2^-13 of the largest block of its 128 keys, V to 2^-10 of the largest that set its reference or less, and
+// blocks 2^14 below that are exact: so are those 2^16 below what a row sees while the others of its tile see this much more
+constexpr int kTcRoomK = 11, kTcRoomV = 8;
 constexpr int kTcRaw = 3;        // blocks in the ring of raw codes
 
 template <int D> struct TcCfg {
@@ -104,7 +108,7 @@ __device__ __forceinline__ int max_byte(const uint32_t* w, bool& nan) {
     return (int)(m & 0xFFu);
 }
 
-template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention_tiles(const AtArgs p, unsigned int* err) {
+template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention_tiles(const __grid_constant__ AtArgs p, unsigned int* err) {
     using C = TcCfg<D>;
     extern __shared__ uint8_t dsm8[];
     uint8_t* const base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm8) + 1023) & ~uintptr_t(1023));
@@ -114,6 +118,7 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
     __shared__ int abort_flag;
     __shared__ BlockInfo infos[8];  // eight blocks: more than the roles can be apart
     __shared__ uint32_t there[8][2];      // groups of 16 keys of a block that are in pages: even and odd ones
+    __shared__ Spread spreads[4][2];      // noted by the decoding warps, where the rows see different keys
     __shared__ uint8_t nan_keys[8][128];  // of a block with NaN values: bit b of key's byte: its block b is NaN
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -163,8 +168,9 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
     if (p.fill && rt == 0 && sp == 0) fill_rows<D>(p, s, b, head * p.group, p.group);
     Groups gr{0, 0, 1};
     KeyRange some{0, 0};  // the keys that a row of the CTA sees: the bytes of others count as zeros
+    int i0 = 0, i1 = 0;   // the CTA's queries
     if (r0 < rows) {
-        const int i0 = p.by_group(r0), i1 = p.by_group(min(r0 + kTileRows, rows) - 1);
+        i0 = p.by_group(r0), i1 = p.by_group(min(r0 + kTileRows, rows) - 1);
         gr = groups_of<kTileKeysShift, kTileMinBlocks>(p, s, i0, i1);
         some = keys_seen(p, s, i0, i1);
     }
@@ -309,7 +315,11 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
             if (n > 0 && ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full(x), (uint32_t)n & 1u, ab, err));
             tc_fence_after();
             if (!(thr > 0.f)) m = -INFINITY;
-            if (ok) {
+            if (ok && n > 0 && i1 > i0 && spread_beyond<4>(spreads, kTcRoomK, kTcRoomV)) {
+                const int t0 = 128 * x + quad * 32;
+                for (int k = t0; k < t0 + 32 && r0 + k < rows; ++k)
+                    exact_row<D>(p, s, b, head, r0 + k, first * 128, (first + n) * 128, alone, (long long)blockIdx.x * kTileRows + k);
+            } else if (ok) {
                 const long long at = (long long)(s.q0 + i) * p.heads + h, slot0 = (long long)blockIdx.x * kTileRows + 128 * x + quad * 32;
                 const float vtrue = pow2i(vref - 127), f = alone ? (l == 0.f ? 0.f : vtrue / l) : vtrue;
                 const float nan = __uint_as_float(0x7FC00000u);
@@ -375,6 +385,8 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
         uint32_t pages_v = 0;
         int vref_v = 0;
         bool nan_v = false, live = work && n > 0;
+        // while Q and the first codes are on their way; the softmax warps read it when O, and so all of K, is done
+        if (live && i1 > i0) note_spread<D>(p, s, b, head, i0, i1, first * 128, (first + n) * 128, d, 128, spreads);
         for (int it = 0; live && it <= n; ++it) {
             const int key0 = (first + it) * 128;
             BlockInfo bi{0, 0, 0, 0};
@@ -577,7 +589,7 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                     top[v] = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)max_byte(x, nan));
                 }
                 nan = __any_sync(0xFFFFFFFFu, nan);
-                if (top[1] > vref + 13) vref = top[1] - 6;
+                if (top[1] > vref + 13) vref = top[1] - 10;
                 if (lane == 0) {
                     infos[it & 7] = {top[0] - 13, vref, pages, nan ? 1u : 0u};
                     mbar_arrive(info_full(at.s));

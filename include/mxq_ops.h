@@ -147,9 +147,8 @@ MXQ_API mxq_status mxq_kv_read(const mxq_kv_cache* cache, const int64_t* slots, 
  *   out = sum_j w_j v_j,  w = softmax over the keys seen of scale * (q . k_j)
  *   lse = log sum_j exp(scale * (q . k_j))           (natural logarithm)
  * q head h reads key/value head h / (q_heads / kv_heads). A query that sees no
- * key gives out = 0 and lse = -inf. Keys that no query of the sequence sees do
- * not enter it, whatever bytes they hold (one that only some of its queries see
- * can cost the others bits: below); a key whose page number is outside [0,
+ * key gives out = 0 and lse = -inf. Keys that a query does not see do not enter
+ * it, whatever bytes they hold; a key whose page number is outside [0,
  * pages) is seen by no query. Starts do not decrease; each is clamped to [0, q_rows].
  * Rows of q that belong to no sequence, and queries of a sequence beyond max_q,
  * are not computed: with fill == 0 they are left as they are in out and lse,
@@ -164,10 +163,13 @@ MXQ_API mxq_status mxq_kv_read(const mxq_kv_cache* cache, const int64_t* slots, 
  *          16-byte aligned, used by this call alone until it has finished. What
  *          a max_keys asks for is enough for every smaller one, and for tables
  *          of any width.
- * Keys and values are decoded to half precision (f16) exactly up to a power of
- * two that up to 256 rows (query x head of a key head) share: a block more than
- * 2^20 below the largest that one of these rows sees may lose bits or count as
- * zero. Scores and sums are fp32; the weights w enter the second product in f16.
+ * Keys, values and rows of q are brought to half precision (f16), exactly up to a
+ * power of two: a block more than 2^16 below the largest that the query sees (of
+ * the keys; of the values), and values of q more than 2^17 below the largest of
+ * their row, may lose bits or count as zero. Scores and sums are fp32, 2^x has an
+ * error of 2^-22; the weights w enter the second product in f16 (2^-11). Where a
+ * key that only some queries of a chunk see is far larger than the others, the
+ * chunk's rows are computed one by one in fp32, many times slower.
  * Where max_q * (q_heads / kv_heads) exceeds 32, the kernel's waits are bounded
  * (mxq_check_device).
  */

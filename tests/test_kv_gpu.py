@@ -607,3 +607,82 @@ def test_ragged_single_tokens_without_max_q():
     check(rand(7, 5, 8, 64).bfloat16(), c, table, lens, list(range(6)), max_q=None)
     check(rand(7, 5, 8, 64).bfloat16(), c, table, lens, list(range(6)), max_q=5)
     check(rand(7, 40, 8, 64).bfloat16(), c, table, lens, [8, 9, 9, 10, 11, 12], max_q=40)
+
+
+HIDDEN = [  # (keys of each sequence, queries, group, head_dim, window, key counted from the last, page)
+    ([90], [3], 4, 128, 0, 0, 16), ([90], [8], 4, 64, 0, 3, 16), ([700, 300], [5, 2], 1, 64, 0, 0, 32), ([3000], [8], 4, 128, 0, 5, 64),
+    ([3000, 2000], [4, 4], 4, 128, 0, 2, 64), ([16], [16], 2, 128, 0, 9, 16), ([70], [70], 4, 128, 0, 60, 16), ([70], [70], 1, 64, 0, 0, 16),
+    ([500], [100], 4, 128, 0, 40, 16), ([5000], [64], 4, 128, 0, 1, 64), ([5000], [40], 8, 64, 0, 30, 64), ([2000], [300], 1, 128, 0, 290, 32),
+    ([90], [4], 4, 128, 20, 22, 16), ([3000, 900], [8, 8], 4, 64, 500, 506, 32), ([3000], [6], 1, 128, 1000, 1003, 32), ([300], [60], 4, 128, 30, 80, 16),
+    ([3000], [64], 4, 128, 1000, 1040, 64), ([2000], [200], 1, 64, 150, 333, 32), ([40], [43], 2, 64, 0, 0, 16), ([200], [60], 2, 128, 3, 59, 16)]
+
+
+@pytest.mark.parametrize("k_byte,v_byte", [(127, 0xFC), (0xFC, 127), (0xFC, 0xFC), (147, 147), (127, 240), (0xFF, 0xFF)])
+@pytest.mark.parametrize("case", range(len(HIDDEN)))
+def test_keys_that_some_queries_do_not_see(case, k_byte, v_byte):
+    """A key with huge blocks that only some queries of a tile see: later ones in a causal chunk, earlier ones where a window
+    leaves it behind. The others' results are those without it."""
+    lens, news, group, d, window, back, page = HIDDEN[case]
+    c = filled(3, sum(-(-n // page) for n in lens) + 1, 2, page, d)
+    table = tables(lens, page, c.pages)
+    spoil_tails(c, table, lens)
+    starts = [sum(news[:i]) for i in range(len(news) + 1)]
+    q = rand(9, sum(news), 2 * group, d).bfloat16()
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    call = lambda: ops.kv_attention(q, c, table, dev(lens), q_starts=dev(starts), max_q=max(news), window=window, lse=True)  # noqa: E731
+    out, want_lse, tol, _ = reference(q, c, table, lens, starts, window)
+    clean = call()
+    blind = torch.ones(sum(news), dtype=torch.bool, device="cuda")   # queries that see none of the huge keys
+    for b, (n, new) in enumerate(zip(lens, news)):
+        key = n - 1 - back
+        pos = n - new + torch.arange(new, device="cuda")
+        blind[starts[b]:starts[b + 1]] = (key > pos) | ((key <= pos - window) if window else False)
+        for t, x in ((c.k_codes, 0x77), (c.v_codes, 0x77), (c.k_scales, k_byte), (c.v_scales, v_byte)):
+            t[int(table[b, key // page]), :, key % page] = x
+    assert blind.any() and not blind.all()
+    got, lse = call()
+    assert ((got.double() - out).abs() <= tol + out.abs() * 2.0 ** -8)[blind].all()
+    fin = torch.isfinite(want_lse) & blind[:, None]
+    assert torch.equal(lse == -math.inf, want_lse == -math.inf) or k_byte != 127
+    assert ((lse.double() - want_lse).abs()[fin] <= 2.0 ** -12 * (1 + want_lse.abs()[fin])).all()
+    assert torch.equal(got, call()[0]) or not torch.isfinite(got).all()
+    if k_byte == 127:    # the others: that key with the rest
+        check(q, c, table, lens, starts, window=window)
+    if k_byte == 0xFF:
+        assert torch.isnan(got[~blind]).all()
+    assert torch.isfinite(clean[0]).all()
+
+
+@pytest.mark.parametrize("news,group,d", [(5, 4, 128), (1, 4, 64), (60, 4, 128), (90, 1, 64)])
+@pytest.mark.parametrize("prefix", [0, 16, 37, 300])
+def test_prefixes_of_zeros(prefix, news, group, d):
+    """Keys and values of zeros in front, and in the middle of the new ones: scale bytes of 0 next to ordinary ones."""
+    page, n = 16, prefix + news
+    c = ops.KVCache.empty(25, 2, page, d)
+    table = tables([n], page, 25)
+    pos = torch.arange(n, device="cuda")
+    k, v = rand(1, n, 2, d).bfloat16(), rand(2, n, 2, d).bfloat16()
+    k[:prefix], v[:prefix] = 0, 0
+    k[prefix + news // 2], v[prefix + news // 2] = 0, 0
+    ops.kv_append(k, v, c, table[0, pos // page].long() * page + pos % page)
+    check(rand(3, news, 2 * group, d).bfloat16(), c, table, [n], [0, news])
+    check(rand(3, news, 2 * group, d).bfloat16(), c, table, [n], [0, news], window=20)
+
+
+def test_tokens_written_beside_huge_ones():
+    """Through kv_append: the chunk's last token holds the largest values of bf16, the first ones small values; a later chunk
+    whose window has left the token behind."""
+    page, n, d = 16, 80, 128
+    for news in (6, 40):
+        c = ops.KVCache.empty(12, 2, page, d)
+        table, pos = tables([n], page, 12, width=12), torch.arange(n, device="cuda")
+        k, v = rand(1, n, 2, d).bfloat16(), (rand(2, n, 2, d) * 1e-3).bfloat16()
+        want_k, want_v = k.clone(), v.clone()
+        v[-1] = torch.finfo(torch.bfloat16).max
+        slots = table[0, pos // page].long() * page + pos % page
+        ops.kv_append(want_k, want_v, c, slots)
+        q = rand(3, news, 8, d).bfloat16()
+        clean = check(q, c, table, [n], [0, news])
+        ops.kv_append(k, v, c, slots)
+        got = check(q, c, table, [n], [0, news])
+        assert ((got[:-1] - clean[:-1]).abs() <= 2 * 2.0 ** -8 * clean[:-1].abs() + 1e-6).all()
