@@ -29,10 +29,11 @@
 // and heads are cut into equal shares, one per resident CTA, whatever the lengths: a CTA walks the pieces of its
 // share, and the at most two of them that are part of a split sequence leave their sums to a second kernel, which
 // joins them in order. Otherwise a long sequence is split over a fixed number of CTAs, joined the same way.
-// Measured (32 heads on 8 of 128, one query each): 16 sequences of 24 .. 32 thousand keys 140 us (3.6 TB/s of cache; the
+// Measured (32 heads on 8 of 128, one query each): 16 sequences of 24 .. 32 thousand keys 137 us (3.7 TB/s of cache; the
 // issue slots are 63% busy, the arithmetic pipe 52%, and the waits of dependent conversions fill the rest: with three
-// CTAs to an SM, 183 us; five, with spilled registers, 158; two groups at a time, 143), one sequence of 4000 keys 10
-// us, of 32768 keys 22.
+// CTAs to an SM, 183 us; five, with spilled registers, 158; two groups at a time, 143), one sequence of 4000 keys 9
+// us, of 32768 keys 20; of head_dim 64, 16 sequences of 16384 keys 63. At head_dim 128 the limits of 128 and 168 registers
+// make the compiler spill (72 and 180 bytes of stores a thread for 8 and 16 rows).
 #include <atomic>
 #include <cstdint>
 #include <type_traits>

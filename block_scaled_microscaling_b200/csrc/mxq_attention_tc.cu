@@ -16,7 +16,8 @@
 //   operand of the second product. The maximum is raised (and O rescaled, in tensor memory) only when a score exceeds
 //   it by 2^8, or when a value block exceeds 2^13 of the reference scale.
 // - one warp issues the MMAs: O of a tile's block, then S of its next block, while the other tile is in its softmax.
-// Measured: 128 queries of 32 heads over 32768 keys (8 heads of 128) 82 us, 0.83 PFLOP/s; 512 over 8192 keys 131 us. A block
+// Measured: 128 queries of 32 heads over 32768 keys (8 heads of 128) 81 us, 0.85 PFLOP/s; 512 over 8192 keys 93 us, a prompt of
+// 2048 on itself 82 us; of head_dim 64, 128 over 16384 keys 44 us. A block
 // of 128 keys for 256 rows takes about 4300 cycles: a tile's softmax (2500 to 3000) and its two products (1400) follow
 // each other, while the other tile is half a block away; decoding is busy for 3000 cycles, the tensor cores for 42% of the
 // time. Other divisions were slower: one tile per CTA with S in two buffers (163 us when this took 120), blocks of 64 keys

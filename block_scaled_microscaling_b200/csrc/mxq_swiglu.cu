@@ -7,7 +7,7 @@
 //   dgate = dy * u * s * (1 + g * (1 - s)),   dup = dy * g * s.
 // Both are bound by memory: 8.06 bytes per value pair forward and 8.06 backward in bf16 (about 40 instructions
 // per pair fit beside that): 16384 x 9728 bf16 takes 190 us forward (6.8 TB/s; 218 with the checkpoint after the products,
-// for want of warps) and 187 backward (6.9 TB/s). One thread per block needs no shuffle for the block's maximum; a few
+// for want of warps) and 188 backward (6.8 TB/s), 8192 x 9728 fp32 181 and 171 (6.2 and 6.6 TB/s). One thread per block needs no shuffle for the block's maximum; a few
 // rows are bound by that thread's latency instead (37 x 2560 fp32 4 us a pass). bf16 divides with the
 // hardware's approximate reciprocal (2 units in the last place, before the rounding to 2^-8); the exponential is the
 // accurate one for both types, since the approximate one loses |x| / 2^24 of its result.
