@@ -144,7 +144,7 @@ template <int D, int NQ, bool MIXED> __device__ __forceinline__ void attend(cons
     // ---- the rows' queries: lane (g, t) holds row g of each eight, dimensions t D/4 .., divided by 2^e ----
     uint32_t qf[QS ? 1 : NQ][STEPS][2];
     uint2* const qsm = reinterpret_cast<uint2*>(reinterpret_cast<char*>(dsm) + kAtWarps * kAtStages * S::BYTES);
-    float mul[NQ][2];  // per column of the score tiles (rows 2t, 2t + 1): scale * log2(e) * 2^e
+    int q_exp[NQ][2];  // e per column of the score tiles (rows 2t, 2t + 1)
     int pos[NQ][2];    // last key that the row sees (-1: no row, or none; never less, so that pos - window is an int)
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -190,7 +190,7 @@ template <int D, int NQ, bool MIXED> __device__ __forceinline__ void attend(cons
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int col = 2 * t + k, rr = r0 + 8 * n + col;
-            mul[n][k] = p.scale * pow2i(__shfl_sync(0xFFFFFFFFu, e, 4 * col));
+            q_exp[n][k] = __shfl_sync(0xFFFFFFFFu, e, 4 * col);
             pos[n][k] = rr < rows ? max(s.len - s.n + p.by_group(rr), -1) : -1;
         }
     }
@@ -212,7 +212,7 @@ template <int D, int NQ, bool MIXED> __device__ __forceinline__ void attend(cons
     }
     int kref = -1000, vref = -1000;   // block scales are taken relative to these bytes
     int klim = -1, vlim = -1;         // and may be at most these
-    float mk[NQ][2];                  // mul * 2^(kref - 127)
+    float mk[NQ][2];                  // scale * log2(e) * 2^(q_exp + kref - 127)
 #pragma unroll
     for (int n = 0; n < NQ; ++n) mk[n][0] = mk[n][1] = 0.f;
     uint32_t vnan = 0;                // bit 2n + k: a value block that row sees is NaN
@@ -300,7 +300,7 @@ template <int D, int NQ, bool MIXED> __device__ __forceinline__ void attend(cons
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) mk[n][k] = mul[n][k] * pow2i(kref - 127);
+                    for (int k = 0; k < 2; ++k) mk[n][k] = p.scale * pow2i(min(q_exp[n][k] + kref - 127, 127));
             }
             vt = __reduce_max_sync(0xFFFFFFFFu, vt);
             if (vt > vref + 13) {
@@ -480,7 +480,7 @@ template <int D, int NQ, bool MIXED> __device__ __forceinline__ void attend(cons
             if (!(thr[n][k] > 0.f)) m[n][k] = -INFINITY;
 
     // ---- join the warps ----
-    const float vtrue = vref > -1000 ? pow2i(vref - 127) : 0.f;
+    const float vtrue = scale_of(vref);
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -508,13 +508,13 @@ template <int D, int NQ, bool MIXED> __device__ __forceinline__ void attend(cons
 #pragma unroll
             for (int q = 1; q < kAtWarps; ++q) top = fmaxf(top, sm_m[q][r]);
             // a warp without a visible key has sums of 0 (or NaN, which stays)
-            float f = (m[n][k] == -INFINITY ? 1.f : ex2(m[n][k] - top)) * vtrue;
+            float f = m[n][k] == -INFINITY ? 1.f : ex2(m[n][k] - top);
             if (vnan & (1u << (2 * n + k))) f = __uint_as_float(0x7FC00000u);
             // the lane's dimensions g D/8 ..: tile 4j + q holds 8j + 2q (first eight rows of the tile) and the next
 #pragma unroll
             for (int j = 0; j < TILES; j += 2)
                 *reinterpret_cast<float4*>(mine + res_off<D>(r, g * (D / 8) + 2 * j)) =
-                    make_float4(o[n][j][k] * f, o[n][j][k + 2] * f, o[n][j + 1][k] * f, o[n][j + 1][k + 2] * f);
+                    make_float4(o[n][j][k] * f * vtrue, o[n][j][k + 2] * f * vtrue, o[n][j + 1][k] * f * vtrue, o[n][j + 1][k + 2] * f * vtrue);
         }
     __syncthreads();
     for (int i = threadIdx.x; i < ROWS * (D / 4); i += kAtThreads) {

@@ -136,6 +136,10 @@ __device__ __forceinline__ void e2m1_to_h2(uint32_t x, uint32_t* r) {
 }
 // 2^e for any integer e (clamped to the fp32 range, subnormals flushed)
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)min(max(e + 127, 0), 255) << 23); }
+// 2^(byte - 127) of a reference scale byte of -149 .. 254: below 1 a subnormal, whose product with a normal sum is exact
+__device__ __forceinline__ float scale_of(int byte) {
+    return __uint_as_float(byte > 0 ? (uint32_t)byte << 23 : byte > -23 ? 1u << (byte + 22) : 0u);
+}
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }

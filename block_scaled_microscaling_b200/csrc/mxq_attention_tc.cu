@@ -249,7 +249,9 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                         if (key0 + j < see_hi && key0 + j >= see_lo) vnan |= bits;
                     }
                 }
-                const unsigned long long mk2 = dup2(mul * pow2i(bi.kref - 127)), m2 = dup2(-m);
+                float mk = mul * pow2i(bi.kref - 127);
+                if (bi.kref <= 0) mk = mul * 0x1p-64f * pow2i(bi.kref - 63);  // 2^(kref - 127) is a subnormal
+                const unsigned long long mk2 = dup2(mk), m2 = dup2(-m);
 #pragma unroll
                 for (int j = 0; j < 64; ++j) e.d[j] = f2fma(e.d[j], mk2, m2);
                 // keys that the row does not see
@@ -322,7 +324,7 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                     exact_row<D>(p, s, b, head, r0 + k, first * 128, (first + n) * 128, alone, (long long)blockIdx.x * kTileRows + k);
             } else if (ok) {
                 const long long at = (long long)(s.q0 + i) * p.heads + h, slot0 = (long long)blockIdx.x * kTileRows + 128 * x + quad * 32;
-                const float vtrue = pow2i(vref - 127), f = alone ? (l == 0.f ? 0.f : vtrue / l) : vtrue;
+                const float vtrue = scale_of(vref), f = alone ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
                 const float nan = __uint_as_float(0x7FC00000u);
                 // through the rows' place of Q, which nothing reads any more: whole rows, 16 bytes a lane
                 const uint32_t stage = sb + x * C::Q + quad * (C::Q / 4), mine = stage + lane * (2 * D);
@@ -341,7 +343,7 @@ template <int D> __global__ void __launch_bounds__(kTcThreads, 1) k_kv_attention
                         }
                         const float g = (vnan >> (c >> 5)) & 1u ? nan : f;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * g);
+                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * g * vtrue);
                         if (alone) {
                             uint32_t w[8];
 #pragma unroll

@@ -166,7 +166,8 @@ MXQ_API mxq_status mxq_kv_read(const mxq_kv_cache* cache, const int64_t* slots, 
  * Keys, values and rows of q are brought to half precision (f16), exactly up to a
  * power of two: a block more than 2^16 below the largest that the query sees (of
  * the keys; of the values), and values of q more than 2^17 below the largest of
- * their row, may lose bits or count as zero. Scores and sums are fp32, 2^x has an
+ * their row, may lose bits or count as zero. Scores and sums are fp32 (a row's sum
+ * of weights of up to 2^8 times its values must stay below 2^128), 2^x has an
  * error of 2^-22; the weights w enter the second product in f16 (2^-11). Where a
  * key that only some queries of a chunk see is far larger than the others, the
  * chunk's rows are computed one by one in fp32, many times slower.

@@ -686,3 +686,24 @@ def test_tokens_written_beside_huge_ones():
         ops.kv_append(k, v, c, slots)
         got = check(q, c, table, [n], [0, news])
         assert ((got[:-1] - clean[:-1]).abs() <= 2 * 2.0 ** -8 * clean[:-1].abs() + 1e-6).all()
+
+
+@pytest.mark.parametrize("rows", [1, 2, 8, 60])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("k_exp,v_exp", [(0, -118), (0, -122), (0, 108), (-112, 0), (-120, -120), (100, 0)])
+def test_blocks_at_the_ends_of_the_range(k_exp, v_exp, d, rows):
+    """Scale bytes next to 0 and 254, the queries so large or small that the scores are ordinary. Below bf16's normal range a
+    step is 2^-133; fp32's subnormals, 2^-149 apart, are below that. At the upper end the sums are bounded by fp32: 150 keys, weights
+    of up to 2^8, values of 6 x 2^(108 + 2) at most, stay below 2^128 (with 2^124 they would not)."""
+    lens, page = [150], 16
+    c = filled(5, 10, 2, page, d, 2.0 ** k_exp, 2.0 ** v_exp)
+    table = tables(lens, page, 10)
+    q = (rand(11, rows, 8, d) * 2.0 ** min(-k_exp, 118)).bfloat16()
+    scale = 2.0 ** (max(0, -k_exp - 118) - 3)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    got, lse = ops.kv_attention(q, c, table, dev(lens), q_starts=dev([0, rows]), max_q=rows, scale=scale, lse=True)
+    out, want, tol, _ = reference(q, c, table, lens, [0, rows], scale=scale)
+    err = (got.double() - out).abs()
+    assert (err <= tol + out.abs() * 2.0 ** -8 + 2.0 ** -134).all(), float((err / out.abs()).max())
+    assert ((lse.double() - want).abs() <= 2.0 ** -12 * (1 + want.abs())).all()
+    assert got.float().abs().max() > 2.0 ** (v_exp - 6)
