@@ -171,12 +171,13 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
 // `least` where no key is seen by all: where `edge` exceeds that by more than `room`, the tile's rows are computed anew by
 // exact_row, which shares nothing. That is slow (4 queries of 32 heads
 // over 3000 keys 92 us for 18, 128 over 32768 keys 21 ms for 0.08) and does not happen with keys and values of one kind;
-// the look itself takes up to 1 us a call (prompts of 2000 tokens with a window of 512 180 us for 174).
+// the look itself takes up to 1 us a call (8 sequences of 4 queries over 8000 keys 47.5 us for 47.1, 4 prompts of 2000 tokens
+// with a window of 512, whose CTAs are short, 181 for 175).
 struct Spread {
     int whole, edge, least;
     __device__ __forceinline__ bool beyond(int room) const { return edge > (whole >= 0 ? whole : least) + room; }
 };
-constexpr int kSpreadKeys = 128;
+constexpr int kSpreadKeys = 64;
 // `out` [warps][2]: of K and V, for the queries i0 .. i1 (i1 > i0) over the keys first .. last - 1; `t` of `threads` threads,
 // whole warps, call it
 template <int D> __device__ __forceinline__ void note_spread(const AtArgs& p, const Span& s, int b, int head, int i0, int i1, int first, int last, int t, int threads, Spread (*out)[2]) {
@@ -187,23 +188,44 @@ template <int D> __device__ __forceinline__ void note_spread(const AtArgs& p, co
     const int all_lo = min(max(p.window > 0 ? pos_hi - p.window + 1 : 0, lo), hi), all_hi = max(min(pos_lo + 1, hi), all_lo);
     const int below = all_lo - lo, edges = below + (hi - all_hi), n = edges + min(all_hi - all_lo, kSpreadKeys);
     int whole[2] = {-1, -1}, edge[2] = {-1, -1}, least[2] = {256, 256};
-    for (int e = t; e < n; e += threads) {
-        const int key = e < below ? lo + e : e < edges ? all_hi + (e - below) : all_hi - 1 - (e - edges);
-        const int at = p.by_page(key), pg = __ldg(p.table + b * p.table_stride + at);
-        if (pg < 0 || pg >= p.c.pages) continue;
-        const long long row = ((long long)pg * p.c.heads + head) * p.c.page + (key - at * p.c.page);
+    constexpr int AHEAD = 2;  // keys of a thread whose loads are in flight
+    for (int e0 = t; e0 < n; e0 += AHEAD * threads) {
+        int at[AHEAD], off[AHEAD], pg[AHEAD];
+        uint32_t w[AHEAD][2];
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const uint8_t* const scales = (v ? p.c.vs : p.c.ks) + row * (D / 32);
-            uint32_t w = D == 128 ? *reinterpret_cast<const uint32_t*>(scales) : (uint32_t)*reinterpret_cast<const uint16_t*>(scales);
-            w &= ~__vcmpeq4(w, 0xFFFFFFFFu);  // NaN blocks aside
-            w = __vmaxu4(w, w >> 16);
-            const int most = (int)max(w & 0xFFu, (w >> 8) & 0xFFu);
-            if (e >= edges) {
-                whole[v] = max(whole[v], most);
-            } else {
-                edge[v] = max(edge[v], most);
-                if (most > 0) least[v] = min(least[v], most);
+        for (int u = 0; u < AHEAD; ++u) {
+            const int e = e0 + u * threads;
+            const int key = e < below ? lo + e : e < edges ? all_hi + (e - below) : all_hi - 1 - (e - edges);
+            at[u] = p.by_page(key);
+            off[u] = key - at[u] * p.c.page;
+            pg[u] = -1;
+            if (e < n) pg[u] = __ldg(p.table + b * p.table_stride + at[u]);
+            if (pg[u] >= p.c.pages) pg[u] = -1;
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const long long row = ((long long)max(pg[u], 0) * p.c.heads + head) * p.c.page + off[u];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const uint8_t* const scales = (v ? p.c.vs : p.c.ks) + row * (D / 32);
+                w[u][v] = 0;
+                if (pg[u] >= 0) w[u][v] = D == 128 ? *reinterpret_cast<const uint32_t*>(scales) : (uint32_t)*reinterpret_cast<const uint16_t*>(scales);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            if (pg[u] < 0) continue;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                uint32_t x = w[u][v] & ~__vcmpeq4(w[u][v], 0xFFFFFFFFu);  // NaN blocks aside
+                x = __vmaxu4(x, x >> 16);
+                const int most = (int)max(x & 0xFFu, (x >> 8) & 0xFFu);
+                if (e0 + u * threads >= edges) {
+                    whole[v] = max(whole[v], most);
+                } else {
+                    edge[v] = max(edge[v], most);
+                    if (most > 0) least[v] = min(least[v], most);
+                }
             }
         }
     }
