@@ -455,6 +455,8 @@ def kv_attention(q, cache, block_table, seq_lens, q_starts=None, max_q=None, sca
                  kernel for many queries (right, but slow)
     scale        of the scores (default head_dim ** -0.5); window: keys a query sees at most (0: all)
     max_keys     an upper bound of seq_lens, if known, for a better split of the work (longer sequences are cut)
+    Keys that a query does not see do not enter it, whatever they hold; where a chunk has one that only some of its queries
+    see and that is far larger than the others, its rows are computed one by one (right, but slow).
     Returns out [rows, heads, head_dim]; with lse=True (out, log-sum-exp fp32 [rows, heads]). A query that sees no key
     gives 0 (and -inf), and so do rows of no sequence and queries beyond max_q, which a given `out` keeps. For serving: the
     results carry no gradient."""
